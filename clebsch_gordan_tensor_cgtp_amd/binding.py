@@ -14,7 +14,10 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libcgtp.so")
 
 CGTP_UVU, CGTP_UVW = 0, 1
-CGTP_F32, CGTP_F64 = 0, 1
+CGTP_F32, CGTP_F64, CGTP_BF16, CGTP_F16 = 0, 1, 2, 3
+DTYPES = {"f32": CGTP_F32, "f64": CGTP_F64, "bf16": CGTP_BF16, "f16": CGTP_F16}
+GATES = {None: 0, "row": 1, "channel": 2}
+ACTS = {"identity": 0, "sigmoid": 1, "silu": 2, "tanh": 3}
 STATUS = {0: "CGTP_OK", 1: "CGTP_ERR_INVALID_ARG", 2: "CGTP_ERR_IRREPS", 3: "CGTP_ERR_UNSUPPORTED",
           4: "CGTP_ERR_COMPILE", 5: "CGTP_ERR_HIP", 6: "CGTP_ERR_INTERNAL"}
 STATUS_CODES = {v: k for k, v in STATUS.items()}
@@ -29,9 +32,14 @@ EXPORTS = ("cgtp_plan_create", "cgtp_plan_destroy", "cgtp_plan_info_get", "cgtp_
            "cgtp_plan_conv_uvw_backward_source", "cgtp_conv_backward_radial", "cgtp_conv_backward_radial_workspace_size",
            "cgtp_conv_row_split", "cgtp_tp_backward_noalloc", "cgtp_conv_backward_receiver",
            "cgtp_conv_backward_receiver_workspace_size", "cgtp_conv_double_backward_workspace_size",
-           "cgtp_conv_double_backward_ws")
+           "cgtp_conv_double_backward_ws",
+           "cgtp_block_create", "cgtp_block_destroy", "cgtp_block_info_get", "cgtp_block_source",
+           "cgtp_block_workspace_size", "cgtp_norm_forward", "cgtp_norm_backward", "cgtp_join_forward",
+           "cgtp_join_backward", "cgtp_adamw_create", "cgtp_adamw_destroy", "cgtp_adamw_info_get", "cgtp_adamw_offset",
+           "cgtp_grad_norm", "cgtp_adamw_step", "cgtp_adamw_schedule", "cgtp_adamw_state_read",
+           "cgtp_adamw_state_write")
 _STRING_RESULTS = ("cgtp_last_error", "cgtp_plan_source", "cgtp_plan_radial_source", "cgtp_plan_uvw_backward_source",
-                   "cgtp_plan_conv_uvw_backward_source")
+                   "cgtp_plan_conv_uvw_backward_source", "cgtp_block_source")
 
 
 class CgtpError(RuntimeError):
@@ -51,6 +59,28 @@ class PathInfo(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int32) for n in ("i1", "i2", "slot", "l1", "l2", "l3", "p3", "x_off", "y_off",
                                               "out_off", "mul_in", "mul_out")] + \
                [("w_off", ctypes.c_int64), ("nnz", ctypes.c_int32)]
+
+
+class BlockConfig(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("dtype", "gate", "act", "post_norm", "next_norm")] + \
+               [("eps", ctypes.c_double), ("alpha", ctypes.c_double)]
+
+
+class BlockInfo(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("d", "channels", "gate_width", "dtype", "lanes", "chunks")]
+
+
+class AdamWConfig(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("dtype", "state_bits", "master")]
+
+
+class AdamWInfo(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int64) for n in ("elements", "blocks", "norm_workspace")] + [("n_tensors", ctypes.c_int32)]
+
+
+class AdamWHyper(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_double) for n in ("lr", "beta1", "beta2", "eps", "weight_decay", "max_norm",
+                                               "grad_scale")] + [("step", ctypes.c_int64)]
 
 
 _lib = None
@@ -103,6 +133,27 @@ def lib():
         L.cgtp_graph_transpose.argtypes = [i64, i64, vp, vp, vp, vp, vp, vp]
         L.cgtp_conv_backward.argtypes = [vp, i64, i64] + [vp] * 13
         L.cgtp_spherical_harmonics.argtypes = [i32, ctypes.c_int, i64, vp, vp, vp]
+        sz, dbl, szp = ctypes.c_size_t, ctypes.c_double, ctypes.POINTER(ctypes.c_size_t)
+        L.cgtp_block_source.restype = ctypes.c_char_p
+        L.cgtp_block_source.argtypes = [vp]
+        L.cgtp_block_create.argtypes = [ctypes.c_char_p, ctypes.POINTER(BlockConfig), ctypes.POINTER(vp)]
+        L.cgtp_block_destroy.argtypes = [vp]
+        L.cgtp_block_info_get.argtypes = [vp, ctypes.POINTER(BlockInfo)]
+        L.cgtp_block_workspace_size.argtypes = [vp, i64, szp]
+        L.cgtp_norm_forward.argtypes = [vp, i64, vp, i64, vp, vp, vp, vp]
+        L.cgtp_norm_backward.argtypes = [vp, i64, vp, i64] + [vp] * 7 + [sz, vp]
+        L.cgtp_join_forward.argtypes = [vp, i64, vp, vp, i64, vp, i64] + [vp] * 8
+        L.cgtp_join_backward.argtypes = [vp, i64, vp, vp, vp, vp, i64, vp, i64] + [vp] * 7 + [i64, vp, i64] + \
+            [vp] * 4 + [sz, vp]
+        L.cgtp_adamw_create.argtypes = [i32, vp, ctypes.POINTER(AdamWConfig), ctypes.POINTER(vp)]
+        L.cgtp_adamw_destroy.argtypes = [vp]
+        L.cgtp_adamw_info_get.argtypes = [vp, ctypes.POINTER(AdamWInfo)]
+        L.cgtp_adamw_offset.argtypes = [vp, i32, ctypes.POINTER(i64)]
+        L.cgtp_grad_norm.argtypes = [vp, vp, vp, vp, sz, vp]
+        L.cgtp_adamw_step.argtypes = [vp] * 7 + [ctypes.POINTER(AdamWHyper), vp, vp, vp]
+        L.cgtp_adamw_schedule.argtypes = [vp, dbl, dbl, vp]
+        L.cgtp_adamw_state_read.argtypes = [vp] * 7
+        L.cgtp_adamw_state_write.argtypes = [vp] * 7
         for name in EXPORTS:
             if name not in _STRING_RESULTS:
                 getattr(L, name).restype = ctypes.c_int
@@ -586,3 +637,364 @@ def spherical_harmonics(lmax: int, vec, out=None, stream=None):
                                           _dev(vec, "vec", dt, (E, 3)), _dev(out, "y", dt, (E, (lmax + 1) ** 2)),
                                           _stream(stream, vec.device)))
     return out
+
+
+# ------------------------------------------------------------------------------------ blocks
+
+def _torch_dtype(dtype: str):
+    import torch
+    return {"f32": torch.float32, "f64": torch.float64, "bf16": torch.bfloat16, "f16": torch.float16}[dtype]
+
+
+class Block:
+    """The row norm at a block's entry and the join at its end (norm, gate, residual sum, the next
+    block's norm) for one irreps row and configuration; compiled when it is created."""
+
+    def __init__(self, irreps, dtype="f32", gate=None, act="sigmoid", post_norm=False, next_norm=False, eps=1e-6,
+                 alpha=1.0):
+        self._h = None
+        self.irreps, self.dtype = irreps, dtype
+        self.gate, self.act, self.post_norm, self.next_norm = gate, act, bool(post_norm), bool(next_norm)
+        self.eps, self.alpha = float(eps), float(alpha)
+        cfg = BlockConfig(DTYPES[dtype], GATES[gate], ACTS[act], int(self.post_norm), int(self.next_norm), self.eps,
+                          self.alpha)
+        h = ctypes.c_void_p()
+        _check(lib().cgtp_block_create(irreps.encode(), ctypes.byref(cfg), ctypes.byref(h)))
+        self._h = h
+        info = BlockInfo()
+        _check(lib().cgtp_block_info_get(h, ctypes.byref(info)))
+        self.d, self.channels, self.gate_width = info.d, info.channels, info.gate_width
+        self.lanes, self.chunks = info.lanes, info.chunks
+        self.torch_dtype = _torch_dtype(dtype)                              # of rows
+        self.real_dtype = _torch_dtype("f64" if dtype == "f64" else "f32")  # of statistics and weights
+
+    @property
+    def handle(self):
+        return self._h
+
+    @property
+    def source(self) -> str:
+        return lib().cgtp_block_source(self._h).decode()
+
+    def close(self):
+        if self._h is not None and _lib is not None:
+            lib().cgtp_block_destroy(self._h)
+        self._h = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+@lru_cache(maxsize=None)
+def block_for(irreps, dtype="f32", gate=None, act="sigmoid", post_norm=False, next_norm=False, eps=1e-6,
+              alpha=1.0) -> Block:
+    """The block of a configuration (cached per process)."""
+    return Block(irreps, dtype, gate, act, post_norm, next_norm, eps, alpha)
+
+
+def _rows(t, name, dtype, n, width):
+    """(pointer, row pitch) of n rows of `width` consecutive elements, any pitch of at least that."""
+    import torch
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA (HIP) torch tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if tuple(t.shape) != (n, width):
+        raise ValueError(f"{name} must have shape {(n, width)}, got {tuple(t.shape)}")
+    if width > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name}: the elements of a row must be consecutive")
+    ld = t.stride(0) if n > 1 else width
+    if ld < width:
+        raise ValueError(f"{name}: rows overlap (row pitch {ld} of {width} elements)")
+    return ctypes.c_void_p(t.data_ptr()), ld
+
+
+def _rows_or_null(t, name, dtype, n, width):
+    return (ctypes.c_void_p(0), width) if t is None else _rows(t, name, dtype, n, width)
+
+
+def _same_device(x, **tensors):
+    for name, t in tensors.items():
+        if t is not None and t.device != x.device:
+            raise ValueError(f"{name} is on {t.device}, expected {x.device}")
+
+
+def block_workspace_size(block: Block, n: int) -> int:
+    v = ctypes.c_size_t()
+    _check(lib().cgtp_block_workspace_size(block.handle, n, ctypes.byref(v)))
+    return v.value
+
+
+def _workspace(block, n, workspace, device, wanted):
+    import torch
+    if not wanted:
+        return ctypes.c_void_p(0), 0, None
+    if workspace is None:
+        workspace = torch.empty(block_workspace_size(block, n), dtype=torch.uint8, device=device)
+    return _dev(workspace, "workspace"), workspace.numel() * workspace.element_size(), workspace
+
+
+def norm_forward(block: Block, x, w, u=None, rstd=None, need_rstd=True, stream=None):
+    """(u, rstd): u = x * rstd(x) * w per channel.  x may have a row pitch; w None stands for ones."""
+    import torch
+    n, dt, rt = x.shape[0], block.torch_dtype, block.real_dtype
+    u = torch.empty((n, block.d), dtype=dt, device=x.device) if u is None else u
+    if rstd is None and need_rstd:
+        rstd = torch.empty(n, dtype=rt, device=x.device)
+    _same_device(x, w=w, u=u, rstd=rstd)
+    xp, x_ld = _rows(x, "x", dt, n, block.d)
+    _check(lib().cgtp_norm_forward(block.handle, n, xp, x_ld, _ptr_or_null(w, "w", rt, (block.channels,)),
+                                   _dev(u, "u", dt, (n, block.d)), _ptr_or_null(rstd, "rstd", rt, (n,)),
+                                   _stream(stream, x.device)))
+    return u, rstd
+
+
+def norm_backward(block: Block, x, w, rstd, grad_u, grad_add=None, grad_x=None, grad_w=None, need=(True, True),
+                  workspace=None, stream=None):
+    """(grad_x, grad_w); entries not in ``need`` are None and not computed.  grad_add, when given,
+    is added to grad_x (the gradient that reaches x past the norm)."""
+    import torch
+    n, dt, rt, dev = x.shape[0], block.torch_dtype, block.real_dtype, x.device
+    shapes = ((n, block.d), (block.channels,))
+    gx, gw = [None if not nd else (torch.empty(sh, dtype=t, device=dev) if o is None else o)
+              for o, nd, sh, t in zip((grad_x, grad_w), need, shapes, (dt, rt))]
+    _same_device(x, w=w, rstd=rstd, grad_u=grad_u, grad_add=grad_add, grad_x=gx, grad_w=gw, workspace=workspace)
+    xp, x_ld = _rows(x, "x", dt, n, block.d)
+    ws, ws_bytes, workspace = _workspace(block, n, workspace, dev, gw is not None)
+    _check(lib().cgtp_norm_backward(block.handle, n, xp, x_ld, _ptr_or_null(w, "w", rt, (block.channels,)),
+                                    _dev(rstd, "rstd", rt, (n,)), _dev(grad_u, "grad_u", dt, (n, block.d)),
+                                    _ptr_or_null(grad_add, "grad_add", dt, (n, block.d)),
+                                    _ptr_or_null(gx, "grad_x", dt, shapes[0]),
+                                    _ptr_or_null(gw, "grad_w", rt, shapes[1]), ws, ws_bytes, _stream(stream, dev)))
+    return gx, gw
+
+
+def join_forward(block: Block, res, f, gate, w_post, scale, w_next, h=None, u=None, rstd_f=None, rstd_h=None,
+                 need_rstd=True, stream=None):
+    """(h, u, rstd_f, rstd_h): h = alpha*res + scale*act(gate)*w_post*f*rstd(f), u = h*rstd(h)*w_next.
+    f and gate may have a row pitch (both in one buffer, say); weights given as None are ones; what
+    the block's configuration leaves out is None."""
+    import torch
+    n, d, dt, rt, dev = f.shape[0], block.d, block.torch_dtype, block.real_dtype, f.device
+    new = lambda t, want, shape, ty: torch.empty(shape, dtype=ty, device=dev) if t is None and want else t  # noqa: E731
+    h, u = new(h, True, (n, d), dt), new(u, block.next_norm, (n, d), dt)
+    rstd_f = new(rstd_f, need_rstd and block.post_norm, n, rt)
+    rstd_h = new(rstd_h, need_rstd and block.next_norm, n, rt)
+    _same_device(f, res=res, gate=gate, w_post=w_post, scale=scale, w_next=w_next, h=h, u=u, rstd_f=rstd_f,
+                 rstd_h=rstd_h)
+    fp, f_ld = _rows(f, "f", dt, n, d)
+    gp, g_ld = _rows_or_null(gate, "gate", dt, n, block.gate_width)
+    cs = (block.channels,)
+    _check(lib().cgtp_join_forward(
+        block.handle, n, _dev(res, "res", dt, (n, d)), fp, f_ld, gp, g_ld, _ptr_or_null(w_post, "w_post", rt, cs),
+        _ptr_or_null(scale, "scale", rt, cs), _ptr_or_null(w_next, "w_next", rt, cs), _dev(h, "h", dt, (n, d)),
+        _ptr_or_null(u, "u", dt, (n, d)), _ptr_or_null(rstd_f, "rstd_f", rt, (n,)),
+        _ptr_or_null(rstd_h, "rstd_h", rt, (n,)), _stream(stream, dev)))
+    return h, u, rstd_f, rstd_h
+
+
+def join_backward(block: Block, grad_h, grad_u, h, f, gate, w_post, scale, w_next, rstd_f, rstd_h,
+                  outs=(None,) * 6, need=(True,) * 6, workspace=None, stream=None):
+    """(grad_res, grad_f, grad_gate, grad_w_post, grad_scale, grad_w_next) from the gradients of h
+    (None: zero) and u and the forward's h and statistics; entries not in ``need``, or that the
+    block's configuration leaves out, are None and not computed.  grad_f and grad_gate given in
+    ``outs`` may have a row pitch."""
+    import torch
+    n, d, dt, rt, dev = f.shape[0], block.d, block.torch_dtype, block.real_dtype, f.device
+    cs, gw = (block.channels,), block.gate_width
+    shapes = ((n, d), (n, d), (n, gw), cs, cs, cs)
+    has = (True, True, gw > 0, block.post_norm, True, block.next_norm)
+    types = (dt, dt, dt, rt, rt, rt)
+    res = [None if not (nd and hs) else (torch.empty(sh, dtype=ty, device=dev) if o is None else o)
+           for o, nd, hs, sh, ty in zip(outs, need, has, shapes, types)]
+    names = ("grad_res", "grad_f", "grad_gate", "grad_w_post", "grad_scale", "grad_w_next")
+    _same_device(f, grad_h=grad_h, grad_u=grad_u, h=h, gate=gate, w_post=w_post, scale=scale, w_next=w_next,
+                 rstd_f=rstd_f, rstd_h=rstd_h, workspace=workspace, **dict(zip(names, res)))
+    fp, f_ld = _rows(f, "f", dt, n, d)
+    gp, g_ld = _rows_or_null(gate, "gate", dt, n, gw)
+    dfp, df_ld = _rows_or_null(res[1], "grad_f", dt, n, d)
+    dgp, dg_ld = _rows_or_null(res[2], "grad_gate", dt, n, gw)
+    ws, ws_bytes, workspace = _workspace(block, n, workspace, dev, any(r is not None for r in res[3:]))
+    _check(lib().cgtp_join_backward(
+        block.handle, n, _ptr_or_null(grad_h, "grad_h", dt, (n, d)), _ptr_or_null(grad_u, "grad_u", dt, (n, d)),
+        _ptr_or_null(h, "h", dt, (n, d)), fp, f_ld, gp, g_ld, _ptr_or_null(w_post, "w_post", rt, cs),
+        _ptr_or_null(scale, "scale", rt, cs), _ptr_or_null(w_next, "w_next", rt, cs),
+        _ptr_or_null(rstd_f, "rstd_f", rt, (n,)), _ptr_or_null(rstd_h, "rstd_h", rt, (n,)),
+        _ptr_or_null(res[0], "grad_res", dt, (n, d)), dfp, df_ld, dgp, dg_ld,
+        *[_ptr_or_null(r, nm, rt, cs) for r, nm in zip(res[3:], names[3:])], ws, ws_bytes, _stream(stream, dev)))
+    return tuple(res)
+
+
+# ------------------------------------------------------------------------------------ optimizer
+
+class AdamW:
+    """The layout of an AdamW step over tensors of these sizes (host only).  Moments are flat tensors
+    of ``elements`` values, tensor t's at ``offsets[t]``; ``state`` makes them."""
+
+    def __init__(self, sizes, dtype="f32", state_bits=32, master=False):
+        self._h = None
+        self.sizes, self.dtype, self.state_bits, self.master = tuple(int(n) for n in sizes), dtype, state_bits, master
+        arr = (ctypes.c_int64 * max(1, len(self.sizes)))(*self.sizes)
+        cfg = AdamWConfig(DTYPES[dtype], state_bits, int(bool(master)))
+        h = ctypes.c_void_p()
+        _check(lib().cgtp_adamw_create(len(self.sizes), arr, ctypes.byref(cfg), ctypes.byref(h)))
+        self._h = h
+        info = AdamWInfo()
+        _check(lib().cgtp_adamw_info_get(h, ctypes.byref(info)))
+        self.elements, self.blocks, self.norm_workspace = info.elements, info.blocks, info.norm_workspace
+        off, at = [], ctypes.c_int64()
+        for t in range(len(self.sizes)):
+            _check(lib().cgtp_adamw_offset(h, t, ctypes.byref(at)))
+            off.append(at.value)
+        self.offsets = tuple(off)
+        self.torch_dtype = _torch_dtype(dtype)
+        self.real_dtype = _torch_dtype("f64" if dtype == "f64" else "f32")
+
+    @property
+    def handle(self):
+        return self._h
+
+    @property
+    def moment_dtypes(self):
+        import torch
+        return (torch.int8, torch.uint8) if self.state_bits == 8 else (self.real_dtype, self.real_dtype)
+
+    def state(self, device, params=None):
+        """(m, v, scales, master) at the start: zero moments, and master copies of ``params``."""
+        import torch
+        mt, vt = self.moment_dtypes
+        m = torch.zeros(self.elements, dtype=mt, device=device)
+        v = torch.zeros(self.elements, dtype=vt, device=device)
+        scales = torch.zeros((2, self.blocks), device=device) if self.state_bits == 8 else None
+        master = None
+        if self.master:
+            master = torch.zeros(self.elements, device=device)
+            for p, at in zip(params, self.offsets):
+                master[at:at + p.numel()].copy_(p.detach().reshape(-1))
+        return m, v, scales, master
+
+    def close(self):
+        if self._h is not None and _lib is not None:
+            lib().cgtp_adamw_destroy(self._h)
+        self._h = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+class TensorList:
+    """Tensors of an AdamW layout (parameters or gradients, None where a gradient is absent), checked,
+    with their addresses as the library takes them.  The tensors are held; the addresses are read
+    again at every use, and tensors that moved are checked again."""
+
+    def __init__(self, opt: AdamW, tensors):
+        self.opt, self.tensors = opt, tuple(tensors)
+        if len(self.tensors) != len(opt.sizes):
+            raise ValueError(f"{len(self.tensors)} tensors, the layout has {len(opt.sizes)}")
+        self._at = None
+        self.device = next((t.device for t in self.tensors if t is not None), None)
+        self.pointers()
+
+    def pointers(self):
+        at = [0 if t is None else t.data_ptr() for t in self.tensors]
+        if at != self._at:
+            for i, (t, n) in enumerate(zip(self.tensors, self.opt.sizes)):
+                if t is None:
+                    continue
+                _dev(t, f"tensor {i}", self.opt.torch_dtype)
+                if t.numel() != n:
+                    raise ValueError(f"tensor {i} has {t.numel()} elements, the layout {n}")
+                if t.device != self.device:
+                    raise ValueError(f"tensor {i} is on {t.device}, expected {self.device}")
+            self._array, self._at = (ctypes.c_void_p * max(1, len(at)))(*at), at
+        return self._array
+
+
+def tensor_list(opt: AdamW, tensors) -> TensorList:
+    return TensorList(opt, tensors)
+
+
+def _list(opt, tensors):
+    if not isinstance(tensors, TensorList):
+        return TensorList(opt, tensors)
+    if tensors.opt is not opt:
+        raise ValueError("the tensors were listed for another layout")
+    return tensors
+
+
+def grad_norm(opt: AdamW, grads, norm=None, workspace=None, stream=None):
+    """The global norm of the gradients (a TensorList or tensors; None ones are left out): a device
+    float64 tensor of one element."""
+    import torch
+    grads = _list(opt, grads)
+    dev = grads.device
+    norm = torch.empty(1, dtype=torch.float64, device=dev) if norm is None else norm
+    if workspace is None:
+        workspace = torch.empty(opt.norm_workspace, dtype=torch.uint8, device=dev)
+    _check(lib().cgtp_grad_norm(opt.handle, grads.pointers(), _dev(norm, "norm", torch.float64, (1,)),
+                                _dev(workspace, "workspace"), workspace.numel() * workspace.element_size(),
+                                _stream(stream, dev)))
+    return norm
+
+
+def adamw_step(opt: AdamW, params, grads, m, v, scales=None, master=None, *, lr=1e-3, beta1=0.9, beta2=0.999, eps=1e-8,
+               weight_decay=0.01, step=0, max_norm=0.0, grad_scale=1.0, norm=None, schedule=None, stream=None):
+    """One AdamW step in place: params, m, v (and scales, master).  ``step`` counts from 1; with
+    ``norm`` (as of grad_norm) a step whose norm is not finite changes nothing, and max_norm > 0
+    clips by it.  ``schedule``: a device float64 tensor {step, lr, 1 - beta1^step, 1 - beta2^step}
+    in the place of ``step`` and ``lr`` (adamw_schedule advances it)."""
+    import torch
+    params, grads = _list(opt, params), _list(opt, grads)
+    if any(t is None for t in params.tensors):
+        raise ValueError("a parameter is None")
+    dev, el, (mt, vt) = params.device, opt.elements, opt.moment_dtypes
+    for name, t in (("gradients", grads), ("m", m), ("v", v), ("scales", scales), ("master", master), ("norm", norm),
+                    ("schedule", schedule)):
+        if t is not None and t.device is not None and t.device != dev:
+            raise ValueError(f"{name} on {t.device}, expected {dev}")
+    hyper = AdamWHyper(lr, beta1, beta2, eps, weight_decay, max_norm, grad_scale, step)
+    _check(lib().cgtp_adamw_step(
+        opt.handle, params.pointers(), grads.pointers(), _dev(m, "m", mt, (el,)), _dev(v, "v", vt, (el,)),
+        _ptr_or_null(scales, "scales", torch.float32, (2, opt.blocks)),
+        _ptr_or_null(master, "master", torch.float32, (el,)), ctypes.byref(hyper),
+        _ptr_or_null(norm, "norm", torch.float64, (1,)), _ptr_or_null(schedule, "schedule", torch.float64, (4,)),
+        _stream(stream, dev)))
+
+
+def adamw_schedule(schedule, beta1=0.9, beta2=0.999, stream=None):
+    """Advance a device schedule {step, lr, 1 - beta1^step, 1 - beta2^step} by one step."""
+    import torch
+    _check(lib().cgtp_adamw_schedule(_dev(schedule, "schedule", torch.float64, (4,)), beta1, beta2,
+                                     _stream(stream, schedule.device)))
+    return schedule
+
+
+def adamw_state_read(opt: AdamW, m, v, scales, m_out=None, v_out=None, stream=None):
+    """The values that 8-bit moments stand for: (m, v) in float32."""
+    import torch
+    el, (mt, vt) = opt.elements, opt.moment_dtypes
+    m_out = torch.empty(el, dtype=torch.float32, device=m.device) if m_out is None else m_out
+    v_out = torch.empty(el, dtype=torch.float32, device=m.device) if v_out is None else v_out
+    _check(lib().cgtp_adamw_state_read(opt.handle, _dev(m, "m", mt, (el,)), _dev(v, "v", vt, (el,)),
+                                       _ptr_or_null(scales, "scales", torch.float32, (2, opt.blocks)),
+                                       _dev(m_out, "m_out", torch.float32, (el,)),
+                                       _dev(v_out, "v_out", torch.float32, (el,)), _stream(stream, m.device)))
+    return m_out, v_out
+
+
+def adamw_state_write(opt: AdamW, m_in, v_in, m, v, scales, stream=None):
+    """8-bit moments from float32 values (both in the flat layout)."""
+    import torch
+    el, (mt, vt) = opt.elements, opt.moment_dtypes
+    _check(lib().cgtp_adamw_state_write(opt.handle, _dev(m_in, "m_in", torch.float32, (el,)),
+                                        _dev(v_in, "v_in", torch.float32, (el,)), _dev(m, "m", mt, (el,)),
+                                        _dev(v, "v", vt, (el,)),
+                                        _ptr_or_null(scales, "scales", torch.float32, (2, opt.blocks)),
+                                        _stream(stream, m.device)))
+    return m, v, scales

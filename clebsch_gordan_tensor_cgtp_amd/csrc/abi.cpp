@@ -11,6 +11,7 @@
 #include <memory>
 #include <string>
 
+#include "abi_util.h"
 #include "plan.h"
 #include "static_kernels.h"
 
@@ -20,54 +21,11 @@ struct cgtp_plan {
 
 namespace {
 
-thread_local std::string g_last_error;
-
-cgtp_status fail(cgtp_status code, const std::string &msg)
-{
-    g_last_error = msg;
-    return code;
-}
-
-template <class F> cgtp_status guarded(F &&f)
-{
-    try {
-        f();
-        return CGTP_OK;
-    } catch (const cgtp::Error &e) {
-        return fail(e.code, e.what());
-    } catch (const std::bad_alloc &) {
-        return fail(CGTP_ERR_INTERNAL, "host out of memory");
-    } catch (const std::exception &e) {
-        return fail(CGTP_ERR_INTERNAL, e.what());
-    } catch (...) {
-        return fail(CGTP_ERR_INTERNAL, "unknown failure");
-    }
-}
-
-void require(bool ok, const std::string &msg)
-{
-    if (!ok) throw cgtp::Error(CGTP_ERR_INVALID_ARG, msg);
-}
-
-void require_ptr(const void *p, const char *name, size_t align)
-{
-    require(p != nullptr, std::string(name) + " is NULL");
-    require(reinterpret_cast<uintptr_t>(p) % align == 0,
-            std::string(name) + " is not aligned to " + std::to_string(align) + " bytes");
-}
-
-// [a, a+na) and [b, b+nb) in bytes must not overlap
-void require_disjoint(const void *a, size_t na, const char *an, const void *b, size_t nb, const char *bn)
-{
-    if (!a || !b || !na || !nb) return;
-    auto x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-    require(x + na <= y || y + nb <= x, std::string(an) + " overlaps " + bn);
-}
-
-void check_hip(hipError_t e, const char *what)
-{
-    if (e != hipSuccess) throw cgtp::Error(CGTP_ERR_HIP, std::string(what) + ": " + hipGetErrorString(e));
-}
+using cgtp::check_hip;
+using cgtp::guarded;
+using cgtp::require;
+using cgtp::require_disjoint;
+using cgtp::require_ptr;
 
 void launch(hipFunction_t f, int64_t waves, void **args, void *stream, unsigned lds_bytes = 0)
 {
@@ -262,7 +220,7 @@ void uvw_radial_backward(cgtp::Plan &P, int64_t N, int64_t E, const int32_t *row
 
 extern "C" {
 
-const char *cgtp_last_error(void) { return g_last_error.c_str(); }
+const char *cgtp_last_error(void) { return cgtp::last_error_message().c_str(); }
 
 cgtp_status cgtp_plan_create(const char *in_irreps, const char *sh_irreps, const char *out_irreps, cgtp_mode mode,
                              cgtp_dtype dtype, cgtp_plan **plan_out)
@@ -495,7 +453,7 @@ cgtp_status cgtp_tp_backward(const cgtp_plan *plan, int64_t B, const void *x, co
             check_hip(cgtp::launch_iota(B + 1, ids, static_cast<hipStream_t>(stream)), "iota launch");
             const cgtp_status st = cgtp_conv_backward_ws(plan, B, B, ids, ids, nullptr, ids, ids, ids, x, y, w,
                                                          grad_out, grad_x, grad_y, grad_w, workspace, part, stream);
-            if (st != CGTP_OK) throw cgtp::Error(st, g_last_error);
+            if (st != CGTP_OK) throw cgtp::Error(st, cgtp::last_error_message());
             return;
         }
         const size_t es = elem(P);
@@ -567,7 +525,7 @@ cgtp_status cgtp_tp_backward_noalloc(const cgtp_plan *plan, int64_t B, const voi
         require(plan != nullptr, "plan is NULL");
         size_t need = 0;
         cgtp_status st = cgtp_tp_backward_workspace_size(plan, B, &need);
-        if (st != CGTP_OK) throw cgtp::Error(st, g_last_error);
+        if (st != CGTP_OK) throw cgtp::Error(st, cgtp::last_error_message());
         if (need > cgtp::kScratchBytes)
             throw cgtp::Error(CGTP_ERR_UNSUPPORTED,
                               "cgtp_tp_backward_noalloc: this batch needs " + std::to_string(need) +
@@ -578,7 +536,7 @@ cgtp_status cgtp_tp_backward_noalloc(const cgtp_plan *plan, int64_t B, const voi
         if (need > 0) check_hip(cgtp::scratch_for_current_device(&ws), "hipGetSymbolAddress(scratch)");
         st = cgtp_tp_backward(plan, B, x, y, w, shared_weights, grad_out, grad_x, grad_y, grad_w, ws,
                               need > 0 ? cgtp::kScratchBytes : 0, stream);
-        if (st != CGTP_OK) throw cgtp::Error(st, g_last_error);
+        if (st != CGTP_OK) throw cgtp::Error(st, cgtp::last_error_message());
     });
 }
 
@@ -1053,7 +1011,7 @@ cgtp_status cgtp_conv_backward_ws(const cgtp_plan *plan, int64_t N, int64_t E, c
         if (P.mode == CGTP_UVU) {
             const cgtp_status st = cgtp_conv_backward(plan, N, E, row_ptr, col, t_row_ptr, t_edge, t_dst, x, y, w,
                                                       grad_out, grad_x, grad_y, grad_w, stream);
-            if (st != CGTP_OK) throw cgtp::Error(st, g_last_error);
+            if (st != CGTP_OK) throw cgtp::Error(st, cgtp::last_error_message());
             return;
         }
         if (!P.uvc_ok) throw cgtp::Error(CGTP_ERR_UNSUPPORTED, P.uvc_why);
@@ -1257,7 +1215,7 @@ cgtp_status cgtp_conv_double_backward_ws(const cgtp_plan *plan, int64_t N, int64
             const cgtp_status st = cgtp_conv_double_backward(plan, N, E, row_ptr, col, order, t_row_ptr, t_edge, t_dst, x,
                                                              y, w, grad_out, gg_x, gg_y, gg_w, grad_x, grad_y, grad_w,
                                                              grad_grad_out, stream);
-            if (st != CGTP_OK) throw cgtp::Error(st, g_last_error);
+            if (st != CGTP_OK) throw cgtp::Error(st, cgtp::last_error_message());
             return;
         }
         if (!P.uvc_ok) throw cgtp::Error(CGTP_ERR_UNSUPPORTED, P.uvc_why);

@@ -1,0 +1,535 @@
+// Block plans: row layout, launch geometry, the generated source's constants, and the entry points
+// cgtp_block_*, cgtp_norm_* and cgtp_join_* (documented in include/cgtp.h).
+#include "block.h"
+
+#include <algorithm>
+#include <climits>
+#include <cmath>
+#include <cstdlib>
+#include <memory>
+
+#include "abi_util.h"
+#include "block_kernels.h"
+
+struct cgtp_block {
+    cgtp::Block b;
+};
+
+namespace cgtp {
+
+namespace {
+
+constexpr int kLds = 160 * 1024;  // bytes of a workgroup
+
+int tuned(const char *name, int otherwise)
+{
+    const char *e = std::getenv(name);
+    return e && *e ? std::atoi(e) : otherwise;
+}
+
+const char *type_name(int dtype)
+{
+    switch (dtype) {
+    case CGTP_F64: return "double";
+    case CGTP_BF16: return "__bf16";
+    case CGTP_F16: return "_Float16";
+    default: return "float";
+    }
+}
+
+// Lanes per row: the power of two that leaves the fewest of a row's 16-byte chunk slots empty with
+// at most `most` chunks to a lane (more lanes where two are within a twentieth); rows that a
+// wave cannot hold so are shared by the waves of one workgroup.
+void pick_lanes(Block &b)
+{
+    const int k = (b.d + b.vec - 1) / b.vec;
+    const int most = std::max(1, std::min(8, tuned("CGTP_BLOCK_CHUNKS", 4)));
+    b.lanes = 0;
+    double best = 0;
+    for (int g = 64; g >= 1; g /= 2) {
+        const int nv = (k + g - 1) / g;
+        if (nv > most) break;
+        const double used = (double)k / ((double)g * nv);
+        if (b.lanes == 0 || used > best + 0.05) {
+            b.lanes = g;
+            best = used;
+        }
+    }
+    if (b.lanes == 0) {
+        for (int g = 128; g <= 1024 && b.lanes == 0; g *= 2)
+            if ((k + g - 1) / g <= most) b.lanes = g;
+        if (b.lanes == 0) b.lanes = 1024;
+    }
+    b.chunks = (k + b.lanes - 1) / b.lanes;
+    b.block = b.lanes > 64 ? b.lanes : 256;
+    if (b.chunks > 8)
+        throw Error(CGTP_ERR_UNSUPPORTED, "block: a row of " + std::to_string(b.d) + " columns exceeds " +
+                                              std::to_string(1024 * 8 * b.vec) + " for this dtype");
+}
+
+void check_lds(const Block &b)
+{
+    const long dp = (long)((b.d + b.vec - 1) / b.vec) * b.vec, cp = (long)((b.c + b.vec - 1) / b.vec) * b.vec;
+    const bool scalar = b.d == b.c;
+    const long rows = b.rows_per_group();
+    long bytes = 2 * std::max(1, b.lanes / 64) * b.real;
+    if (!scalar || rows > 1) bytes += rows * dp * b.real;
+    if (!scalar && b.cfg.gate == CGTP_GATE_CHANNEL) bytes += rows * cp * b.real;
+    if (bytes > kLds)
+        throw Error(CGTP_ERR_UNSUPPORTED, "block: the sums over a row's channels need " + std::to_string(bytes) +
+                                              " bytes of LDS, a workgroup has 163840");
+}
+
+std::string constants(const Block &b)
+{
+    std::string s = "// row norm and block join: " + std::to_string(b.d) + " columns, " + std::to_string(b.c) +
+                    " channels\n";
+    auto line = [&](const std::string &t) { s += t + "\n"; };
+    line(std::string("typedef ") + type_name(b.cfg.dtype) + " T;");
+    line(std::string("typedef ") + (b.cfg.dtype == CGTP_F64 ? "double" : "float") + " R;");
+    auto num = [&](const char *n, long v) { line(std::string("constexpr int ") + n + " = " + std::to_string(v) + ";"); };
+    num("D", b.d);
+    num("C", b.c);
+    num("VEC", b.vec);
+    num("G", b.lanes);
+    num("NV", b.chunks);
+    num("BLOCK", b.block);
+    num("GATE", b.cfg.gate);
+    num("ACT", b.cfg.act);
+    num("POST", b.cfg.post_norm ? 1 : 0);
+    num("NEXT", b.cfg.next_norm ? 1 : 0);
+    num("NSEG", (long)b.segs.size());
+    auto list = [&](const char *n, int Block::Segment::*f) {
+        std::string t = std::string("constexpr int ") + n + "[NSEG] = {";
+        for (size_t i = 0; i < b.segs.size(); ++i) t += (i ? ", " : "") + std::to_string(b.segs[i].*f);
+        line(t + "};");
+    };
+    list("SEG_COL", &Block::Segment::col);
+    list("SEG_CH", &Block::Segment::ch);
+    list("SEG_K", &Block::Segment::k);
+    return s;
+}
+
+}  // namespace
+
+void build_block(Block &b, const std::string &irreps)
+{
+    int64_t col = 0, ch = 0;
+    for (const Irrep &ir : parse_irreps(irreps, "block")) {
+        const int k = 2 * ir.l + 1;
+        if (b.segs.empty() || b.segs.back().k != k) b.segs.push_back({(int)col, (int)ch, k});
+        col += (int64_t)ir.mul * k;
+        ch += ir.mul;
+        if (col > (1 << 20)) throw Error(CGTP_ERR_UNSUPPORTED, "block: a row of more than 1048576 columns");
+    }
+    if (b.segs.size() > 64)
+        throw Error(CGTP_ERR_UNSUPPORTED, "block: more than 64 changes of degree along a row");
+    b.d = (int)col;
+    b.c = (int)ch;
+    b.elem = b.cfg.dtype == CGTP_F64 ? 8 : b.cfg.dtype == CGTP_F32 ? 4 : 2;
+    b.real = b.cfg.dtype == CGTP_F64 ? 8 : 4;
+    b.vec = 16 / b.elem;
+    pick_lanes(b);
+    check_lds(b);
+    b.source = constants(b) + kBlockKernels;
+    b.code = compile_source(b.source);
+}
+
+const Block::Fns &block_for_current_device(Block &b)
+{
+    int dev = 0;
+    check_hip(hipGetDevice(&dev), "hipGetDevice");
+    std::lock_guard<std::mutex> lock(b.mu);
+    auto it = b.loaded.find(dev);
+    if (it != b.loaded.end()) return it->second;
+    Block::Fns F;
+    check_hip(hipModuleLoadData(&F.module, b.code.data()), "hipModuleLoadData");
+    check_hip(hipModuleGetFunction(&F.norm_fwd, F.module, "cgtp_norm_fwd"), "hipModuleGetFunction(norm_fwd)");
+    check_hip(hipModuleGetFunction(&F.norm_bwd, F.module, "cgtp_norm_bwd"), "hipModuleGetFunction(norm_bwd)");
+    check_hip(hipModuleGetFunction(&F.join_fwd, F.module, "cgtp_join_fwd"), "hipModuleGetFunction(join_fwd)");
+    check_hip(hipModuleGetFunction(&F.join_bwd, F.module, "cgtp_join_bwd"), "hipModuleGetFunction(join_bwd)");
+    check_hip(hipModuleGetFunction(&F.reduce, F.module, "cgtp_block_reduce"), "hipModuleGetFunction(block_reduce)");
+    return b.loaded.emplace(dev, F).first->second;
+}
+
+void unload_block(Block &b)
+{
+    if (b.loaded.empty()) return;
+    int prev = 0;
+    const bool have_prev = hipGetDevice(&prev) == hipSuccess;
+    for (auto &kv : b.loaded)
+        if (kv.second.module && hipSetDevice(kv.first) == hipSuccess) (void)hipModuleUnload(kv.second.module);
+    b.loaded.clear();
+    if (have_prev) (void)hipSetDevice(prev);
+}
+
+int64_t block_forward_groups(const Block &b, int64_t N)
+{
+    const int64_t rows = b.rows_per_group();
+    const int64_t most = (int64_t)tuned("CGTP_BLOCK_FWD_WAVES", 8192) / (b.block / 64);
+    return std::max<int64_t>(1, std::min((N + rows - 1) / rows, most));
+}
+
+int64_t block_backward_groups(const Block &b, int64_t N)
+{
+    const int64_t rows = b.rows_per_group();
+    const int64_t most = (int64_t)tuned("CGTP_BLOCK_BWD_WAVES", 4096) / (b.block / 64);
+    return std::max<int64_t>(1, std::min((N + rows - 1) / rows, most));
+}
+
+namespace {
+
+// Rows of `width` elements every `ld` elements.
+struct Rows {
+    const void *p;
+    int64_t width, ld;
+    const char *name;
+};
+
+void check_rows(const Block &b, int64_t N, const Rows &r)
+{
+    require_ptr(r.p, r.name, b.elem);
+    require(r.ld >= r.width && r.ld < INT_MAX,
+            std::string(r.name) + ": row pitch " + std::to_string(r.ld) + " is below the row's " +
+                std::to_string(r.width) + " elements or above 2^31-1");
+    (void)N;
+}
+
+// No row of one may overlap a row of the other: their ranges are apart, or both have the same
+// pitch and lie side by side inside it (a block's output and its gates in one buffer).
+void rows_apart(const Block &b, int64_t N, const Rows &x, const Rows &y)
+{
+    if (!x.p || !y.p || !N || !x.width || !y.width) return;
+    const int64_t es = b.elem;
+    const uint64_t a = reinterpret_cast<uintptr_t>(x.p), c = reinterpret_cast<uintptr_t>(y.p);
+    const uint64_t na = (uint64_t)((N - 1) * x.ld + x.width) * es, nc = (uint64_t)((N - 1) * y.ld + y.width) * es;
+    if (a + na <= c || c + nc <= a) return;
+    if (x.ld == y.ld) {
+        const int64_t pitch = x.ld * es;
+        int64_t m = (int64_t)(c - a) % pitch;
+        if (m < 0) m += pitch;
+        if (m >= x.width * es && m + y.width * es <= pitch) return;
+    }
+    throw Error(CGTP_ERR_INVALID_ARG, std::string(x.name) + " overlaps " + y.name);
+}
+
+void rows_apart(const Block &b, int64_t N, const Rows &x, const void *p, size_t bytes, const char *name)
+{
+    if (!x.p || !p || !N) return;
+    require_disjoint(x.p, (size_t)((N - 1) * x.ld + x.width) * b.elem, x.name, p, bytes, name);
+}
+
+void check_count(int64_t N)
+{
+    require(N >= 0 && N < INT_MAX, "N must be in [0, 2^31-1)");
+}
+
+void run(hipFunction_t f, int64_t groups, int threads, void **args, void *stream)
+{
+    check_hip(hipModuleLaunchKernel(f, (unsigned)groups, 1, 1, (unsigned)threads, 1, 1, 0,
+                                    static_cast<hipStream_t>(stream), args, nullptr),
+              "hipModuleLaunchKernel");
+}
+
+void reduce_partials(const Block &b, const Block::Fns &F, const void *part, int64_t parts, bool join, const void *w_post,
+                     const void *scale, void *g_post, void *g_scale, void *g_next, void *stream)
+{
+    long rows = (long)parts;
+    int is_join = join ? 1 : 0;
+    int width = b.c * (join && b.cfg.next_norm ? 2 : 1);
+    void *args[] = {&part, &rows, &width, &is_join, &w_post, &scale, &g_post, &g_scale, &g_next};
+    run(F.reduce, (width + 63) / 64, 1024, args, stream);
+}
+
+size_t workspace_bytes_of(const Block &b, int64_t N)
+{
+    return N == 0 ? 0 : (size_t)block_backward_groups(b, N) * b.c * (b.cfg.next_norm ? 2 : 1) * b.real;
+}
+
+// scalars passed to a kernel as its statistics' type
+struct Real {
+    float f;
+    double d;
+    bool wide;
+    Real(const Block &b, double v) : f((float)v), d(v), wide(b.real == 8) {}
+    void *arg() { return wide ? (void *)&d : (void *)&f; }
+};
+
+}  // namespace
+
+}  // namespace cgtp
+
+using namespace cgtp;
+
+extern "C" {
+
+cgtp_status cgtp_block_create(const char *irreps, const cgtp_block_config *config, cgtp_block **block_out)
+{
+    return guarded([&] {
+        require(irreps && config && block_out, "NULL argument to cgtp_block_create");
+        *block_out = nullptr;
+        const cgtp_block_config &c = *config;
+        require(c.dtype == CGTP_F32 || c.dtype == CGTP_F64 || c.dtype == CGTP_BF16 || c.dtype == CGTP_F16,
+                "dtype must be CGTP_F32, CGTP_F64, CGTP_BF16 or CGTP_F16");
+        require(c.gate >= CGTP_GATE_NONE && c.gate <= CGTP_GATE_CHANNEL, "gate must be a cgtp_gate");
+        require(c.act >= CGTP_ACT_IDENTITY && c.act <= CGTP_ACT_TANH, "act must be a cgtp_act");
+        require(std::isfinite(c.eps) && c.eps > 0 && (c.dtype == CGTP_F64 || (float)c.eps >= 1e-30f),
+                "eps must be finite and positive (at least 1e-30 where statistics are float)");
+        require(std::isfinite(c.alpha), "alpha must be finite");
+        auto h = std::make_unique<cgtp_block>();
+        h->b.cfg = c;
+        build_block(h->b, irreps);
+        *block_out = h.release();
+    });
+}
+
+cgtp_status cgtp_block_destroy(cgtp_block *block)
+{
+    return guarded([&] {
+        if (!block) return;
+        unload_block(block->b);
+        delete block;
+    });
+}
+
+cgtp_status cgtp_block_info_get(const cgtp_block *block, cgtp_block_info *info)
+{
+    return guarded([&] {
+        require(block && info, "NULL argument to cgtp_block_info_get");
+        const Block &b = block->b;
+        info->d = b.d;
+        info->channels = b.c;
+        info->gate_width = b.gate_width();
+        info->dtype = b.cfg.dtype;
+        info->lanes = b.lanes;
+        info->chunks = b.chunks;
+    });
+}
+
+const char *cgtp_block_source(const cgtp_block *block) { return block ? block->b.source.c_str() : nullptr; }
+
+cgtp_status cgtp_block_workspace_size(const cgtp_block *block, int64_t N, size_t *bytes)
+{
+    return guarded([&] {
+        require(block && bytes, "NULL argument to cgtp_block_workspace_size");
+        check_count(N);
+        *bytes = workspace_bytes_of(block->b, N);
+    });
+}
+
+cgtp_status cgtp_norm_forward(const cgtp_block *block, int64_t N, const void *x, int64_t x_ld, const void *w, void *u,
+                              void *rstd, void *stream)
+{
+    return guarded([&] {
+        require(block != nullptr, "block is NULL");
+        Block &b = const_cast<cgtp_block *>(block)->b;
+        check_count(N);
+        if (N == 0) return;
+        const Rows X{x, b.d, x_ld, "x"}, U{u, b.d, b.d, "u"};
+        check_rows(b, N, X);
+        check_rows(b, N, U);
+        if (w) require_ptr(w, "w", b.real);
+        if (rstd) require_ptr(rstd, "rstd", b.real);
+        const size_t nw = (size_t)b.c * b.real, ns = (size_t)N * b.real;
+        rows_apart(b, N, U, X);
+        rows_apart(b, N, U, w, nw, "w");
+        rows_apart(b, N, U, rstd, ns, "rstd");
+        rows_apart(b, N, X, rstd, ns, "rstd");
+        require_disjoint(rstd, rstd ? ns : 0, "rstd", w, w ? nw : 0, "w");
+        const auto &F = block_for_current_device(b);
+        long ld = (long)x_ld, rows = (long)N;
+        Real eps(b, b.cfg.eps);
+        void *args[] = {&x, &ld, &w, &u, &rstd, &rows, eps.arg()};
+        run(F.norm_fwd, block_forward_groups(b, N), b.block, args, stream);
+    });
+}
+
+cgtp_status cgtp_norm_backward(const cgtp_block *block, int64_t N, const void *x, int64_t x_ld, const void *w,
+                               const void *rstd, const void *grad_u, const void *grad_add, void *grad_x, void *grad_w,
+                               void *workspace, size_t workspace_bytes, void *stream)
+{
+    return guarded([&] {
+        require(block != nullptr, "block is NULL");
+        Block &b = const_cast<cgtp_block *>(block)->b;
+        check_count(N);
+        if (!grad_x && !grad_w) return;
+        if (grad_w) require_ptr(grad_w, "grad_w", b.real);
+        const size_t nw = (size_t)b.c * b.real, ns = (size_t)N * b.real;
+        if (N == 0) {
+            if (grad_w)
+                reduce_partials(b, block_for_current_device(b), nullptr, 0, false, nullptr, nullptr, nullptr, nullptr,
+                                grad_w, stream);
+            return;
+        }
+        const Rows X{x, b.d, x_ld, "x"}, DU{grad_u, b.d, b.d, "grad_u"}, ADD{grad_add, b.d, b.d, "grad_add"},
+            DX{grad_x, b.d, b.d, "grad_x"};
+        check_rows(b, N, X);
+        check_rows(b, N, DU);
+        if (grad_add) check_rows(b, N, ADD);
+        if (grad_x) check_rows(b, N, DX);
+        if (w) require_ptr(w, "w", b.real);
+        require_ptr(rstd, "rstd", b.real);
+        size_t need = 0;
+        if (grad_w) {
+            need = (size_t)block_backward_groups(b, N) * nw;
+            require_ptr(workspace, "workspace", 256);
+            require(workspace_bytes >= need, "workspace too small (see cgtp_block_workspace_size)");
+        }
+        struct { void *p; size_t n; const char *name; } outs[] = {
+            {grad_x, grad_x ? (size_t)N * b.d * b.elem : 0, "grad_x"},
+            {grad_w, grad_w ? nw : 0, "grad_w"},
+            {need ? workspace : nullptr, need, "workspace"}};
+        struct { const void *p; size_t n; const char *name; } ins[] = {
+            {x, (size_t)((N - 1) * x_ld + b.d) * b.elem, "x"}, {grad_u, (size_t)N * b.d * b.elem, "grad_u"},
+            {grad_add, grad_add ? (size_t)N * b.d * b.elem : 0, "grad_add"}, {w, w ? nw : 0, "w"}, {rstd, ns, "rstd"}};
+        for (int i = 0; i < 3; ++i) {
+            for (auto &in : ins) require_disjoint(outs[i].p, outs[i].n, outs[i].name, in.p, in.n, in.name);
+            for (int j = i + 1; j < 3; ++j)
+                require_disjoint(outs[i].p, outs[i].n, outs[i].name, outs[j].p, outs[j].n, outs[j].name);
+        }
+        const auto &F = block_for_current_device(b);
+        long ld = (long)x_ld, rows = (long)N;
+        void *part = grad_w ? workspace : nullptr;
+        void *args[] = {&x, &ld, &w, &rstd, &grad_u, &grad_add, &grad_x, &part, &rows};
+        const int64_t groups = block_backward_groups(b, N);
+        run(F.norm_bwd, groups, b.block, args, stream);
+        if (grad_w)
+            reduce_partials(b, F, part, groups, false, nullptr, nullptr, nullptr, nullptr, grad_w, stream);
+    });
+}
+
+cgtp_status cgtp_join_forward(const cgtp_block *block, int64_t N, const void *res, const void *f, int64_t f_ld,
+                              const void *gate, int64_t gate_ld, const void *w_post, const void *scale,
+                              const void *w_next, void *h, void *u, void *rstd_f, void *rstd_h, void *stream)
+{
+    return guarded([&] {
+        require(block != nullptr, "block is NULL");
+        Block &b = const_cast<cgtp_block *>(block)->b;
+        check_count(N);
+        if (N == 0) return;
+        const int gw = b.gate_width();
+        const bool next = b.cfg.next_norm != 0, post = b.cfg.post_norm != 0;
+        require(gw > 0 || !gate, "gate given to a block without one");
+        require(next || (!u && !w_next && !rstd_h), "u, w_next or rstd_h given to a block without a next norm");
+        require(post || (!w_post && !rstd_f), "w_post or rstd_f given to a block without a post norm");
+        const Rows RES{res, b.d, b.d, "res"}, F_{f, b.d, f_ld, "f"}, GT{gate, gw, gate_ld, "gate"}, H{h, b.d, b.d, "h"},
+            U{u, b.d, b.d, "u"};
+        check_rows(b, N, RES);
+        check_rows(b, N, F_);
+        if (gw) check_rows(b, N, GT);
+        check_rows(b, N, H);
+        if (next) check_rows(b, N, U);
+        struct { const void *p; size_t n; const char *name; bool out; } reals[] = {
+            {w_post, (size_t)b.c * b.real, "w_post", false}, {scale, (size_t)b.c * b.real, "scale", false},
+            {w_next, (size_t)b.c * b.real, "w_next", false}, {rstd_f, (size_t)N * b.real, "rstd_f", true},
+            {rstd_h, (size_t)N * b.real, "rstd_h", true}};
+        for (auto &r : reals) {
+            if (r.p) require_ptr(r.p, r.name, b.real);
+            rows_apart(b, N, H, r.p, r.n, r.name);
+            if (next) rows_apart(b, N, U, r.p, r.n, r.name);
+            if (!r.out) continue;
+            for (const Rows *in : {&RES, &F_, &GT}) rows_apart(b, N, *in, r.p, r.n, r.name);
+            for (auto &o : reals)
+                if (&o != &r) require_disjoint(r.p, r.p ? r.n : 0, r.name, o.p, o.p ? o.n : 0, o.name);
+        }
+        for (const Rows *in : {&RES, &F_, &GT}) {
+            rows_apart(b, N, H, *in);
+            if (next) rows_apart(b, N, U, *in);
+        }
+        if (next) rows_apart(b, N, H, U);
+        const auto &F = block_for_current_device(b);
+        long fl = (long)f_ld, gl = (long)gate_ld, rows = (long)N;
+        Real alpha(b, b.cfg.alpha), eps(b, b.cfg.eps);
+        void *args[] = {&res, &f, &fl, &gate, &gl, &w_post, &scale, &w_next, &h, &u, &rstd_f, &rstd_h, &rows,
+                        alpha.arg(), eps.arg()};
+        run(F.join_fwd, block_forward_groups(b, N), b.block, args, stream);
+    });
+}
+
+cgtp_status cgtp_join_backward(const cgtp_block *block, int64_t N, const void *grad_h, const void *grad_u,
+                               const void *h, const void *f, int64_t f_ld, const void *gate, int64_t gate_ld,
+                               const void *w_post, const void *scale, const void *w_next, const void *rstd_f,
+                               const void *rstd_h, void *grad_res, void *grad_f, int64_t grad_f_ld, void *grad_gate,
+                               int64_t grad_gate_ld, void *grad_w_post, void *grad_scale, void *grad_w_next,
+                               void *workspace, size_t workspace_bytes, void *stream)
+{
+    return guarded([&] {
+        require(block != nullptr, "block is NULL");
+        Block &b = const_cast<cgtp_block *>(block)->b;
+        check_count(N);
+        const int gw = b.gate_width();
+        const bool next = b.cfg.next_norm != 0, post = b.cfg.post_norm != 0;
+        require(gw > 0 || (!gate && !grad_gate), "gate or grad_gate given to a block without one");
+        require(next || (!grad_u && !w_next && !rstd_h && !grad_w_next),
+                "grad_u, w_next, rstd_h or grad_w_next given to a block without a next norm");
+        require(post || (!w_post && !rstd_f && !grad_w_post),
+                "w_post, rstd_f or grad_w_post given to a block without a post norm");
+        const bool weights = grad_w_post || grad_scale || grad_w_next;
+        if (!grad_res && !grad_f && !grad_gate && !weights) return;
+        const size_t nw = (size_t)b.c * b.real, ns = (size_t)N * b.real;
+        if (w_post) require_ptr(w_post, "w_post", b.real);
+        if (scale) require_ptr(scale, "scale", b.real);
+        if (w_next) require_ptr(w_next, "w_next", b.real);
+        if (grad_w_post) require_ptr(grad_w_post, "grad_w_post", b.real);
+        if (grad_scale) require_ptr(grad_scale, "grad_scale", b.real);
+        if (grad_w_next) require_ptr(grad_w_next, "grad_w_next", b.real);
+        if (N == 0) {
+            if (weights)
+                reduce_partials(b, block_for_current_device(b), nullptr, 0, true, nullptr, nullptr, grad_w_post,
+                                grad_scale, grad_w_next, stream);
+            return;
+        }
+        const Rows DH{grad_h, b.d, b.d, "grad_h"}, DU{grad_u, b.d, b.d, "grad_u"}, H{h, b.d, b.d, "h"},
+            F_{f, b.d, f_ld, "f"}, GT{gate, gw, gate_ld, "gate"};
+        const Rows DR{grad_res, b.d, b.d, "grad_res"}, DF{grad_f, b.d, grad_f_ld, "grad_f"},
+            DG{grad_gate, gw, grad_gate_ld, "grad_gate"};
+        require(grad_h || next, "grad_h is NULL");
+        if (grad_h) check_rows(b, N, DH);
+        if (next) {
+            check_rows(b, N, DU);
+            check_rows(b, N, H);
+            require_ptr(rstd_h, "rstd_h", b.real);
+        }
+        check_rows(b, N, F_);
+        if (gw) check_rows(b, N, GT);
+        if (post) require_ptr(rstd_f, "rstd_f", b.real);
+        for (const Rows *o : {&DR, &DF, &DG})
+            if (o->p) check_rows(b, N, *o);
+        size_t need = 0;
+        if (weights) {
+            need = workspace_bytes_of(b, N);
+            require_ptr(workspace, "workspace", 256);
+            require(workspace_bytes >= need, "workspace too small (see cgtp_block_workspace_size)");
+        }
+        const Rows NH = next ? H : Rows{nullptr, 0, 0, "h"};
+        const Rows *row_in[] = {&DH, &DU, &NH, &F_, &GT}, *row_out[] = {&DR, &DF, &DG};
+        struct { const void *p; size_t n; const char *name; bool out; } reals[] = {
+            {w_post, nw, "w_post", false}, {scale, nw, "scale", false}, {w_next, nw, "w_next", false},
+            {rstd_f, ns, "rstd_f", false}, {rstd_h, ns, "rstd_h", false}, {grad_w_post, nw, "grad_w_post", true},
+            {grad_scale, nw, "grad_scale", true}, {grad_w_next, nw, "grad_w_next", true},
+            {weights ? workspace : nullptr, need, "workspace", true}};
+        for (int i = 0; i < 3; ++i) {
+            for (const Rows *in : row_in) rows_apart(b, N, *row_out[i], *in);
+            for (int j = i + 1; j < 3; ++j) rows_apart(b, N, *row_out[i], *row_out[j]);
+            for (auto &r : reals) rows_apart(b, N, *row_out[i], r.p, r.n, r.name);
+        }
+        for (auto &r : reals) {
+            if (!r.out || !r.p) continue;
+            for (const Rows *in : row_in) rows_apart(b, N, *in, r.p, r.n, r.name);
+            for (auto &o : reals)
+                if (&o != &r) require_disjoint(r.p, r.n, r.name, o.p, o.p ? o.n : 0, o.name);
+        }
+        const auto &F = block_for_current_device(b);
+        long fl = (long)f_ld, gl = (long)gate_ld, dfl = (long)grad_f_ld, dgl = (long)grad_gate_ld, rows = (long)N;
+        void *part = weights ? workspace : nullptr;
+        Real alpha(b, b.cfg.alpha);
+        void *args[] = {&grad_h, &grad_u, &h, &f, &fl, &gate, &gl, &w_post, &scale, &w_next, &rstd_f, &rstd_h, &grad_res,
+                        &grad_f, &dfl, &grad_gate, &dgl, &part, &rows, alpha.arg()};
+        const int64_t groups = block_backward_groups(b, N);
+        run(F.join_bwd, groups, b.block, args, stream);
+        if (weights)
+            reduce_partials(b, F, part, groups, true, w_post, scale, grad_w_post, grad_scale, grad_w_next, stream);
+    });
+}
+
+}  // extern "C"

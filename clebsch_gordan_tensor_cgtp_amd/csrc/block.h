@@ -1,0 +1,48 @@
+// A block plan: the row norm at a block's entry and the join at its end, for one irreps row and
+// one configuration.  Its kernels (block_kernels.h) are compiled per plan, as the convolution's are.
+#pragma once
+
+#include <hip/hip_runtime_api.h>
+
+#include <cstdint>
+#include <map>
+#include <mutex>
+#include <string>
+#include <vector>
+
+#include "cgtp.h"
+#include "plan.h"
+
+namespace cgtp {
+
+struct Block {
+    struct Segment {
+        int col, ch, k;  // first column, first channel, 2l+1
+    };
+    std::vector<Segment> segs;  // neighbouring irreps of equal degree are one
+    int d = 0, c = 0;           // columns, channels
+    cgtp_block_config cfg{};
+    int elem = 4, real = 4;     // bytes of an element; of a statistic, weight or sum
+    int vec = 4, lanes = 64, chunks = 1, block = 256;
+    std::string source;
+    std::vector<char> code;
+
+    std::mutex mu;  // guards the per-device modules
+    struct Fns {
+        hipModule_t module = nullptr;
+        hipFunction_t norm_fwd = nullptr, norm_bwd = nullptr, join_fwd = nullptr, join_bwd = nullptr, reduce = nullptr;
+    };
+    std::map<int, Fns> loaded;
+
+    int rows_per_group() const { return block / lanes; }  // rows of a workgroup at a time
+    int gate_width() const { return cfg.gate == CGTP_GATE_CHANNEL ? c : cfg.gate == CGTP_GATE_ROW ? 1 : 0; }
+};
+
+void build_block(Block &b, const std::string &irreps);
+const Block::Fns &block_for_current_device(Block &b);
+void unload_block(Block &b);
+// workgroups of a forward and of a backward pass over N rows (one partial of the weight gradients each)
+int64_t block_forward_groups(const Block &b, int64_t N);
+int64_t block_backward_groups(const Block &b, int64_t N);
+
+}  // namespace cgtp

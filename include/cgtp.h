@@ -32,11 +32,12 @@
  *    uvw weights (shared): the concatenation over paths of [mul_in][mul_out].
  *
  * Memory and streams: every device buffer is owned by the caller, must be a
- * device pointer to contiguous row-major data of the plan's dtype, aligned
- * to its element size, and outputs must not alias inputs.  The library
+ * device pointer to contiguous row-major data of the plan's dtype (rows a
+ * stated pitch apart where an entry point takes one), aligned to its element size, and outputs must not alias inputs.  The library
  * never allocates, frees or synchronises device memory; the entry points that
  * need temporary memory (cgtp_tp_backward and cgtp_conv_backward_ws for uvw,
- * cgtp_conv_backward_radial for dTheta) take it from the caller.  `stream` is a hipStream_t (NULL = the default
+ * cgtp_conv_backward_radial for dTheta, the block backwards' weight gradients,
+ * cgtp_grad_norm) take it from the caller.  `stream` is a hipStream_t (NULL = the default
  * stream); all work is enqueued on it asynchronously.
  * Index arrays are int32 and N, E < 2^31.
  *
@@ -66,7 +67,8 @@ typedef enum cgtp_status {
 } cgtp_status;
 
 typedef enum cgtp_mode { CGTP_UVU = 0, CGTP_UVW = 1 } cgtp_mode;
-typedef enum cgtp_dtype { CGTP_F32 = 0, CGTP_F64 = 1 } cgtp_dtype;
+/* The 16-bit types are taken by the block and optimizer entry points only. */
+typedef enum cgtp_dtype { CGTP_F32 = 0, CGTP_F64 = 1, CGTP_BF16 = 2, CGTP_F16 = 3 } cgtp_dtype;
 
 typedef struct cgtp_plan cgtp_plan; /* opaque, immutable after creation */
 
@@ -519,6 +521,174 @@ cgtp_status cgtp_conv_double_backward_ws(const cgtp_plan *plan, int64_t N, int64
  */
 cgtp_status cgtp_spherical_harmonics(int32_t lmax, cgtp_dtype dtype, int64_t E, const void *vec,
                                      void *y, void *stream);
+
+/*
+ * Blocks: what stands between two convolutions of a residual network, in one pass over the node
+ * features each way.  A row is one node's irreps features as everywhere in this library (channel u,
+ * component m of an irrep at offset + u*(2L+1) + (m+L)); "Dx0e" is an ordinary row of D scalars.
+ *   norm:  u = x rstd(x) w[c],  rstd(x) = (sum_columns x^2 / d + eps)^(-1/2);
+ *   join:  h = alpha res + scale[c] act(gate) w_post[c] f rstd(f),
+ *          u = h rstd(h) w_next[c]
+ * with c the channel of a column.  A rotation changes no row's sum of squares, and weights and
+ * gates are one per channel, so both commute with rotations (cgtp_plan_create's conventions).
+ * post_norm = 0 leaves out w_post and rstd(f); next_norm = 0 leaves out u.
+ *
+ * Types: x, res, f, gate, h, u and their gradients are of the block's dtype; statistics, weights
+ * and weight gradients are float (double for CGTP_F64), and so is all arithmetic.  h is rounded once;
+ * u is formed from h before that rounding.
+ *
+ * The kernels of a block are compiled for its irreps and configuration when it is created (as a
+ * plan's: same compiler, cache and cgtp_last_error log).  Allocates no device memory.
+ * CGTP_ERR_UNSUPPORTED: a row of more than 131072 bytes, more than 64 changes of degree along it, or
+ * sums over its channels that exceed a workgroup's LDS.
+ */
+typedef enum cgtp_gate { CGTP_GATE_NONE = 0, CGTP_GATE_ROW = 1, CGTP_GATE_CHANNEL = 2 } cgtp_gate;
+typedef enum cgtp_act { CGTP_ACT_IDENTITY = 0, CGTP_ACT_SIGMOID = 1, CGTP_ACT_SILU = 2, CGTP_ACT_TANH = 3 } cgtp_act;
+
+typedef struct cgtp_block cgtp_block; /* opaque, immutable after creation */
+
+typedef struct cgtp_block_config {
+    int32_t dtype;     /* cgtp_dtype                                             */
+    int32_t gate;      /* cgtp_gate: one logit per row, or one per channel       */
+    int32_t act;       /* cgtp_act, of the gate                                  */
+    int32_t post_norm; /* 1: f is normed                                         */
+    int32_t next_norm; /* 1: u is formed                                         */
+    double eps;        /* > 0                                                    */
+    double alpha;      /* of the residual                                        */
+} cgtp_block_config;
+
+typedef struct cgtp_block_info {
+    int32_t d;          /* columns of a row                                      */
+    int32_t channels;   /* weights per row                                       */
+    int32_t gate_width; /* 0, 1 or channels                                      */
+    int32_t dtype;
+    int32_t lanes;      /* lanes that share a row                                */
+    int32_t chunks;     /* 16-byte chunks of a lane                              */
+} cgtp_block_info;
+
+cgtp_status cgtp_block_create(const char *irreps, const cgtp_block_config *config, cgtp_block **block_out);
+/* As cgtp_plan_destroy: after every kernel launched with it has finished; NULL is ignored. */
+cgtp_status cgtp_block_destroy(cgtp_block *block);
+cgtp_status cgtp_block_info_get(const cgtp_block *block, cgtp_block_info *info);
+/* The HIP source of the block's module (owned by the block). */
+const char *cgtp_block_source(const cgtp_block *block);
+/* Workspace of a backward pass over N rows that returns a weight gradient: one partial sum per
+ * workgroup.  256-byte aligned, caller-owned, contents ignored on entry. */
+cgtp_status cgtp_block_workspace_size(const cgtp_block *block, int64_t N, size_t *bytes);
+
+/*
+ * The norm at a block's entry (its own configuration needs no gate or norms).  x is N rows, `x_ld`
+ * elements apart (x_ld >= d), u [N][d]; rstd [N] (may be NULL) receives the rows' statistics for
+ * the backward; w [channels], NULL for ones.  N = 0 is a no-op.  Errors: CGTP_ERR_INVALID_ARG.
+ */
+cgtp_status cgtp_norm_forward(const cgtp_block *block, int64_t N, const void *x, int64_t x_ld, const void *w, void *u,
+                              void *rstd, void *stream);
+/*
+ * Its backward: with g = grad_u [N][d] and y = x rstd,
+ *   grad_x [N][d]        = rstd (g w - y mean(g w y)) + grad_add,
+ *   grad_w [channels]    = sum over rows and the channel's columns of g y.
+ * grad_add [N][d] (NULL: none) is the gradient that reaches x past the norm, its residual's.  Either
+ * output may be NULL; the workspace is needed for grad_w.  Outputs are overwritten, no atomics,
+ * bitwise deterministic; N = 0 sets grad_w to zero.
+ */
+cgtp_status cgtp_norm_backward(const cgtp_block *block, int64_t N, const void *x, int64_t x_ld, const void *w,
+                               const void *rstd, const void *grad_u, const void *grad_add, void *grad_x, void *grad_w,
+                               void *workspace, size_t workspace_bytes, void *stream);
+/*
+ * The join of a block's output with its residual and the next block's norm.  res, h, u [N][d]; f
+ * and gate are N rows f_ld and gate_ld elements apart (they may lie side by side in one buffer);
+ * gate [N][gate_width], NULL without one; w_post, scale, w_next [channels], each NULL for ones;
+ * rstd_f, rstd_h [N] receive the statistics for the backward and may be NULL.  N = 0 is a no-op.
+ */
+cgtp_status cgtp_join_forward(const cgtp_block *block, int64_t N, const void *res, const void *f, int64_t f_ld,
+                              const void *gate, int64_t gate_ld, const void *w_post, const void *scale,
+                              const void *w_next, void *h, void *u, void *rstd_f, void *rstd_h, void *stream);
+/*
+ * Its backward, from the gradients of h (NULL: zero, where the block has a next norm) and of u, the
+ * forward's h and statistics.  With z = h rstd_h, q = grad_u w_next, y = f rstd_f (f without the norm),
+ * a = act(gate), b = a scale w_post:
+ *   e            = grad_h + rstd_h (q - z mean(q z))
+ *   grad_res     = alpha e
+ *   grad_f       = rstd_f (e b - y mean(e b y))            (e b without the norm)
+ *   grad_gate    = act'(gate) sum_columns e y scale w_post  (a channel's columns, or the row's)
+ *   grad_scale   = w_post P, grad_w_post = scale P,  P = sum_rows a sum_columns e y
+ *   grad_w_next  = sum_rows sum_columns grad_u z
+ * grad_f and grad_gate may lie side by side in one buffer (grad_f_ld, grad_gate_ld).  Any output may
+ * be NULL; the workspace is needed for a weight gradient.  Outputs are overwritten, no atomics,
+ * bitwise deterministic; N = 0 sets the weight gradients to zero.
+ */
+cgtp_status cgtp_join_backward(const cgtp_block *block, int64_t N, const void *grad_h, const void *grad_u,
+                               const void *h, const void *f, int64_t f_ld, const void *gate, int64_t gate_ld,
+                               const void *w_post, const void *scale, const void *w_next, const void *rstd_f,
+                               const void *rstd_h, void *grad_res, void *grad_f, int64_t grad_f_ld, void *grad_gate,
+                               int64_t grad_gate_ld, void *grad_w_post, void *grad_scale, void *grad_w_next,
+                               void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * AdamW over many tensors at once.  With f = grad_scale, times max_norm / n where the scaled norm
+ * n = |grad_scale| norm exceeds max_norm, and g = f grad:
+ *   m = beta1 m + (1 - beta1) g,  v = beta2 v + (1 - beta2) g^2,
+ *   p = p (1 - lr weight_decay) - lr / (1 - beta1^step) m / (sqrt(v) / sqrt(1 - beta2^step) + eps).
+ * Where a norm is given and is not finite, the step changes nothing.
+ *
+ * Moments are flat buffers of `elements` values (cgtp_adamw_info): tensor t's start at
+ * cgtp_adamw_offset, every tensor padded to 2048 elements; the padding starts as zero and stays so.
+ * state_bits 32: m, v float (double for CGTP_F64).  state_bits 8: m int8, v uint8 codes and scales
+ * [2][blocks] float, one for 64 values each: m = scales[0] sign (code / 127)^2, v = s^2 with
+ * s = scales[1] (code / 255)^2; a code is the nearest one, and never 0 for a v above 0; all zeros are the start.
+ * A block that holds a value that is not finite reads as NaN.  master = 1 (16-bit tensors): `master`
+ * [elements] float holds the weights, and the tensors receive its rounding; without it the 16-bit tensors
+ * are the weights and are rounded to nearest each step.
+ * m, v, master: 16-byte aligned.  Arithmetic is float (double for CGTP_F64).
+ *
+ * params and grads are host arrays of n_tensors device pointers, taken at the call (a tensor's
+ * gradient has its type; any alignment to it).  A tensor whose gradient is NULL is left as it is, its moments too.
+ * step counts from 1.  For captured graphs, `schedule` (device, double[4]: step, lr, 1 - beta1^step,
+ * 1 - beta2^step; NULL otherwise) takes the place of hyper's lr and step; cgtp_adamw_schedule adds
+ * one to its step and sets the last two.  `norm` is a device double, as of cgtp_grad_norm, or NULL.
+ * Errors: CGTP_ERR_INVALID_ARG (also where memory that is written overlaps any other),
+ * CGTP_ERR_UNSUPPORTED (8-bit moments of double precision tensors).
+ */
+typedef struct cgtp_adamw cgtp_adamw; /* opaque, immutable after creation; host memory only */
+
+typedef struct cgtp_adamw_config {
+    int32_t dtype;      /* cgtp_dtype of every tensor and its gradient */
+    int32_t state_bits; /* 32 or 8                                     */
+    int32_t master;     /* 1: single precision copies of 16-bit tensors */
+} cgtp_adamw_config;
+
+typedef struct cgtp_adamw_info {
+    int64_t elements;       /* of m, v and master                  */
+    int64_t blocks;         /* scales of one moment                */
+    int64_t norm_workspace; /* bytes of cgtp_grad_norm's workspace */
+    int32_t n_tensors;
+} cgtp_adamw_info;
+
+typedef struct cgtp_adamw_hyper {
+    double lr, beta1, beta2, eps, weight_decay;
+    double max_norm;   /* 0: no clipping   */
+    double grad_scale; /* 1: none          */
+    int64_t step;
+} cgtp_adamw_hyper;
+
+cgtp_status cgtp_adamw_create(int32_t n_tensors, const int64_t *sizes, const cgtp_adamw_config *config,
+                              cgtp_adamw **opt_out);
+cgtp_status cgtp_adamw_destroy(cgtp_adamw *opt); /* NULL is ignored */
+cgtp_status cgtp_adamw_info_get(const cgtp_adamw *opt, cgtp_adamw_info *info);
+cgtp_status cgtp_adamw_offset(const cgtp_adamw *opt, int32_t tensor, int64_t *offset);
+/* norm = sqrt of the sum of squares of every gradient that is not NULL, squared and summed in double
+ * in a fixed order; norm and the 256-byte aligned workspace are device memory. */
+cgtp_status cgtp_grad_norm(const cgtp_adamw *opt, const void *const *grads, double *norm, void *workspace,
+                           size_t workspace_bytes, void *stream);
+cgtp_status cgtp_adamw_step(const cgtp_adamw *opt, void *const *params, const void *const *grads, void *m, void *v,
+                            float *scales, float *master, const cgtp_adamw_hyper *hyper, const double *norm,
+                            const double *schedule, void *stream);
+cgtp_status cgtp_adamw_schedule(double *schedule, double beta1, double beta2, void *stream);
+/* 8-bit moments as float values (`elements` each; either output may be NULL) and back. */
+cgtp_status cgtp_adamw_state_read(const cgtp_adamw *opt, const void *m, const void *v, const float *scales,
+                                  float *m_out, float *v_out, void *stream);
+cgtp_status cgtp_adamw_state_write(const cgtp_adamw *opt, const float *m_in, const float *v_in, void *m, void *v,
+                                   float *scales, void *stream);
 
 /*
  * Message of the last failed call on this thread ("" if none).  Not on the
