@@ -28,6 +28,8 @@ ref      numpy definitions: batched TP (uvu, uvw) and its backward, conv forward
 loops    ctypes front-end to ``cpu_loops.c`` (explicit fp64 loops, OpenMP), and
          the double backward, the uvw conv and the radial conv on sampled rows
          composed from those loops
+block    row norm and block join (norm, gate, residual sum, next norm), forward and backward
+optim    AdamW in float64 and the 8-bit codes of its moments
 
 Parity status: every function here is pinned by the ``-m "not gpu"`` tests
 (closed forms, orthogonality, a library CG/SH, brute force, equivariance,
@@ -35,5 +37,6 @@ the trilinear identity and finite differences; the double backward (uvu and
 uvw) against torch autograd applied twice to a dense einsum, finite
 differences of the first-order oracle, and its four Euler identities; the uvw and radial
 backwards against torch autograd through a dense einsum, one-hot and adjoint
-identities).  No function is "parity unpinned".
+identities; the norm, the join and AdamW against torch autograd and torch.optim on the CPU and
+finite differences).  No function is "parity unpinned".
 """
