@@ -189,8 +189,8 @@ cgtp_status cgtp_adamw_step(const cgtp_adamw *opt, void *const *params, const vo
         const cgtp_adamw_hyper &h = *hyper;
         require(std::isfinite(h.lr) && h.lr >= 0, "lr must be finite and not negative");
         require(h.beta1 >= 0 && h.beta1 < 1 && h.beta2 >= 0 && h.beta2 < 1, "betas must lie in [0, 1)");
-        require(std::isfinite(h.eps) && h.eps > 0 && (o.real == 8 || (float)h.eps > 0),
-                "eps must be finite and positive in the moments' precision");
+        require(std::isfinite(h.eps) && h.eps > 0 && (o.real == 8 || h.eps >= 1e-30),
+                "eps must be finite and positive (at least 1e-30 where arithmetic is float)");
         require(std::isfinite(h.weight_decay) && h.weight_decay >= 0, "weight_decay must be finite and not negative");
         require(h.max_norm >= 0, "max_norm must not be negative or NaN (0: no clipping)");
         require(std::isfinite(h.grad_scale), "grad_scale must be finite");
