@@ -67,7 +67,7 @@ class BlockConfig(ctypes.Structure):
 
 
 class BlockInfo(ctypes.Structure):
-    _fields_ = [(n, ctypes.c_int32) for n in ("d", "channels", "gate_width", "dtype", "lanes", "chunks")]
+    _fields_ = [(n, ctypes.c_int32) for n in ("d", "channels", "gate_width", "dtype", "lanes", "elements")]
 
 
 class AdamWConfig(ctypes.Structure):
@@ -664,7 +664,7 @@ class Block:
         info = BlockInfo()
         _check(lib().cgtp_block_info_get(h, ctypes.byref(info)))
         self.d, self.channels, self.gate_width = info.d, info.channels, info.gate_width
-        self.lanes, self.chunks = info.lanes, info.chunks
+        self.lanes, self.lane_elements = info.lanes, info.elements
         self.torch_dtype = _torch_dtype(dtype)                              # of rows
         self.real_dtype = _torch_dtype("f64" if dtype == "f64" else "f32")  # of statistics and weights
 
@@ -695,31 +695,60 @@ def block_for(irreps, dtype="f32", gate=None, act="sigmoid", post_norm=False, ne
     return Block(irreps, dtype, gate, act, post_norm, next_norm, eps, alpha)
 
 
-def _rows(t, name, dtype, n, width):
-    """(pointer, row pitch) of n rows of `width` consecutive elements, any pitch of at least that."""
+def _device_index(t, name):
     import torch
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA (HIP) torch tensor")
-    if t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if tuple(t.shape) != (n, width):
-        raise ValueError(f"{name} must have shape {(n, width)}, got {tuple(t.shape)}")
-    if width > 1 and t.stride(1) != 1:
-        raise ValueError(f"{name}: the elements of a row must be consecutive")
-    ld = t.stride(0) if n > 1 else width
-    if ld < width:
-        raise ValueError(f"{name}: rows overlap (row pitch {ld} of {width} elements)")
-    return ctypes.c_void_p(t.data_ptr()), ld
+    return t.get_device()
 
 
-def _rows_or_null(t, name, dtype, n, width):
-    return (ctypes.c_void_p(0), width) if t is None else _rows(t, name, dtype, n, width)
+def _raw_stream(stream, index):
+    import torch
+    return stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(index)
 
 
-def _same_device(x, **tensors):
-    for name, t in tensors.items():
-        if t is not None and t.device != x.device:
-            raise ValueError(f"{name} is on {t.device}, expected {x.device}")
+def _refuse(t, name, dtype, shape, index):
+    """Raise what is wrong with a tensor that _addr did not take."""
+    _dev(t, name, dtype, shape)
+    raise ValueError(f"{name} is on {t.device}, expected cuda:{index}")
+
+
+def _addr(t, name, dtype, shape, index):
+    """Address of a contiguous tensor of this type, shape and device."""
+    try:
+        if t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.get_device() == index:
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    return _refuse(t, name, dtype, shape, index)
+
+
+def _addr_or_null(t, name, dtype, shape, index):
+    return None if t is None else _addr(t, name, dtype, shape, index)
+
+
+def _rows(t, name, dtype, shape, index):
+    """(address, row pitch) of n rows of `width` consecutive elements, any pitch of at least that."""
+    n, width = shape
+    try:
+        if t.dtype is dtype and t.shape == shape and t.get_device() == index:
+            ld, one = t.stride()
+            if n <= 1:
+                ld = width
+            if ld >= width and (one == 1 or width <= 1):
+                return t.data_ptr(), ld
+    except AttributeError:
+        pass
+    _device_index(t, name)
+    if t.dtype == dtype and tuple(t.shape) == tuple(shape) and t.get_device() == index:
+        if width > 1 and t.stride(1) != 1:
+            raise ValueError(f"{name}: the elements of a row must be consecutive")
+        raise ValueError(f"{name}: rows overlap (row pitch {t.stride(0)} of {width} elements)")
+    return _refuse(t.contiguous(), name, dtype, shape, index)
+
+
+def _rows_or_null(t, name, dtype, shape, index):
+    return (None, shape[1]) if t is None else _rows(t, name, dtype, shape, index)
 
 
 def block_workspace_size(block: Block, n: int) -> int:
@@ -728,27 +757,27 @@ def block_workspace_size(block: Block, n: int) -> int:
     return v.value
 
 
-def _workspace(block, n, workspace, device, wanted):
+def _workspace(t, name, nbytes, like, index):
+    """(address, bytes, tensor) of the caller's workspace, or of a new one."""
     import torch
-    if not wanted:
-        return ctypes.c_void_p(0), 0, None
-    if workspace is None:
-        workspace = torch.empty(block_workspace_size(block, n), dtype=torch.uint8, device=device)
-    return _dev(workspace, "workspace"), workspace.numel() * workspace.element_size(), workspace
+    if t is None:
+        t = like.new_empty(nbytes, dtype=torch.uint8)
+        return t.data_ptr(), nbytes, t
+    return _addr(t, name, t.dtype, t.shape, index), t.numel() * t.element_size(), t
 
 
 def norm_forward(block: Block, x, w, u=None, rstd=None, need_rstd=True, stream=None):
     """(u, rstd): u = x * rstd(x) * w per channel.  x may have a row pitch; w None stands for ones."""
-    import torch
+    dev = _device_index(x, "x")
     n, dt, rt = x.shape[0], block.torch_dtype, block.real_dtype
-    u = torch.empty((n, block.d), dtype=dt, device=x.device) if u is None else u
+    rows = (n, block.d)
+    xp, x_ld = _rows(x, "x", dt, rows, dev)
+    u = x.new_empty(rows) if u is None else u
     if rstd is None and need_rstd:
-        rstd = torch.empty(n, dtype=rt, device=x.device)
-    _same_device(x, w=w, u=u, rstd=rstd)
-    xp, x_ld = _rows(x, "x", dt, n, block.d)
-    _check(lib().cgtp_norm_forward(block.handle, n, xp, x_ld, _ptr_or_null(w, "w", rt, (block.channels,)),
-                                   _dev(u, "u", dt, (n, block.d)), _ptr_or_null(rstd, "rstd", rt, (n,)),
-                                   _stream(stream, x.device)))
+        rstd = x.new_empty(n, dtype=rt)
+    _check(lib().cgtp_norm_forward(block.handle, n, xp, x_ld, _addr_or_null(w, "w", rt, (block.channels,), dev),
+                                   _addr(u, "u", dt, rows, dev), _addr_or_null(rstd, "rstd", rt, (n,), dev),
+                                   _raw_stream(stream, dev)))
     return u, rstd
 
 
@@ -756,19 +785,20 @@ def norm_backward(block: Block, x, w, rstd, grad_u, grad_add=None, grad_x=None, 
                   workspace=None, stream=None):
     """(grad_x, grad_w); entries not in ``need`` are None and not computed.  grad_add, when given,
     is added to grad_x (the gradient that reaches x past the norm)."""
-    import torch
-    n, dt, rt, dev = x.shape[0], block.torch_dtype, block.real_dtype, x.device
-    shapes = ((n, block.d), (block.channels,))
-    gx, gw = [None if not nd else (torch.empty(sh, dtype=t, device=dev) if o is None else o)
-              for o, nd, sh, t in zip((grad_x, grad_w), need, shapes, (dt, rt))]
-    _same_device(x, w=w, rstd=rstd, grad_u=grad_u, grad_add=grad_add, grad_x=gx, grad_w=gw, workspace=workspace)
-    xp, x_ld = _rows(x, "x", dt, n, block.d)
-    ws, ws_bytes, workspace = _workspace(block, n, workspace, dev, gw is not None)
-    _check(lib().cgtp_norm_backward(block.handle, n, xp, x_ld, _ptr_or_null(w, "w", rt, (block.channels,)),
-                                    _dev(rstd, "rstd", rt, (n,)), _dev(grad_u, "grad_u", dt, (n, block.d)),
-                                    _ptr_or_null(grad_add, "grad_add", dt, (n, block.d)),
-                                    _ptr_or_null(gx, "grad_x", dt, shapes[0]),
-                                    _ptr_or_null(gw, "grad_w", rt, shapes[1]), ws, ws_bytes, _stream(stream, dev)))
+    dev = _device_index(x, "x")
+    n, dt, rt, cs = x.shape[0], block.torch_dtype, block.real_dtype, (block.channels,)
+    rows = (n, block.d)
+    xp, x_ld = _rows(x, "x", dt, rows, dev)
+    gx = None if not need[0] else x.new_empty(rows) if grad_x is None else grad_x
+    gw = None if not need[1] else x.new_empty(cs, dtype=rt) if grad_w is None else grad_w
+    ws, ws_bytes = None, 0
+    if gw is not None:
+        ws, ws_bytes, workspace = _workspace(workspace, "workspace", block_workspace_size(block, n), x, dev)
+    _check(lib().cgtp_norm_backward(block.handle, n, xp, x_ld, _addr_or_null(w, "w", rt, cs, dev),
+                                    _addr(rstd, "rstd", rt, (n,), dev), _addr(grad_u, "grad_u", dt, rows, dev),
+                                    _addr_or_null(grad_add, "grad_add", dt, rows, dev),
+                                    _addr_or_null(gx, "grad_x", dt, rows, dev),
+                                    _addr_or_null(gw, "grad_w", rt, cs, dev), ws, ws_bytes, _raw_stream(stream, dev)))
     return gx, gw
 
 
@@ -777,22 +807,25 @@ def join_forward(block: Block, res, f, gate, w_post, scale, w_next, h=None, u=No
     """(h, u, rstd_f, rstd_h): h = alpha*res + scale*act(gate)*w_post*f*rstd(f), u = h*rstd(h)*w_next.
     f and gate may have a row pitch (both in one buffer, say); weights given as None are ones; what
     the block's configuration leaves out is None."""
-    import torch
-    n, d, dt, rt, dev = f.shape[0], block.d, block.torch_dtype, block.real_dtype, f.device
-    new = lambda t, want, shape, ty: torch.empty(shape, dtype=ty, device=dev) if t is None and want else t  # noqa: E731
-    h, u = new(h, True, (n, d), dt), new(u, block.next_norm, (n, d), dt)
-    rstd_f = new(rstd_f, need_rstd and block.post_norm, n, rt)
-    rstd_h = new(rstd_h, need_rstd and block.next_norm, n, rt)
-    _same_device(f, res=res, gate=gate, w_post=w_post, scale=scale, w_next=w_next, h=h, u=u, rstd_f=rstd_f,
-                 rstd_h=rstd_h)
-    fp, f_ld = _rows(f, "f", dt, n, d)
-    gp, g_ld = _rows_or_null(gate, "gate", dt, n, block.gate_width)
-    cs = (block.channels,)
+    dev = _device_index(f, "f")
+    n, dt, rt, cs = f.shape[0], block.torch_dtype, block.real_dtype, (block.channels,)
+    rows, stat = (n, block.d), (n,)
+    fp, f_ld = _rows(f, "f", dt, rows, dev)
+    gp, g_ld = _rows_or_null(gate, "gate", dt, (n, block.gate_width), dev)
+    if h is None:
+        h = f.new_empty(rows)
+    if u is None and block.next_norm:
+        u = f.new_empty(rows)
+    if rstd_f is None and need_rstd and block.post_norm:
+        rstd_f = f.new_empty(n, dtype=rt)
+    if rstd_h is None and need_rstd and block.next_norm:
+        rstd_h = f.new_empty(n, dtype=rt)
     _check(lib().cgtp_join_forward(
-        block.handle, n, _dev(res, "res", dt, (n, d)), fp, f_ld, gp, g_ld, _ptr_or_null(w_post, "w_post", rt, cs),
-        _ptr_or_null(scale, "scale", rt, cs), _ptr_or_null(w_next, "w_next", rt, cs), _dev(h, "h", dt, (n, d)),
-        _ptr_or_null(u, "u", dt, (n, d)), _ptr_or_null(rstd_f, "rstd_f", rt, (n,)),
-        _ptr_or_null(rstd_h, "rstd_h", rt, (n,)), _stream(stream, dev)))
+        block.handle, n, _addr(res, "res", dt, rows, dev), fp, f_ld, gp, g_ld,
+        _addr_or_null(w_post, "w_post", rt, cs, dev), _addr_or_null(scale, "scale", rt, cs, dev),
+        _addr_or_null(w_next, "w_next", rt, cs, dev), _addr(h, "h", dt, rows, dev),
+        _addr_or_null(u, "u", dt, rows, dev), _addr_or_null(rstd_f, "rstd_f", rt, stat, dev),
+        _addr_or_null(rstd_h, "rstd_h", rt, stat, dev), _raw_stream(stream, dev)))
     return h, u, rstd_f, rstd_h
 
 
@@ -802,29 +835,30 @@ def join_backward(block: Block, grad_h, grad_u, h, f, gate, w_post, scale, w_nex
     (None: zero) and u and the forward's h and statistics; entries not in ``need``, or that the
     block's configuration leaves out, are None and not computed.  grad_f and grad_gate given in
     ``outs`` may have a row pitch."""
-    import torch
-    n, d, dt, rt, dev = f.shape[0], block.d, block.torch_dtype, block.real_dtype, f.device
-    cs, gw = (block.channels,), block.gate_width
-    shapes = ((n, d), (n, d), (n, gw), cs, cs, cs)
-    has = (True, True, gw > 0, block.post_norm, True, block.next_norm)
-    types = (dt, dt, dt, rt, rt, rt)
-    res = [None if not (nd and hs) else (torch.empty(sh, dtype=ty, device=dev) if o is None else o)
-           for o, nd, hs, sh, ty in zip(outs, need, has, shapes, types)]
-    names = ("grad_res", "grad_f", "grad_gate", "grad_w_post", "grad_scale", "grad_w_next")
-    _same_device(f, grad_h=grad_h, grad_u=grad_u, h=h, gate=gate, w_post=w_post, scale=scale, w_next=w_next,
-                 rstd_f=rstd_f, rstd_h=rstd_h, workspace=workspace, **dict(zip(names, res)))
-    fp, f_ld = _rows(f, "f", dt, n, d)
-    gp, g_ld = _rows_or_null(gate, "gate", dt, n, gw)
-    dfp, df_ld = _rows_or_null(res[1], "grad_f", dt, n, d)
-    dgp, dg_ld = _rows_or_null(res[2], "grad_gate", dt, n, gw)
-    ws, ws_bytes, workspace = _workspace(block, n, workspace, dev, any(r is not None for r in res[3:]))
+    dev = _device_index(f, "f")
+    n, dt, rt, cs = f.shape[0], block.torch_dtype, block.real_dtype, (block.channels,)
+    rows, gates, stat = (n, block.d), (n, block.gate_width), (n,)
+    fp, f_ld = _rows(f, "f", dt, rows, dev)
+    gp, g_ld = _rows_or_null(gate, "gate", dt, gates, dev)
+    has = (True, True, block.gate_width > 0, block.post_norm, True, block.next_norm)
+    res = [None] * 6
+    for i, (o, shape) in enumerate(zip(outs, (rows, rows, gates, cs, cs, cs))):
+        if need[i] and has[i]:
+            res[i] = o if o is not None else f.new_empty(shape) if i < 3 else f.new_empty(shape, dtype=rt)
+    gr, gf, gg, gp_, gs, gn = res
+    dfp, df_ld = _rows_or_null(gf, "grad_f", dt, rows, dev)
+    dgp, dg_ld = _rows_or_null(gg, "grad_gate", dt, gates, dev)
+    ws, ws_bytes = None, 0
+    if gp_ is not None or gs is not None or gn is not None:
+        ws, ws_bytes, workspace = _workspace(workspace, "workspace", block_workspace_size(block, n), f, dev)
     _check(lib().cgtp_join_backward(
-        block.handle, n, _ptr_or_null(grad_h, "grad_h", dt, (n, d)), _ptr_or_null(grad_u, "grad_u", dt, (n, d)),
-        _ptr_or_null(h, "h", dt, (n, d)), fp, f_ld, gp, g_ld, _ptr_or_null(w_post, "w_post", rt, cs),
-        _ptr_or_null(scale, "scale", rt, cs), _ptr_or_null(w_next, "w_next", rt, cs),
-        _ptr_or_null(rstd_f, "rstd_f", rt, (n,)), _ptr_or_null(rstd_h, "rstd_h", rt, (n,)),
-        _ptr_or_null(res[0], "grad_res", dt, (n, d)), dfp, df_ld, dgp, dg_ld,
-        *[_ptr_or_null(r, nm, rt, cs) for r, nm in zip(res[3:], names[3:])], ws, ws_bytes, _stream(stream, dev)))
+        block.handle, n, _addr_or_null(grad_h, "grad_h", dt, rows, dev), _addr_or_null(grad_u, "grad_u", dt, rows, dev),
+        _addr_or_null(h, "h", dt, rows, dev), fp, f_ld, gp, g_ld, _addr_or_null(w_post, "w_post", rt, cs, dev),
+        _addr_or_null(scale, "scale", rt, cs, dev), _addr_or_null(w_next, "w_next", rt, cs, dev),
+        _addr_or_null(rstd_f, "rstd_f", rt, stat, dev), _addr_or_null(rstd_h, "rstd_h", rt, stat, dev),
+        _addr_or_null(gr, "grad_res", dt, rows, dev), dfp, df_ld, dgp, dg_ld,
+        _addr_or_null(gp_, "grad_w_post", rt, cs, dev), _addr_or_null(gs, "grad_scale", rt, cs, dev),
+        _addr_or_null(gn, "grad_w_next", rt, cs, dev), ws, ws_bytes, _raw_stream(stream, dev)))
     return tuple(res)
 
 
@@ -897,12 +931,13 @@ class TensorList:
         self.opt, self.tensors = opt, tuple(tensors)
         if len(self.tensors) != len(opt.sizes):
             raise ValueError(f"{len(self.tensors)} tensors, the layout has {len(opt.sizes)}")
+        self._given = [t for t in self.tensors if t is not None]
         self._at = None
-        self.device = next((t.device for t in self.tensors if t is not None), None)
+        self.device_index = _device_index(self._given[0], "tensor") if self._given else None
         self.pointers()
 
     def pointers(self):
-        at = [0 if t is None else t.data_ptr() for t in self.tensors]
+        at = [t.data_ptr() for t in self._given]
         if at != self._at:
             for i, (t, n) in enumerate(zip(self.tensors, self.opt.sizes)):
                 if t is None:
@@ -910,9 +945,10 @@ class TensorList:
                 _dev(t, f"tensor {i}", self.opt.torch_dtype)
                 if t.numel() != n:
                     raise ValueError(f"tensor {i} has {t.numel()} elements, the layout {n}")
-                if t.device != self.device:
-                    raise ValueError(f"tensor {i} is on {t.device}, expected {self.device}")
-            self._array, self._at = (ctypes.c_void_p * max(1, len(at)))(*at), at
+                if t.get_device() != self.device_index:
+                    raise ValueError(f"tensor {i} is on {t.device}, expected cuda:{self.device_index}")
+            every = [None if t is None else t.data_ptr() for t in self.tensors]
+            self._array, self._at = (ctypes.c_void_p * max(1, len(every)))(*every), at
         return self._array
 
 
@@ -933,13 +969,14 @@ def grad_norm(opt: AdamW, grads, norm=None, workspace=None, stream=None):
     float64 tensor of one element."""
     import torch
     grads = _list(opt, grads)
-    dev = grads.device
-    norm = torch.empty(1, dtype=torch.float64, device=dev) if norm is None else norm
-    if workspace is None:
-        workspace = torch.empty(opt.norm_workspace, dtype=torch.uint8, device=dev)
-    _check(lib().cgtp_grad_norm(opt.handle, grads.pointers(), _dev(norm, "norm", torch.float64, (1,)),
-                                _dev(workspace, "workspace"), workspace.numel() * workspace.element_size(),
-                                _stream(stream, dev)))
+    dev = grads.device_index
+    if dev is None:
+        raise ValueError("there is no gradient")
+    like = grads._given[0]
+    norm = like.new_empty(1, dtype=torch.float64) if norm is None else norm
+    ws, ws_bytes, workspace = _workspace(workspace, "workspace", opt.norm_workspace, like, dev)
+    _check(lib().cgtp_grad_norm(opt.handle, grads.pointers(), _addr(norm, "norm", torch.float64, (1,), dev), ws,
+                                ws_bytes, _raw_stream(stream, dev)))
     return norm
 
 
@@ -951,20 +988,18 @@ def adamw_step(opt: AdamW, params, grads, m, v, scales=None, master=None, *, lr=
     in the place of ``step`` and ``lr`` (adamw_schedule advances it)."""
     import torch
     params, grads = _list(opt, params), _list(opt, grads)
-    if any(t is None for t in params.tensors):
+    if len(params._given) != len(opt.sizes):
         raise ValueError("a parameter is None")
-    dev, el, (mt, vt) = params.device, opt.elements, opt.moment_dtypes
-    for name, t in (("gradients", grads), ("m", m), ("v", v), ("scales", scales), ("master", master), ("norm", norm),
-                    ("schedule", schedule)):
-        if t is not None and t.device is not None and t.device != dev:
-            raise ValueError(f"{name} on {t.device}, expected {dev}")
+    dev, el, (mt, vt) = params.device_index, (opt.elements,), opt.moment_dtypes
+    if dev is None or grads.device_index not in (None, dev):
+        raise ValueError("parameters and gradients are not on one device" if params._given else "there is no parameter")
     hyper = AdamWHyper(lr, beta1, beta2, eps, weight_decay, max_norm, grad_scale, step)
     _check(lib().cgtp_adamw_step(
-        opt.handle, params.pointers(), grads.pointers(), _dev(m, "m", mt, (el,)), _dev(v, "v", vt, (el,)),
-        _ptr_or_null(scales, "scales", torch.float32, (2, opt.blocks)),
-        _ptr_or_null(master, "master", torch.float32, (el,)), ctypes.byref(hyper),
-        _ptr_or_null(norm, "norm", torch.float64, (1,)), _ptr_or_null(schedule, "schedule", torch.float64, (4,)),
-        _stream(stream, dev)))
+        opt.handle, params.pointers(), grads.pointers(), _addr(m, "m", mt, el, dev), _addr(v, "v", vt, el, dev),
+        _addr_or_null(scales, "scales", torch.float32, (2, opt.blocks), dev),
+        _addr_or_null(master, "master", torch.float32, el, dev), ctypes.byref(hyper),
+        _addr_or_null(norm, "norm", torch.float64, (1,), dev),
+        _addr_or_null(schedule, "schedule", torch.float64, (4,), dev), _raw_stream(stream, dev)))
 
 
 def adamw_schedule(schedule, beta1=0.9, beta2=0.999, stream=None):

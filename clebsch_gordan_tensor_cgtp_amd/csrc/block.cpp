@@ -5,7 +5,6 @@
 #include <algorithm>
 #include <climits>
 #include <cmath>
-#include <cstdlib>
 #include <memory>
 
 #include "abi_util.h"
@@ -21,12 +20,6 @@ namespace {
 
 constexpr int kLds = 160 * 1024;  // bytes of a workgroup
 
-int tuned(const char *name, int otherwise)
-{
-    const char *e = std::getenv(name);
-    return e && *e ? std::atoi(e) : otherwise;
-}
-
 const char *type_name(int dtype)
 {
     switch (dtype) {
@@ -37,44 +30,50 @@ const char *type_name(int dtype)
     }
 }
 
-// Lanes per row: the power of two that leaves the fewest of a row's 16-byte chunk slots empty with
-// at most `most` chunks to a lane (more lanes where two are within a twentieth); rows that a
-// wave cannot hold so are shared by the waves of one workgroup.
+// The lanes' share of a row: G lanes, CV neighbouring channels (columns in a flat layout) to a slot.
+// Of every pair, the cost of a row in lane operations is taken: its lanes times a lane's elements,
+// which idle lanes and channels past an irrep's end raise, more where loads are narrow (below 16 bytes
+// in a flat layout, below 8 in runs of channels, which are neighbours in the same cache lines), where a
+// lane holds over 16 words (fewer waves fit a SIMD), and where waves must meet at barriers; the most
+// lanes of equal cost.  The weights are fitted to times of 12 shapes at 3 to 9 pairs each.  The join's
+// backward, fp32: 20,000 rows of 128x(0e,1o,2e,3o), 64 lanes of 32 elements 210 us, 128 of 16 201 us, 512
+// of 16, half idle, 216 us; 5,000 rows of 32x(0e,1o,2e), 32 lanes of 9 13.7 us, 16 of 18 15.9 us.  The
+// norm, 200,000 flat rows of 65 in fp16: 4 lanes of 9 loads of 4 bytes 25.7 us, of 3 loads of 16 11.7 us.
 void pick_lanes(Block &b)
 {
-    const int k = (b.d + b.vec - 1) / b.vec;
-    const int most = std::max(1, std::min(8, tuned("CGTP_BLOCK_CHUNKS", 4)));
-    b.lanes = 0;
     double best = 0;
-    for (int g = 64; g >= 1; g /= 2) {
-        const int nv = (k + g - 1) / g;
-        if (nv > most) break;
-        const double used = (double)k / ((double)g * nv);
-        if (b.lanes == 0 || used > best + 0.05) {
-            b.lanes = g;
-            best = used;
+    const int64_t most = 128;  // elements of a lane
+    b.lanes = 0;
+    for (int cv = 1; cv <= b.vec; cv *= 2)
+        for (int g = 1; g <= 1024; g *= 2) {
+            int64_t elems = 0, bytes = 0;
+            for (const Block::Segment &s : b.slots_over()) {
+                const int64_t slots = ((s.mul + cv - 1) / cv + g - 1) / g;
+                const int run = cv * s.k;
+                elems += slots * run;
+                bytes += slots * (run / b.vec) * 16;  // by loads, none below 8 bytes
+                for (int piece = b.vec / 2; piece >= 1; piece /= 2)
+                    if (run & piece) bytes += slots * std::max(b.flat ? 16 : 8, piece * b.elem);
+            }
+            if (elems > most) continue;
+            const double words = (double)elems * b.real / 4;
+            double cost = (double)g * elems / b.d;
+            cost *= 1 + 0.02 * std::max(0.0, words - 16);
+            cost *= 1 + (b.flat ? 0.3 : 0.1) * ((double)bytes / (elems * b.elem) - 1);
+            if (g > 64) cost *= 1 + 0.04 * std::log2(g / 64);
+            if (b.lanes == 0 || cost <= best) {
+                best = cost;
+                b.lanes = g;
+                b.cv = cv;
+                b.elems = (int)elems;
+            }
         }
-    }
-    if (b.lanes == 0) {
-        for (int g = 128; g <= 1024 && b.lanes == 0; g *= 2)
-            if ((k + g - 1) / g <= most) b.lanes = g;
-        if (b.lanes == 0) b.lanes = 1024;
-    }
-    b.chunks = (k + b.lanes - 1) / b.lanes;
+    if (b.lanes == 0)
+        throw Error(CGTP_ERR_UNSUPPORTED, "block: a lane would hold more than 128 elements of a row (too many columns, "
+                                          "or too many changes of degree)");
     b.block = b.lanes > 64 ? b.lanes : 256;
-    if (b.chunks > 8)
-        throw Error(CGTP_ERR_UNSUPPORTED, "block: a row of " + std::to_string(b.d) + " columns exceeds " +
-                                              std::to_string(1024 * 8 * b.vec) + " for this dtype");
-}
-
-void check_lds(const Block &b)
-{
-    const long dp = (long)((b.d + b.vec - 1) / b.vec) * b.vec, cp = (long)((b.c + b.vec - 1) / b.vec) * b.vec;
-    const bool scalar = b.d == b.c;
-    const long rows = b.rows_per_group();
-    long bytes = 2 * std::max(1, b.lanes / 64) * b.real;
-    if (!scalar || rows > 1) bytes += rows * dp * b.real;
-    if (!scalar && b.cfg.gate == CGTP_GATE_CHANNEL) bytes += rows * cp * b.real;
+    const long sums = b.lanes > 64 ? 1 : b.block / 64;
+    const long bytes = 2L * std::max(1, b.lanes / 64) * b.real + (sums > 1 || b.flat ? sums * (b.flat ? b.d : b.c) * b.real : 0);
     if (bytes > kLds)
         throw Error(CGTP_ERR_UNSUPPORTED, "block: the sums over a row's channels need " + std::to_string(bytes) +
                                               " bytes of LDS, a workgroup has 163840");
@@ -92,21 +91,49 @@ std::string constants(const Block &b)
     num("C", b.c);
     num("VEC", b.vec);
     num("G", b.lanes);
-    num("NV", b.chunks);
+    num("CV", b.cv);
     num("BLOCK", b.block);
     num("GATE", b.cfg.gate);
     num("ACT", b.cfg.act);
     num("POST", b.cfg.post_norm ? 1 : 0);
     num("NEXT", b.cfg.next_norm ? 1 : 0);
-    num("NSEG", (long)b.segs.size());
-    auto list = [&](const char *n, int Block::Segment::*f) {
-        std::string t = std::string("constexpr int ") + n + "[NSEG] = {";
-        for (size_t i = 0; i < b.segs.size(); ++i) t += (i ? ", " : "") + std::to_string(b.segs[i].*f);
-        line(t + "};");
+    std::string col, ch, k, mul, unit, at, of;
+    int slots = 0, elems = 0;
+    auto add = [](std::string &t, int v) { t += (t.empty() ? "" : ", ") + std::to_string(v); };
+    for (const Block::Segment &g : b.slots_over())
+        for (int u = 0; u * b.cv < g.mul; u += b.lanes, ++slots) {
+            add(col, g.col);
+            add(ch, g.ch);
+            add(k, g.k);
+            add(mul, g.mul);
+            add(unit, u);
+            add(at, elems);
+            for (int i = 0; i < b.cv * g.k; ++i) add(of, slots * b.cv + i / g.k);
+            elems += b.cv * g.k;
+        }
+    num("NSLOT", slots);
+    num("EPL", elems);
+    auto list = [&](const char *n, const char *len, const std::string &v) {
+        line(std::string("constexpr int ") + n + "[" + len + "] = {" + v + "};");
     };
-    list("SEG_COL", &Block::Segment::col);
-    list("SEG_CH", &Block::Segment::ch);
-    list("SEG_K", &Block::Segment::k);
+    list("S_COL", "NSLOT", col);
+    list("S_CH", "NSLOT", ch);
+    list("S_K", "NSLOT", k);
+    list("S_MUL", "NSLOT", mul);
+    list("S_UNIT", "NSLOT", unit);
+    list("S_AT", "NSLOT", at);
+    list("E_C", "EPL", of);
+    line(std::string("constexpr bool FLAT = ") + (b.flat ? "true;" : "false;"));
+    num("NSEG", (long)b.segs.size());
+    std::string gcol, gch, gk;
+    for (const Block::Segment &g : b.segs) {
+        add(gcol, g.col);
+        add(gch, g.ch);
+        add(gk, g.k);
+    }
+    list("G_COL", "NSEG", gcol);
+    list("G_CH", "NSEG", gch);
+    list("G_K", "NSEG", gk);
     return s;
 }
 
@@ -117,20 +144,19 @@ void build_block(Block &b, const std::string &irreps)
     int64_t col = 0, ch = 0;
     for (const Irrep &ir : parse_irreps(irreps, "block")) {
         const int k = 2 * ir.l + 1;
-        if (b.segs.empty() || b.segs.back().k != k) b.segs.push_back({(int)col, (int)ch, k});
+        if (b.segs.empty() || b.segs.back().k != k) b.segs.push_back({(int)col, (int)ch, k, 0});
+        b.segs.back().mul += ir.mul;
         col += (int64_t)ir.mul * k;
         ch += ir.mul;
         if (col > (1 << 20)) throw Error(CGTP_ERR_UNSUPPORTED, "block: a row of more than 1048576 columns");
     }
-    if (b.segs.size() > 64)
-        throw Error(CGTP_ERR_UNSUPPORTED, "block: more than 64 changes of degree along a row");
     b.d = (int)col;
     b.c = (int)ch;
     b.elem = b.cfg.dtype == CGTP_F64 ? 8 : b.cfg.dtype == CGTP_F32 ? 4 : 2;
     b.real = b.cfg.dtype == CGTP_F64 ? 8 : 4;
     b.vec = 16 / b.elem;
+    b.flat = b.d != b.c && b.cfg.gate != CGTP_GATE_CHANNEL;
     pick_lanes(b);
-    check_lds(b);
     b.source = constants(b) + kBlockKernels;
     b.code = compile_source(b.source);
 }
@@ -163,18 +189,13 @@ void unload_block(Block &b)
     if (have_prev) (void)hipSetDevice(prev);
 }
 
-int64_t block_forward_groups(const Block &b, int64_t N)
+// At most two waves to each of the 1,024 SIMDs, which then take rows in turn: the weights are read and
+// the partial sums written once by each (the join's backward, 200,000 rows of 64x(0e,1o,2e) bf16: 345, 289,
+// 304, 313 us at 1, 2, 4, 8 waves to a SIMD; the norm's, 8,192 rows of 4,096 bf16: 54, 43, 45, 53 us).
+int64_t block_groups(const Block &b, int64_t N)
 {
     const int64_t rows = b.rows_per_group();
-    const int64_t most = (int64_t)tuned("CGTP_BLOCK_FWD_WAVES", 8192) / (b.block / 64);
-    return std::max<int64_t>(1, std::min((N + rows - 1) / rows, most));
-}
-
-int64_t block_backward_groups(const Block &b, int64_t N)
-{
-    const int64_t rows = b.rows_per_group();
-    const int64_t most = (int64_t)tuned("CGTP_BLOCK_BWD_WAVES", 4096) / (b.block / 64);
-    return std::max<int64_t>(1, std::min((N + rows - 1) / rows, most));
+    return std::max<int64_t>(1, std::min<int64_t>((N + rows - 1) / rows, 2048 / (b.block / 64)));
 }
 
 namespace {
@@ -238,12 +259,12 @@ void reduce_partials(const Block &b, const Block::Fns &F, const void *part, int6
     int is_join = join ? 1 : 0;
     int width = b.c * (join && b.cfg.next_norm ? 2 : 1);
     void *args[] = {&part, &rows, &width, &is_join, &w_post, &scale, &g_post, &g_scale, &g_next};
-    run(F.reduce, (width + 63) / 64, 1024, args, stream);
+    run(F.reduce, (width + 15) / 16, 1024, args, stream);
 }
 
 size_t workspace_bytes_of(const Block &b, int64_t N)
 {
-    return N == 0 ? 0 : (size_t)block_backward_groups(b, N) * b.c * (b.cfg.next_norm ? 2 : 1) * b.real;
+    return N == 0 ? 0 : (size_t)block_groups(b, N) * b.c * (b.cfg.next_norm ? 2 : 1) * b.real;
 }
 
 // scalars passed to a kernel as its statistics' type
@@ -302,7 +323,7 @@ cgtp_status cgtp_block_info_get(const cgtp_block *block, cgtp_block_info *info)
         info->gate_width = b.gate_width();
         info->dtype = b.cfg.dtype;
         info->lanes = b.lanes;
-        info->chunks = b.chunks;
+        info->elements = b.elems;
     });
 }
 
@@ -340,7 +361,7 @@ cgtp_status cgtp_norm_forward(const cgtp_block *block, int64_t N, const void *x,
         long ld = (long)x_ld, rows = (long)N;
         Real eps(b, b.cfg.eps);
         void *args[] = {&x, &ld, &w, &u, &rstd, &rows, eps.arg()};
-        run(F.norm_fwd, block_forward_groups(b, N), b.block, args, stream);
+        run(F.norm_fwd, block_groups(b, N), b.block, args, stream);
     });
 }
 
@@ -371,7 +392,7 @@ cgtp_status cgtp_norm_backward(const cgtp_block *block, int64_t N, const void *x
         require_ptr(rstd, "rstd", b.real);
         size_t need = 0;
         if (grad_w) {
-            need = (size_t)block_backward_groups(b, N) * nw;
+            need = (size_t)block_groups(b, N) * nw;
             require_ptr(workspace, "workspace", 256);
             require(workspace_bytes >= need, "workspace too small (see cgtp_block_workspace_size)");
         }
@@ -391,7 +412,7 @@ cgtp_status cgtp_norm_backward(const cgtp_block *block, int64_t N, const void *x
         long ld = (long)x_ld, rows = (long)N;
         void *part = grad_w ? workspace : nullptr;
         void *args[] = {&x, &ld, &w, &rstd, &grad_u, &grad_add, &grad_x, &part, &rows};
-        const int64_t groups = block_backward_groups(b, N);
+        const int64_t groups = block_groups(b, N);
         run(F.norm_bwd, groups, b.block, args, stream);
         if (grad_w)
             reduce_partials(b, F, part, groups, false, nullptr, nullptr, nullptr, nullptr, grad_w, stream);
@@ -442,7 +463,7 @@ cgtp_status cgtp_join_forward(const cgtp_block *block, int64_t N, const void *re
         Real alpha(b, b.cfg.alpha), eps(b, b.cfg.eps);
         void *args[] = {&res, &f, &fl, &gate, &gl, &w_post, &scale, &w_next, &h, &u, &rstd_f, &rstd_h, &rows,
                         alpha.arg(), eps.arg()};
-        run(F.join_fwd, block_forward_groups(b, N), b.block, args, stream);
+        run(F.join_fwd, block_groups(b, N), b.block, args, stream);
     });
 }
 
@@ -525,7 +546,7 @@ cgtp_status cgtp_join_backward(const cgtp_block *block, int64_t N, const void *g
         Real alpha(b, b.cfg.alpha);
         void *args[] = {&grad_h, &grad_u, &h, &f, &fl, &gate, &gl, &w_post, &scale, &w_next, &rstd_f, &rstd_h, &grad_res,
                         &grad_f, &dfl, &grad_gate, &dgl, &part, &rows, alpha.arg()};
-        const int64_t groups = block_backward_groups(b, N);
+        const int64_t groups = block_groups(b, N);
         run(F.join_bwd, groups, b.block, args, stream);
         if (weights)
             reduce_partials(b, F, part, groups, true, w_post, scale, grad_w_post, grad_scale, grad_w_next, stream);

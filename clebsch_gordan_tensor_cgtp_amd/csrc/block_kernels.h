@@ -3,13 +3,19 @@
 // plan's constants in front of this text and compiles it for gfx950.
 //
 // Constants of a plan:
-//   T, R        element type in memory; type of statistics, weights and sums (float, or double)
-//   D, C        columns and channels of a row
-//   VEC, G, NV  elements of a 16-byte chunk; lanes that share a row; chunks of a lane
-//   BLOCK       threads of a workgroup
-//   NSEG, SEG_COL, SEG_CH, SEG_K   irreps of equal degree: first column, first channel, 2l+1
-//   GATE, ACT   0 none, 1 one logit per row, 2 one per channel; 0 identity 1 sigmoid 2 silu 3 tanh
-//   POST, NEXT  norm after the block; norm of the next block
+//   T, R         element type in memory; type of statistics, weights and sums (float, or double)
+//   D, C         columns and channels of a row
+//   VEC          elements of 16 bytes
+//   G, BLOCK     lanes that share a row; threads of a workgroup
+//   CV           neighbouring channels that a lane takes together
+//   GATE, ACT    0 none, 1 one logit per row, 2 one per channel; 0 identity 1 sigmoid 2 silu 3 tanh
+//   POST, NEXT   norm after the block; norm of the next block
+//   NSLOT, S_*   a lane's slots, each CV channels of one irrep (neighbouring irreps of equal degree are
+//                one): S_COL, S_CH the irrep's first column and channel, S_K = 2l+1, S_MUL its channels,
+//                S_UNIT lane 0's first group of CV channels, S_AT the slot's first element in the lane
+//   EPL, E_C     elements of a lane; the lane's channel (of NSLOT x CV) that each belongs to
+//   FLAT         the slots are over columns, as if each were a channel (S_K = 1, S_MUL = D): rows without a
+//                gate per channel.  NSEG, G_*: the irreps themselves, of which weights are gathered
 #pragma once
 
 namespace cgtp {
@@ -17,97 +23,163 @@ namespace cgtp {
 static const char kBlockKernels[] = R"HIP(
 #define DEV static __device__ __forceinline__
 
-constexpr int CHUNKS = (D + VEC - 1) / VEC;        // chunks of a row, the last one perhaps short
-constexpr int FULL = D / VEC, TAIL = D % VEC;
-constexpr int CCHUNKS = (C + VEC - 1) / VEC;       // the same of a row of channels
-constexpr int CFULL = C / VEC, CTAIL = C % VEC;
-constexpr int NVC = (CCHUNKS + G - 1) / G;
+constexpr int NC = NSLOT * CV;
 constexpr int NW = G > 64 ? G / 64 : 1;            // waves that share a row
 constexpr int RPB = BLOCK / G;                     // rows of a workgroup at a time (1 when NW > 1)
-constexpr int DP = CHUNKS * VEC, CP = CCHUNKS * VEC;
-constexpr bool SCALAR = D == C;                    // every irrep has l = 0: a column is a channel
-constexpr bool STAGED = GATE == 2 && !SCALAR;      // the gate goes through LDS
-
-typedef T Raw __attribute__((ext_vector_type(VEC), aligned(sizeof(T))));
-typedef R RawR __attribute__((ext_vector_type(VEC), aligned(sizeof(R))));
 
 // ---------------------------------------------------------------- rows in registers
-// Lane `lane` of a row's G lanes holds chunks lane, lane + G, ...: every load is 16 bytes and the
-// row's lanes read consecutive ones.  Rows start at any element, so the vector types claim no
-// more than the element's alignment.  Columns past the row's end read as 0 and are not written.
+// With a gate per channel, a lane holds whole channels, all components of each: CV neighbouring
+// channels of 2l+1 components are one run of memory, the runs of the row's lanes follow one another, and
+// what is per channel (weights, gates, their gradients) meets its components in the lane's own
+// registers.  Dealing columns to the lanes and passing gates and their gradients through LDS took 775
+// us for the join's backward on 200,000 rows of 64x(0e,1o,2e) in bf16, this 289 us.  Without such a
+// gate columns are dealt (FLAT): every load is as wide as it can be, and weights are spread over columns once
+// per workgroup (norm, 20,000 rows of 128x(0e,1o,2e,3o) in fp64: 116 us, 136 us by channels).
+// Rows start at any element, so the vector types claim no more than the element's alignment.
+// Channels past an irrep's end read as 0 and are not written.
 
-template <int N, int NFULL, int NTAIL, typename S> DEV void load_row(const S *row, int lane, R (&x)[N][VEC])
+template <int N, typename S> DEV void load_run(const S *p, R *x)
 {
-    typedef S V __attribute__((ext_vector_type(VEC), aligned(sizeof(S))));
-#pragma unroll
-    for (int j = 0; j < N; ++j) {
-        const int k = lane + G * j;
-        if (G * (j + 1) <= NFULL || k < NFULL) {
-            const V r = *reinterpret_cast<const V *>(row + k * VEC);
-#pragma unroll
-            for (int i = 0; i < VEC; ++i) x[j][i] = (R)r[i];
+    if constexpr (N > 0) {
+        constexpr int W = 16 / sizeof(S);
+        constexpr int n = N >= W ? W : N >= 8 ? 8 : N >= 4 ? 4 : N >= 2 ? 2 : 1;
+        typedef S V __attribute__((ext_vector_type(n), aligned(sizeof(S))));
+        if constexpr (n == 1) {
+            x[0] = (R)p[0];
         } else {
+            const V r = *reinterpret_cast<const V *>(p);
 #pragma unroll
-            for (int i = 0; i < VEC; ++i) x[j][i] = (NTAIL > i && k == NFULL) ? (R)row[k * VEC + i] : (R)0;
+            for (int i = 0; i < n; ++i) x[i] = (R)r[i];
         }
+        load_run<N - n>(p + n, x + n);
     }
 }
 
-template <int N, int NFULL, int NTAIL> DEV void store_row(T *row, int lane, const R (&x)[N][VEC])
+template <int N, typename S> DEV void store_run(S *p, const R *x)
 {
+    if constexpr (N > 0) {
+        constexpr int W = 16 / sizeof(S);
+        constexpr int n = N >= W ? W : N >= 8 ? 8 : N >= 4 ? 4 : N >= 2 ? 2 : 1;
+        typedef S V __attribute__((ext_vector_type(n), aligned(sizeof(S))));
+        if constexpr (n == 1) {
+            p[0] = (S)x[0];
+        } else {
+            V r;
 #pragma unroll
-    for (int j = 0; j < N; ++j) {
-        const int k = lane + G * j;
-        if (G * (j + 1) <= NFULL || k < NFULL) {
-            Raw r;
-#pragma unroll
-            for (int i = 0; i < VEC; ++i) r[i] = (T)x[j][i];
-            *reinterpret_cast<Raw *>(row + k * VEC) = r;
-        } else if (NTAIL > 0 && k == NFULL) {
-#pragma unroll
-            for (int i = 0; i < NTAIL; ++i) row[k * VEC + i] = (T)x[j][i];
+            for (int i = 0; i < n; ++i) r[i] = (S)x[i];
+            *reinterpret_cast<V *>(p) = r;
         }
+        store_run<N - n>(p + n, x + n);
     }
 }
 
-#define LOAD_COLS(p, x) load_row<NV, FULL, TAIL>(p, lane, x)
-#define STORE_COLS(p, x) store_row<NV, FULL, TAIL>(p, lane, x)
-#define LOAD_CHANNELS(p, x) load_row<NVC, CFULL, CTAIL>(p, lane, x)
-#define STORE_CHANNELS(p, x) store_row<NVC, CFULL, CTAIL>(p, lane, x)
-#define EACH(N, j, i) _Pragma("unroll") for (int j = 0; j < (N); ++j) _Pragma("unroll") for (int i = 0; i < VEC; ++i)
+// slot J of a row of K-component channels (columns), or of one value per channel (K = 1)
+template <int J, int K, typename S> DEV void load_slot(const S *irrep, int lane, R *x)
+{
+    const int unit = S_UNIT[J] + lane, left = S_MUL[J] - unit * CV;
+    const S *p = irrep + unit * (CV * K);
+    if ((S_UNIT[J] + G) * CV <= S_MUL[J] || left >= CV) {
+        load_run<CV * K>(p, x);
+    } else {
+#pragma unroll
+        for (int i = 0; i < CV * K; ++i) x[i] = (CV > 1 && i < left * K) ? (R)p[i] : (R)0;
+    }
+}
 
-// channel of a column (of the last one for columns past the end), first column of a channel
+template <int J, int K, typename S> DEV void store_slot(S *irrep, int lane, const R *x)
+{
+    const int unit = S_UNIT[J] + lane, left = S_MUL[J] - unit * CV;
+    S *p = irrep + unit * (CV * K);
+    if ((S_UNIT[J] + G) * CV <= S_MUL[J] || left >= CV) {
+        store_run<CV * K>(p, x);
+    } else if (CV > 1) {
+#pragma unroll
+        for (int i = 0; i < CV * K; ++i)
+            if (i < left * K) p[i] = (S)x[i];
+    }
+}
+
+template <int J = 0> DEV void load_cols(const T *row, int lane, R (&x)[EPL])
+{
+    if constexpr (J < NSLOT) {
+        load_slot<J, S_K[J]>(row + S_COL[J], lane, x + S_AT[J]);
+        load_cols<J + 1>(row, lane, x);
+    }
+}
+
+template <int J = 0> DEV void store_cols(T *row, int lane, const R (&x)[EPL])
+{
+    if constexpr (J < NSLOT) {
+        store_slot<J, S_K[J]>(row + S_COL[J], lane, x + S_AT[J]);
+        store_cols<J + 1>(row, lane, x);
+    }
+}
+
+template <int J = 0, typename S> DEV void load_channels(const S *row, int lane, R (&c)[NC])
+{
+    if constexpr (J < NSLOT) {
+        load_slot<J, 1>(row + S_CH[J], lane, c + J * CV);
+        load_channels<J + 1>(row, lane, c);
+    }
+}
+
+template <int J = 0, typename S> DEV void store_channels(S *row, int lane, const R (&c)[NC])
+{
+    if constexpr (J < NSLOT) {
+        store_slot<J, 1>(row + S_CH[J], lane, c + J * CV);
+        store_channels<J + 1>(row, lane, c);
+    }
+}
+
+#define EACH_E(i) _Pragma("unroll") for (int i = 0; i < EPL; ++i)
+#define EACH_C(c) _Pragma("unroll") for (int c = 0; c < NC; ++c)
+
+// channel of a column; first column and columns of a channel
 DEV int channel_of(int col)
 {
-    col = col < D ? col : D - 1;
     int ch = 0;
 #pragma unroll
     for (int s = 0; s < NSEG; ++s)
-        if (col >= SEG_COL[s]) ch = SEG_CH[s] + (col - SEG_COL[s]) / SEG_K[s];
+        if (col >= G_COL[s]) ch = G_CH[s] + (col - G_COL[s]) / G_K[s];
     return ch;
 }
 
 DEV void columns_of(int c, int &col, int &k)
 {
-    col = 0;
-    k = 1;
 #pragma unroll
     for (int s = 0; s < NSEG; ++s)
-        if (c >= SEG_CH[s]) {
-            k = SEG_K[s];
-            col = SEG_COL[s] + (c - SEG_CH[s]) * k;
+        if (c >= G_CH[s]) {
+            k = G_K[s];
+            col = G_COL[s] + (c - G_CH[s]) * k;
         }
 }
 
-// w[channel of the column], 1 without weights
-DEV void load_weights(const R *w, int lane, R (&x)[NV][VEC])
+// w of the lane's channels (columns where FLAT), 1 without weights
+DEV void load_weights(const R *w, int lane, R (&x)[NC])
 {
-    if (!w) {
-        EACH(NV, j, i) x[j][i] = (R)1;
-    } else if (SCALAR) {
-        LOAD_COLS(w, x);
+    if (w && FLAT) {
+#pragma unroll
+        for (int j = 0; j < NSLOT; ++j)
+#pragma unroll
+            for (int v = 0; v < CV; ++v) {
+                const int col = (S_UNIT[j] + lane) * CV + v;
+                x[j * CV + v] = col < D ? w[channel_of(col)] : (R)0;
+            }
+    } else if (w) {
+        load_channels(w, lane, x);
     } else {
-        EACH(NV, j, i) x[j][i] = w[channel_of((lane + G * j) * VEC + i)];
+        EACH_C(c) x[c] = (R)1;
+    }
+}
+
+// scale[c] w_post[c], each 1 where it is not given
+DEV void load_scale(const R *scale, const R *w_post, int lane, R (&x)[NC])
+{
+    load_weights(scale, lane, x);
+    if (POST && w_post) {
+        R y[NC];
+        load_weights(w_post, lane, y);
+        EACH_C(c) x[c] *= y[c];
     }
 }
 
@@ -172,17 +244,6 @@ DEV R lane_sum(R v)
     return v;
 }
 
-// LDS written by this row's lanes becomes readable by them
-DEV void row_sync()
-{
-    if (NW > 1) {
-        __syncthreads();
-    } else {
-        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-        __builtin_amdgcn_wave_barrier();
-    }
-}
-
 // Sum over the row's lanes, the same in all of them.  Waves that share a row exchange theirs
 // through LDS with one barrier: consecutive sums take alternate halves of `red`, and a half is
 // written again only after the other half's barrier, which every wave reaches after its reads.
@@ -201,54 +262,45 @@ DEV R row_sum(R v, R *red, int &turn)
 }
 
 // ---------------------------------------------------------------- partial weight gradients
-// acc (per column) of the workgroup's row groups, summed group by group and over each channel's
-// columns into out[C]; lds holds RPB x DP elements.
-DEV void partial_from_columns(const R (&acc)[NV][VEC], int lane, int group, R *lds, R *out)
+// A workgroup's sums per channel into out[C]: a wave's row groups are added by lane exchanges, its
+// waves one after the other through LDS; where waves share a row each lane has the whole sum of its
+// channels already.  FLAT: a channel's columns are added on the way out of LDS.
+constexpr int SUMS = NW > 1 ? 1 : BLOCK / 64;
+constexpr int WIDTH = FLAT ? D : C;
+constexpr int SUM_LDS = SUMS == 1 && !FLAT ? 1 : SUMS * WIDTH;
+
+DEV void write_partial(R (&acc)[NC], int lane, R *lds, R *out)
 {
-    if (SCALAR && RPB == 1) {
-        EACH(NV, j, i)
-        {
-            const int col = (lane + G * j) * VEC + i;
-            if (col < C) out[col] = acc[j][i];
-        }
+#pragma unroll
+    for (int s = G; s < 64; s *= 2) EACH_C(c) acc[c] += __shfl_xor(acc[c], s);
+    if (SUMS == 1 && !FLAT) {
+        store_channels(out, lane, acc);
         return;
     }
     __syncthreads();
-    EACH(NV, j, i)
-    {
-        const int col = (lane + G * j) * VEC + i;
-        if (col < DP) lds[group * DP + col] = acc[j][i];
-    }
+    if (NW > 1)
+        store_channels(lds, lane, acc);
+    else if ((threadIdx.x & 63) < G)
+        store_channels(lds + (threadIdx.x >> 6) * WIDTH, lane, acc);
     __syncthreads();
     for (int c = threadIdx.x; c < C; c += BLOCK) {
-        int col, k;
-        columns_of(c, col, k);
+        int col = c, k = 1;
+        if (FLAT) columns_of(c, col, k);
         R s = 0;
-        for (int g = 0; g < RPB; ++g)
-            for (int m = 0; m < k; ++m) s += lds[g * DP + col + m];
-        out[c] = s;
-    }
-}
-
-// the same for sums that are per channel already; lds holds RPB x CP elements
-DEV void partial_from_channels(const R (&acc)[NVC][VEC], int lane, int group, R *lds, R *out)
-{
-    __syncthreads();
-    EACH(NVC, j, i)
-    {
-        const int c = (lane + G * j) * VEC + i;
-        if (c < CP) lds[group * CP + c] = acc[j][i];
-    }
-    __syncthreads();
-    for (int c = threadIdx.x; c < C; c += BLOCK) {
-        R s = 0;
-        for (int g = 0; g < RPB; ++g) s += lds[g * CP + c];
+        for (int m = 0; m < k; ++m)
+#pragma unroll
+            for (int w = 0; w < SUMS; ++w) s += lds[w * WIDTH + col + m];
         out[c] = s;
     }
 }
 
 // ---------------------------------------------------------------- the gate
-DEV float exp_of(float v) { return expf(v); }
+// Rows of 16 bits take the hardware's exponential and reciprocal: their errors, |g| 2^-23 and 2^-23, are
+// far below a rounding to 16 bits (the join's backward, 8,192 scalar rows
+// of 4,096 in bf16 with a SiLU gate: 131 us with expf and a division, 116 us).
+DEV float exp_of(float v) { return sizeof(T) == 2 ? __builtin_amdgcn_exp2f(v * 1.44269504f) : expf(v); }
+DEV float inverse(float v) { return sizeof(T) == 2 ? __builtin_amdgcn_rcpf(v) : 1.0f / v; }
+DEV double inverse(double v) { return 1.0 / v; }
 DEV double exp_of(double v) { return exp(v); }
 DEV float tanh_of(float v) { return tanhf(v); }
 DEV double tanh_of(double v) { return tanh(v); }
@@ -259,7 +311,7 @@ DEV R gate_value(R g)
 {
     if (ACT == 0) return g;
     if (ACT == 3) return tanh_of(g);
-    const R s = (R)1 / ((R)1 + exp_of(-g));
+    const R s = inverse((R)1 + exp_of(-g));
     return ACT == 1 ? s : g * s;
 }
 
@@ -273,29 +325,9 @@ DEV R gate_slope(R g, R &value)
         value = tanh_of(g);
         return (R)1 - value * value;
     }
-    const R s = (R)1 / ((R)1 + exp_of(-g));
+    const R s = inverse((R)1 + exp_of(-g));
     value = ACT == 1 ? s : g * s;
     return ACT == 1 ? s * ((R)1 - s) : s * ((R)1 + g * ((R)1 - s));
-}
-
-// scale[c] * w_post[c], each 1 where it is not given
-DEV void load_channel_scale(const R *scale, const R *w_post, int lane, R (&x)[NVC][VEC])
-{
-    EACH(NVC, j, i)
-    {
-        const int c = (lane + G * j) * VEC + i;
-        x[j][i] = c < C ? (scale ? scale[c] : (R)1) * (POST && w_post ? w_post[c] : (R)1) : (R)0;
-    }
-}
-
-DEV void load_column_scale(const R *scale, const R *w_post, int lane, R (&x)[NV][VEC])
-{
-    load_weights(scale, lane, x);
-    if (POST && w_post) {
-        R y[NV][VEC];
-        load_weights(w_post, lane, y);
-        EACH(NV, j, i) x[j][i] *= y[j][i];
-    }
 }
 
 #define ROW_SETUP                                                       \
@@ -316,17 +348,17 @@ cgtp_norm_fwd(const T *__restrict__ x, long x_ld, const R *__restrict__ w, T *__
               long N, R eps)
 {
     ROW_SETUP
-    R wc[NV][VEC];
+    R wc[NC];
     load_weights(w, lane, wc);
     EACH_ROW(n, on)
     {
-        R v[NV][VEC], ss = 0;
-        LOAD_COLS(x + n * x_ld, v);
-        EACH(NV, j, i) ss += v[j][i] * v[j][i];
+        R v[EPL], ss = 0;
+        load_cols(x + n * x_ld, lane, v);
+        EACH_E(i) ss += v[i] * v[i];
         const R r = root_inverse(row_sum(ss, red, turn) / (R)D + eps);
-        EACH(NV, j, i) v[j][i] = v[j][i] * r * wc[j][i];
+        EACH_E(i) v[i] = v[i] * r * wc[E_C[i]];
         if (on) {
-            STORE_COLS(u + n * D, v);
+            store_cols(u + n * D, lane, v);
             if (rstd && lane == 0) rstd[n] = r;
         }
     }
@@ -338,40 +370,44 @@ cgtp_norm_bwd(const T *__restrict__ x, long x_ld, const R *__restrict__ w, const
               const T *__restrict__ du, const T *__restrict__ add, T *__restrict__ dx, R *__restrict__ part, long N)
 {
     ROW_SETUP
-    R wc[NV][VEC], acc[NV][VEC];
+    R wc[NC], acc[NC];
     load_weights(w, lane, wc);
-    EACH(NV, j, i) acc[j][i] = 0;
+    EACH_C(c) acc[c] = 0;
     EACH_ROW(n, on)
     {
-        R y[NV][VEC], q[NV][VEC], dot = 0;
-        LOAD_COLS(x + n * x_ld, y);
-        LOAD_COLS(du + n * D, q);
+        R y[EPL], q[EPL], t[NC], dot = 0;
+        load_cols(x + n * x_ld, lane, y);
+        load_cols(du + n * D, lane, q);
         const R r = rstd[n];
-        EACH(NV, j, i)
+        EACH_C(c) t[c] = 0;
+        EACH_E(i)
         {
-            y[j][i] *= r;
-            if (part && on) acc[j][i] += q[j][i] * y[j][i];
-            q[j][i] *= wc[j][i];
-            dot += q[j][i] * y[j][i];
+            y[i] *= r;
+            t[E_C[i]] += q[i] * y[i];
+            q[i] *= wc[E_C[i]];
+        }
+        EACH_C(c)
+        {
+            if (part && on) acc[c] += t[c];
+            dot += t[c] * wc[c];
         }
         if (!dx) continue;
         dot = row_sum(dot, red, turn) / (R)D;
-        EACH(NV, j, i) q[j][i] = r * (q[j][i] - y[j][i] * dot);
+        EACH_E(i) q[i] = r * (q[i] - y[i] * dot);
         if (add) {
-            LOAD_COLS(add + n * D, y);
-            EACH(NV, j, i) q[j][i] += y[j][i];
+            load_cols(add + n * D, lane, y);
+            EACH_E(i) q[i] += y[i];
         }
-        if (on) STORE_COLS(dx + n * D, q);
+        if (on) store_cols(dx + n * D, lane, q);
     }
     if (!part) return;
-    __shared__ R lds[SCALAR && RPB == 1 ? 1 : RPB * DP];
-    partial_from_columns(acc, lane, group, lds, part + (long)blockIdx.x * C);
+    __shared__ R lds[SUM_LDS];
+    write_partial(acc, lane, lds, part + (long)blockIdx.x * C);
 }
 
 // ---------------------------------------------------------------- join
 // h = alpha r + b[c] y with y = f (rstd_f) and b = act(gate) scale w_post;  u = h rstd_h w_next.
-// u comes from h before its rounding.  Per-channel gates are evaluated once per channel and
-// shared through LDS where a channel has several components.
+// u comes from h before its rounding.
 extern "C" __global__ void __launch_bounds__(BLOCK)
 cgtp_join_fwd(const T *__restrict__ res, const T *__restrict__ f, long f_ld, const T *__restrict__ gate, long gate_ld,
               const R *__restrict__ w_post, const R *__restrict__ scale, const R *__restrict__ w_next,
@@ -379,59 +415,37 @@ cgtp_join_fwd(const T *__restrict__ res, const T *__restrict__ f, long f_ld, con
               R eps)
 {
     ROW_SETUP
-    __shared__ R staged[STAGED ? RPB * CP : 1];
-    R *b = staged + group * CP;
-    R ws[NV][VEC], wsc[NVC][VEC], wn[NV][VEC];
-    if constexpr (STAGED)
-        load_channel_scale(scale, w_post, lane, wsc);
-    else
-        load_column_scale(scale, w_post, lane, ws);
-    if constexpr (NEXT) load_weights(w_next, lane, wn);
+    R ws[NC], wn[NC];
+    load_scale(scale, w_post, lane, ws);
+    if (NEXT) load_weights(w_next, lane, wn);
     EACH_ROW(n, on)
     {
-        R v[NV][VEC], rv[NV][VEC], ss = 0, rf = 1;
-        LOAD_COLS(f + n * f_ld, v);
-        LOAD_COLS(res + n * D, rv);
-        if constexpr (STAGED) {
-            R g[NVC][VEC];
-            LOAD_CHANNELS(gate + n * gate_ld, g);
-            EACH(NVC, j, i)
-            {
-                const int c = (lane + G * j) * VEC + i;
-                if (c < CP) b[c] = gate_value(g[j][i]) * wsc[j][i];
-            }
-            row_sync();
-        }
-        if constexpr (POST) {
-            EACH(NV, j, i) ss += v[j][i] * v[j][i];
-            rf = root_inverse(row_sum(ss, red, turn) / (R)D + eps);
-        }
-        if constexpr (STAGED) {
-            EACH(NV, j, i)
-            v[j][i] = alpha * rv[j][i] + v[j][i] * rf * b[channel_of((lane + G * j) * VEC + i)];
-            row_sync();
-        } else if constexpr (GATE == 2) {
-            R g[NV][VEC];
-            LOAD_COLS(gate + n * gate_ld, g);
-            EACH(NV, j, i) v[j][i] = alpha * rv[j][i] + v[j][i] * rf * ws[j][i] * gate_value(g[j][i]);
+        R v[EPL], rv[EPL], b[NC], ss = 0, rf = 1;
+        load_cols(f + n * f_ld, lane, v);
+        load_cols(res + n * D, lane, rv);
+        if (GATE == 2) {
+            load_channels(gate + n * gate_ld, lane, b);
+            EACH_C(c) b[c] = gate_value(b[c]) * ws[c];
         } else {
             const R a = GATE == 1 ? gate_value((R)gate[n * gate_ld]) : (R)1;
-            EACH(NV, j, i) v[j][i] = alpha * rv[j][i] + v[j][i] * rf * ws[j][i] * a;
+            EACH_C(c) b[c] = a * ws[c];
         }
-        if constexpr (TAIL > 0 || CHUNKS % G != 0) {
-            EACH(NV, j, i) if ((lane + G * j) * VEC + i >= D) v[j][i] = 0;
+        if (POST) {
+            EACH_E(i) ss += v[i] * v[i];
+            rf = root_inverse(row_sum(ss, red, turn) / (R)D + eps);
         }
+        EACH_E(i) v[i] = alpha * rv[i] + v[i] * rf * b[E_C[i]];
         if (on) {
-            STORE_COLS(h + n * D, v);
+            store_cols(h + n * D, lane, v);
             if (POST && rstd_f && lane == 0) rstd_f[n] = rf;
         }
-        if constexpr (NEXT) {
+        if (NEXT) {
             ss = 0;
-            EACH(NV, j, i) ss += v[j][i] * v[j][i];
+            EACH_E(i) ss += v[i] * v[i];
             const R rh = root_inverse(row_sum(ss, red, turn) / (R)D + eps);
-            EACH(NV, j, i) v[j][i] = v[j][i] * rh * wn[j][i];
+            EACH_E(i) v[i] = v[i] * rh * wn[E_C[i]];
             if (on) {
-                STORE_COLS(u + n * D, v);
+                store_cols(u + n * D, lane, v);
                 if (rstd_h && lane == 0) rstd_h[n] = rh;
             }
         }
@@ -439,7 +453,7 @@ cgtp_join_fwd(const T *__restrict__ res, const T *__restrict__ f, long f_ld, con
 }
 
 // With z = h rstd_h, q = w_next du:  e = dh + rstd_h (q - z mean(q z)) is the whole gradient of h,
-//   dr = alpha e,  t = e y,  P[c] = sum_n act sum_m t,  dgate = act' scale w_post sum_m t,
+//   dr = alpha e,  t[c] = sum_m e y,  P[c] = sum_n act t,  dgate = act' scale w_post t,
 //   p = e b,  df = rstd_f (p - y mean(p y)) (p without the norm),  Q[c] = sum_n sum_m du z.
 // dscale = w_post P, dw_post = scale P and dw_next = Q come from the workgroups' partials.
 extern "C" __global__ void __launch_bounds__(BLOCK)
@@ -450,159 +464,104 @@ cgtp_join_bwd(const T *__restrict__ dh, const T *__restrict__ du, const T *__res
               T *__restrict__ dgate, long dgate_ld, R *__restrict__ part, long N, R alpha)
 {
     ROW_SETUP
-    constexpr int LDS = (SCALAR && RPB == 1) ? 1 : RPB * DP;
-    __shared__ R lds[LDS];
-    __shared__ R staged[STAGED ? RPB * CP : 1];
-    R *b = staged + group * CP;
-    R ws[NV][VEC], wsc[NVC][VEC], wn[NV][VEC];
-    R P[NV][VEC], PC[NVC][VEC], Q[NV][VEC];
-    if constexpr (STAGED) {
-        load_channel_scale(scale, w_post, lane, wsc);
-        EACH(NVC, j, i) PC[j][i] = 0;
-    } else {
-        load_column_scale(scale, w_post, lane, ws);
-        EACH(NV, j, i) P[j][i] = 0;
-    }
-    if constexpr (NEXT) {
-        load_weights(w_next, lane, wn);
-        EACH(NV, j, i) Q[j][i] = 0;
-    }
+    R ws[NC], wn[NC], P[NC], Q[NC];
+    load_scale(scale, w_post, lane, ws);
+    if (NEXT) load_weights(w_next, lane, wn);
+    EACH_C(c) P[c] = Q[c] = 0;
     EACH_ROW(n, on)
     {
-        R e[NV][VEC], y[NV][VEC], dot = 0;
-        R ga[NVC][VEC], gs[NVC][VEC];
-        LOAD_COLS(f + n * f_ld, y);
+        R e[EPL], y[EPL], g[NC], t[NC], a = 1, slope = 0, dot = 0;
+        if (GATE == 2) load_channels(gate + n * gate_ld, lane, g);
+        if (GATE == 1) slope = gate_slope((R)gate[n * gate_ld], a);
+        load_cols(f + n * f_ld, lane, y);
         if (dh) {
-            LOAD_COLS(dh + n * D, e);
+            load_cols(dh + n * D, lane, e);
         } else {
-            EACH(NV, j, i) e[j][i] = 0;
+            EACH_E(i) e[i] = 0;
         }
-        if constexpr (STAGED) {
-            R g[NVC][VEC];
-            LOAD_CHANNELS(gate + n * gate_ld, g);
-            EACH(NVC, j, i)
-            {
-                const int c = (lane + G * j) * VEC + i;
-                gs[j][i] = gate_slope(g[j][i], ga[j][i]);
-                if (c < CP) b[c] = ga[j][i] * wsc[j][i];
-            }
-        }
-        if constexpr (NEXT) {
-            R z[NV][VEC], q[NV][VEC];
-            LOAD_COLS(h + n * D, z);
-            LOAD_COLS(du + n * D, q);
+        if (NEXT) {
+            R z[EPL], q[EPL];
+            load_cols(h + n * D, lane, z);
+            load_cols(du + n * D, lane, q);
             const R rh = rstd_h[n];
-            EACH(NV, j, i)
+            EACH_C(c) t[c] = 0;
+            EACH_E(i)
             {
-                z[j][i] *= rh;
-                if (part && on) Q[j][i] += q[j][i] * z[j][i];
-                q[j][i] *= wn[j][i];
-                dot += q[j][i] * z[j][i];
+                z[i] *= rh;
+                t[E_C[i]] += q[i] * z[i];
+                q[i] *= wn[E_C[i]];
+            }
+            EACH_C(c)
+            {
+                if (part && on) Q[c] += t[c];
+                dot += t[c] * wn[c];
             }
             dot = row_sum(dot, red, turn) / (R)D;
-            EACH(NV, j, i) e[j][i] += rh * (q[j][i] - z[j][i] * dot);
+            EACH_E(i) e[i] += rh * (q[i] - z[i] * dot);
         }
         if (dres && on) {
-            R o[NV][VEC];
-            EACH(NV, j, i) o[j][i] = alpha * e[j][i];
-            STORE_COLS(dres + n * D, o);
+            R o[EPL];
+            EACH_E(i) o[i] = alpha * e[i];
+            store_cols(dres + n * D, lane, o);
         }
         const R rf = POST ? rstd_f[n] : (R)1;
-        EACH(NV, j, i) y[j][i] *= rf;
         dot = 0;
-        if constexpr (STAGED) {
-            R *t = lds + group * DP;
-            EACH(NV, j, i)
-            {
-                const int col = (lane + G * j) * VEC + i;
-                if (col < DP) t[col] = e[j][i] * y[j][i];
-            }
-            row_sync();
-            EACH(NV, j, i)
-            {
-                e[j][i] *= b[channel_of((lane + G * j) * VEC + i)];
-                dot += e[j][i] * y[j][i];
-            }
-            EACH(NVC, j, i)
-            {
-                const int c = (lane + G * j) * VEC + i;
-                R s = 0;
-                if (c < C) {
-                    int col, k;
-                    columns_of(c, col, k);
-                    for (int m = 0; m < k; ++m) s += t[col + m];
-                }
-                if (part && on) PC[j][i] += s * ga[j][i];
-                gs[j][i] *= s * wsc[j][i];
-            }
-            row_sync();
-            if (dgate && on) STORE_CHANNELS(dgate + n * dgate_ld, gs);
-        } else if constexpr (GATE == 2) {
-            R g[NV][VEC];
-            LOAD_COLS(gate + n * gate_ld, g);
-            EACH(NV, j, i)
-            {
-                R a;
-                const R sl = gate_slope(g[j][i], a);
-                const R t = e[j][i] * y[j][i];
-                if (part && on) P[j][i] += t * a;
-                g[j][i] = sl * (t * ws[j][i]);
-                e[j][i] *= ws[j][i] * a;
-                dot += e[j][i] * y[j][i];
-            }
-            if (dgate && on) STORE_COLS(dgate + n * dgate_ld, g);
-        } else {
-            R a = 1, sl = 0;
-            if constexpr (GATE == 1) sl = gate_slope((R)gate[n * gate_ld], a);
-            EACH(NV, j, i)
-            {
-                if (part && on) P[j][i] += e[j][i] * y[j][i] * a;
-                e[j][i] *= ws[j][i];
-                dot += e[j][i] * y[j][i];
-                e[j][i] *= a;
-            }
+        EACH_C(c) t[c] = 0;
+        EACH_E(i)
+        {
+            y[i] *= rf;
+            t[E_C[i]] += e[i] * y[i];
         }
-        if constexpr (POST || GATE == 1) dot = row_sum(dot, red, turn);
-        if constexpr (GATE == 1 || GATE == 0) {
-            R a = 1, sl = 0;
-            if constexpr (GATE == 1) {
-                sl = gate_slope((R)gate[n * gate_ld], a);
-                if (dgate && on && lane == 0) dgate[n * dgate_ld] = (T)(sl * dot);
+        EACH_C(c)
+        {
+            R value = a;
+            if (GATE == 2) {
+                const R s = gate_slope(g[c], value);
+                g[c] = s * (t[c] * ws[c]);
             }
-            dot *= a;
+            if (part && on) P[c] += t[c] * value;
+            dot += t[c] * ws[c] * (GATE == 2 ? value : (R)1);
+            t[c] = ws[c] * value;
         }
-        if constexpr (POST) {
-            dot /= (R)D;
-            EACH(NV, j, i) e[j][i] = rf * (e[j][i] - y[j][i] * dot);
+        if (GATE == 2 && dgate && on) store_channels(dgate + n * dgate_ld, lane, g);
+        if (POST || GATE == 1) dot = row_sum(dot, red, turn);
+        if (GATE == 1 && dgate && on && lane == 0) dgate[n * dgate_ld] = (T)(slope * dot);
+        EACH_E(i) e[i] *= t[E_C[i]];
+        if (POST) {
+            dot = dot * a / (R)D;
+            EACH_E(i) e[i] = rf * (e[i] - y[i] * dot);
         }
-        if (df && on) STORE_COLS(df + n * df_ld, e);
+        if (df && on) store_cols(df + n * df_ld, lane, e);
     }
     if (!part) return;
+    __shared__ R lds[SUM_LDS];
     R *out = part + (long)blockIdx.x * (NEXT ? 2 : 1) * C;
-    if constexpr (STAGED)
-        partial_from_channels(PC, lane, group, staged, out);
-    else
-        partial_from_columns(P, lane, group, lds, out);
-    if constexpr (NEXT) partial_from_columns(Q, lane, group, lds, out + C);
+    write_partial(P, lane, lds, out);
+    if (NEXT) write_partial(Q, lane, lds, out + C);
 }
 
 // ---------------------------------------------------------------- sums of the partials
-// rows of `width` elements, one per workgroup of the pass before, added in a fixed order in double.
+// rows of `width` elements, one per workgroup of the pass before, added in a fixed order in double:
+// a workgroup takes 16 columns, 64 rows at a time (four to a wave, whose sums the lanes exchange).
 // join: the first C are P, the next C are Q; else they are the norm's weight gradient.
 extern "C" __global__ void __launch_bounds__(1024)
 cgtp_block_reduce(const R *__restrict__ part, long rows, int width, int join, const R *__restrict__ w_post,
                   const R *__restrict__ scale, R *__restrict__ g_post, R *__restrict__ g_scale, R *__restrict__ g_next)
 {
-    __shared__ double sums[16][64];
-    const int at = blockIdx.x * 64 + (threadIdx.x & 63), slice = threadIdx.x >> 6;
+    __shared__ double sums[16][16];
+    const int col = threadIdx.x & 15, at = blockIdx.x * 16 + col, wave = threadIdx.x >> 6;
     double s = 0;
-    if (at < width)
-        for (long r = slice; r < rows; r += 16) s += (double)part[r * width + at];
-    sums[slice][threadIdx.x & 63] = s;
+    if (at < width) {
+#pragma unroll 8
+        for (long r = threadIdx.x >> 4; r < rows; r += 64) s += (double)part[r * width + at];
+    }
+    s = swap32(swap16(s));
+    if ((threadIdx.x & 63) < 16) sums[wave][col] = s;
     __syncthreads();
-    if (slice != 0 || at >= width) return;
+    if (threadIdx.x >= 16 || at >= width) return;
+    s = 0;
 #pragma unroll
-    for (int k = 1; k < 16; ++k) s += sums[k][threadIdx.x & 63];
+    for (int k = 0; k < 16; ++k) s += sums[k][col];
     if (join && at < C) {
         if (g_scale) g_scale[at] = (R)(POST && w_post ? s * (double)w_post[at] : s);
         if (POST && g_post) g_post[at] = (R)(scale ? s * (double)scale[at] : s);

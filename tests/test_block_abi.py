@@ -1,6 +1,7 @@
 """Blocks and the optimizer step on the CPU: layouts, sizes, generated sources, and refusals, all
 before any GPU call (the addresses below are never dereferenced)."""
 import ctypes
+import re
 
 import numpy as np
 import pytest
@@ -22,11 +23,26 @@ def at(mb, off=0):
     ("4096x0e", 4096, 4096)])
 @pytest.mark.parametrize("dtype", ["f32", "f64", "bf16", "f16"])
 def test_block_layout(irreps, d, channels, dtype):
-    b = cg.Block(irreps, dtype, gate="channel", act="silu", post_norm=True, next_norm=True)
-    assert (b.d, b.channels, b.gate_width) == (d, channels, channels)
-    vec = {"f32": 4, "f64": 2}.get(dtype, 8)
+    for gate, width in (("channel", channels), ("row", 1), (None, 0)):
+        b = cg.Block(irreps, dtype, gate=gate, act="silu", post_norm=True, next_norm=True)
+        assert (b.d, b.channels, b.gate_width) == (d, channels, width)
+        check_layout(b, d)
+
+
+def check_layout(b, d):
     assert b.lanes & (b.lanes - 1) == 0 and 1 <= b.lanes <= 1024
-    assert b.lanes * b.chunks * vec >= d and b.lanes * (b.chunks - 1) * vec < d
+    assert b.lanes * b.lane_elements >= d and b.lane_elements <= 128
+    # the source's slots cover every column once
+    const = {m[0]: [int(v) for v in m[1].split(",")] for m in
+             re.findall(r"constexpr int (\w+)(?:\[\w+\])? = \{?([-\d, ]+)\}?;", b.source)}
+    cv, seen = const["CV"][0], []
+    for j in range(const["NSLOT"][0]):
+        k = const["S_K"][j]
+        for lane in range(b.lanes):
+            first = (const["S_UNIT"][j] + lane) * cv
+            for c in range(first, min(first + cv, const["S_MUL"][j])):
+                seen += range(const["S_COL"][j] + c * k, const["S_COL"][j] + c * k + k)
+    assert sorted(seen) == list(range(d))
     for name in ("cgtp_norm_fwd", "cgtp_norm_bwd", "cgtp_join_fwd", "cgtp_join_bwd", "cgtp_block_reduce"):
         assert name + "(" in b.source
     assert "atomic" not in b.source.lower().replace("__atomic_acq_rel", "")
@@ -56,9 +72,9 @@ def test_block_creation_refusals():
         assert cg.last_error()
     assert create(None) == INVAL
     assert L.cgtp_block_create(b"4x0e", None, ctypes.byref(h)) == INVAL
-    assert create(b"40000x0e") == UNSUP                       # over 1024 lanes x 8 chunks of 4 floats
-    assert create(b"20000x0e", dtype=1) == UNSUP
-    assert create(b"+".join([b"1x0e+1x1o"] * 33)) == UNSUP    # 66 changes of degree
+    assert create(b"131073x0e") == UNSUP                      # over 1024 lanes x 128 elements
+    many = b"+".join([b"1x0e+1x1o"] * 33)   # with a gate per channel, 132 elements in a lane
+    assert create(many, gate=2) == UNSUP and create(many, gate=1) == 0 and L.cgtp_block_destroy(h) == 0
     assert L.cgtp_block_destroy(None) == 0
     with pytest.raises(cg.CgtpError, match="irreps"):
         cg.Block("nonsense")
