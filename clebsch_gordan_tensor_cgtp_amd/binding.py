@@ -696,15 +696,30 @@ def block_for(irreps, dtype="f32", gate=None, act="sigmoid", post_norm=False, ne
 
 
 def _device_index(t, name):
-    import torch
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise TypeError(f"{name} must be a CUDA (HIP) torch tensor")
-    return t.get_device()
+    try:
+        if t.is_cuda:
+            return t.get_device()
+    except AttributeError:
+        pass
+    raise TypeError(f"{name} must be a CUDA (HIP) torch tensor")
 
 
-def _raw_stream(stream, index):
+_current_raw_stream = None
+
+
+def _in_stream(stream, call, *args, **kw):
+    """The call with `stream` as the current one, so that what it allocates belongs to that stream."""
     import torch
-    return stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(index)
+    with torch.cuda.stream(stream):
+        return call(*args, **kw)
+
+
+def _raw_stream(index):
+    global _current_raw_stream
+    if _current_raw_stream is None:
+        import torch
+        _current_raw_stream = torch._C._cuda_getCurrentRawStream
+    return _current_raw_stream(index)
 
 
 def _refuse(t, name, dtype, shape, index):
@@ -751,6 +766,23 @@ def _rows_or_null(t, name, dtype, shape, index):
     return (None, shape[1]) if t is None else _rows(t, name, dtype, shape, index)
 
 
+def _output(t, wanted, name, dtype, shape, like, index):
+    """(tensor, address) of an output: the caller's, or a new one where it is wanted."""
+    if t is not None:
+        return t, _addr(t, name, dtype, shape, index)
+    if not wanted:
+        return None, None
+    t = like.new_empty(shape, dtype=dtype)
+    return t, t.data_ptr()
+
+
+def _row_output(t, wanted, name, dtype, shape, like, index):
+    """(tensor, address, row pitch) of an output of rows."""
+    if t is not None:
+        return (t,) + _rows(t, name, dtype, shape, index)
+    return _output(None, wanted, name, dtype, shape, like, index) + (shape[1],)
+
+
 def block_workspace_size(block: Block, n: int) -> int:
     v = ctypes.c_size_t()
     _check(lib().cgtp_block_workspace_size(block.handle, n, ctypes.byref(v)))
@@ -759,8 +791,8 @@ def block_workspace_size(block: Block, n: int) -> int:
 
 def _workspace(t, name, nbytes, like, index):
     """(address, bytes, tensor) of the caller's workspace, or of a new one."""
-    import torch
     if t is None:
+        import torch
         t = like.new_empty(nbytes, dtype=torch.uint8)
         return t.data_ptr(), nbytes, t
     return _addr(t, name, t.dtype, t.shape, index), t.numel() * t.element_size(), t
@@ -768,16 +800,16 @@ def _workspace(t, name, nbytes, like, index):
 
 def norm_forward(block: Block, x, w, u=None, rstd=None, need_rstd=True, stream=None):
     """(u, rstd): u = x * rstd(x) * w per channel.  x may have a row pitch; w None stands for ones."""
+    if stream is not None:
+        return _in_stream(stream, norm_forward, block, x, w, u, rstd, need_rstd)
     dev = _device_index(x, "x")
     n, dt, rt = x.shape[0], block.torch_dtype, block.real_dtype
     rows = (n, block.d)
     xp, x_ld = _rows(x, "x", dt, rows, dev)
-    u = x.new_empty(rows) if u is None else u
-    if rstd is None and need_rstd:
-        rstd = x.new_empty(n, dtype=rt)
-    _check(lib().cgtp_norm_forward(block.handle, n, xp, x_ld, _addr_or_null(w, "w", rt, (block.channels,), dev),
-                                   _addr(u, "u", dt, rows, dev), _addr_or_null(rstd, "rstd", rt, (n,), dev),
-                                   _raw_stream(stream, dev)))
+    u, up = _output(u, True, "u", dt, rows, x, dev)
+    rstd, rp = _output(rstd, need_rstd, "rstd", rt, (n,), x, dev)
+    _check(lib().cgtp_norm_forward(block.handle, n, xp, x_ld, _addr_or_null(w, "w", rt, (block.channels,), dev), up, rp,
+                                   _raw_stream(dev)))
     return u, rstd
 
 
@@ -785,20 +817,21 @@ def norm_backward(block: Block, x, w, rstd, grad_u, grad_add=None, grad_x=None, 
                   workspace=None, stream=None):
     """(grad_x, grad_w); entries not in ``need`` are None and not computed.  grad_add, when given,
     is added to grad_x (the gradient that reaches x past the norm)."""
+    if stream is not None:
+        return _in_stream(stream, norm_backward, block, x, w, rstd, grad_u, grad_add, grad_x, grad_w, need, workspace)
     dev = _device_index(x, "x")
     n, dt, rt, cs = x.shape[0], block.torch_dtype, block.real_dtype, (block.channels,)
     rows = (n, block.d)
     xp, x_ld = _rows(x, "x", dt, rows, dev)
-    gx = None if not need[0] else x.new_empty(rows) if grad_x is None else grad_x
-    gw = None if not need[1] else x.new_empty(cs, dtype=rt) if grad_w is None else grad_w
+    gx, gxp = _output(grad_x if need[0] else None, need[0], "grad_x", dt, rows, x, dev)
+    gw, gwp = _output(grad_w if need[1] else None, need[1], "grad_w", rt, cs, x, dev)
     ws, ws_bytes = None, 0
     if gw is not None:
         ws, ws_bytes, workspace = _workspace(workspace, "workspace", block_workspace_size(block, n), x, dev)
     _check(lib().cgtp_norm_backward(block.handle, n, xp, x_ld, _addr_or_null(w, "w", rt, cs, dev),
                                     _addr(rstd, "rstd", rt, (n,), dev), _addr(grad_u, "grad_u", dt, rows, dev),
-                                    _addr_or_null(grad_add, "grad_add", dt, rows, dev),
-                                    _addr_or_null(gx, "grad_x", dt, rows, dev),
-                                    _addr_or_null(gw, "grad_w", rt, cs, dev), ws, ws_bytes, _raw_stream(stream, dev)))
+                                    _addr_or_null(grad_add, "grad_add", dt, rows, dev), gxp, gwp, ws, ws_bytes,
+                                    _raw_stream(dev)))
     return gx, gw
 
 
@@ -807,25 +840,21 @@ def join_forward(block: Block, res, f, gate, w_post, scale, w_next, h=None, u=No
     """(h, u, rstd_f, rstd_h): h = alpha*res + scale*act(gate)*w_post*f*rstd(f), u = h*rstd(h)*w_next.
     f and gate may have a row pitch (both in one buffer, say); weights given as None are ones; what
     the block's configuration leaves out is None."""
+    if stream is not None:
+        return _in_stream(stream, join_forward, block, res, f, gate, w_post, scale, w_next, h, u, rstd_f, rstd_h, need_rstd)
     dev = _device_index(f, "f")
     n, dt, rt, cs = f.shape[0], block.torch_dtype, block.real_dtype, (block.channels,)
     rows, stat = (n, block.d), (n,)
     fp, f_ld = _rows(f, "f", dt, rows, dev)
     gp, g_ld = _rows_or_null(gate, "gate", dt, (n, block.gate_width), dev)
-    if h is None:
-        h = f.new_empty(rows)
-    if u is None and block.next_norm:
-        u = f.new_empty(rows)
-    if rstd_f is None and need_rstd and block.post_norm:
-        rstd_f = f.new_empty(n, dtype=rt)
-    if rstd_h is None and need_rstd and block.next_norm:
-        rstd_h = f.new_empty(n, dtype=rt)
+    h, hp = _output(h, True, "h", dt, rows, f, dev)
+    u, up = _output(u, block.next_norm, "u", dt, rows, f, dev)
+    rstd_f, rfp = _output(rstd_f, need_rstd and block.post_norm, "rstd_f", rt, stat, f, dev)
+    rstd_h, rhp = _output(rstd_h, need_rstd and block.next_norm, "rstd_h", rt, stat, f, dev)
     _check(lib().cgtp_join_forward(
         block.handle, n, _addr(res, "res", dt, rows, dev), fp, f_ld, gp, g_ld,
         _addr_or_null(w_post, "w_post", rt, cs, dev), _addr_or_null(scale, "scale", rt, cs, dev),
-        _addr_or_null(w_next, "w_next", rt, cs, dev), _addr(h, "h", dt, rows, dev),
-        _addr_or_null(u, "u", dt, rows, dev), _addr_or_null(rstd_f, "rstd_f", rt, stat, dev),
-        _addr_or_null(rstd_h, "rstd_h", rt, stat, dev), _raw_stream(stream, dev)))
+        _addr_or_null(w_next, "w_next", rt, cs, dev), hp, up, rfp, rhp, _raw_stream(dev)))
     return h, u, rstd_f, rstd_h
 
 
@@ -835,31 +864,32 @@ def join_backward(block: Block, grad_h, grad_u, h, f, gate, w_post, scale, w_nex
     (None: zero) and u and the forward's h and statistics; entries not in ``need``, or that the
     block's configuration leaves out, are None and not computed.  grad_f and grad_gate given in
     ``outs`` may have a row pitch."""
+    if stream is not None:
+        return _in_stream(stream, join_backward, block, grad_h, grad_u, h, f, gate, w_post, scale, w_next, rstd_f,
+                          rstd_h, outs, need, workspace)
     dev = _device_index(f, "f")
     n, dt, rt, cs = f.shape[0], block.torch_dtype, block.real_dtype, (block.channels,)
     rows, gates, stat = (n, block.d), (n, block.gate_width), (n,)
     fp, f_ld = _rows(f, "f", dt, rows, dev)
     gp, g_ld = _rows_or_null(gate, "gate", dt, gates, dev)
-    has = (True, True, block.gate_width > 0, block.post_norm, True, block.next_norm)
-    res = [None] * 6
-    for i, (o, shape) in enumerate(zip(outs, (rows, rows, gates, cs, cs, cs))):
-        if need[i] and has[i]:
-            res[i] = o if o is not None else f.new_empty(shape) if i < 3 else f.new_empty(shape, dtype=rt)
-    gr, gf, gg, gp_, gs, gn = res
-    dfp, df_ld = _rows_or_null(gf, "grad_f", dt, rows, dev)
-    dgp, dg_ld = _rows_or_null(gg, "grad_gate", dt, gates, dev)
+    has_gate, post, nxt = block.gate_width > 0, block.post_norm, block.next_norm
+    o0, o1, o2, o3, o4, o5 = [o if nd else None for o, nd in zip(outs, need)]
+    gr, grp = _output(o0, need[0], "grad_res", dt, rows, f, dev)
+    gf, gfp, gf_ld = _row_output(o1, need[1], "grad_f", dt, rows, f, dev)
+    gg, ggp, gg_ld = _row_output(o2, need[2] and has_gate, "grad_gate", dt, gates, f, dev)
+    gp3, g3 = _output(o3, need[3] and post, "grad_w_post", rt, cs, f, dev)
+    gp4, g4 = _output(o4, need[4], "grad_scale", rt, cs, f, dev)
+    gp5, g5 = _output(o5, need[5] and nxt, "grad_w_next", rt, cs, f, dev)
     ws, ws_bytes = None, 0
-    if gp_ is not None or gs is not None or gn is not None:
+    if g3 is not None or g4 is not None or g5 is not None:
         ws, ws_bytes, workspace = _workspace(workspace, "workspace", block_workspace_size(block, n), f, dev)
     _check(lib().cgtp_join_backward(
         block.handle, n, _addr_or_null(grad_h, "grad_h", dt, rows, dev), _addr_or_null(grad_u, "grad_u", dt, rows, dev),
         _addr_or_null(h, "h", dt, rows, dev), fp, f_ld, gp, g_ld, _addr_or_null(w_post, "w_post", rt, cs, dev),
         _addr_or_null(scale, "scale", rt, cs, dev), _addr_or_null(w_next, "w_next", rt, cs, dev),
         _addr_or_null(rstd_f, "rstd_f", rt, stat, dev), _addr_or_null(rstd_h, "rstd_h", rt, stat, dev),
-        _addr_or_null(gr, "grad_res", dt, rows, dev), dfp, df_ld, dgp, dg_ld,
-        _addr_or_null(gp_, "grad_w_post", rt, cs, dev), _addr_or_null(gs, "grad_scale", rt, cs, dev),
-        _addr_or_null(gn, "grad_w_next", rt, cs, dev), ws, ws_bytes, _raw_stream(stream, dev)))
-    return tuple(res)
+        grp, gfp, gf_ld, ggp, gg_ld, g3, g4, g5, ws, ws_bytes, _raw_stream(dev)))
+    return gr, gf, gg, gp3, gp4, gp5
 
 
 # ------------------------------------------------------------------------------------ optimizer
@@ -886,15 +916,12 @@ class AdamW:
         self.offsets = tuple(off)
         self.torch_dtype = _torch_dtype(dtype)
         self.real_dtype = _torch_dtype("f64" if dtype == "f64" else "f32")
+        import torch
+        self.moment_dtypes = (torch.int8, torch.uint8) if state_bits == 8 else (self.real_dtype, self.real_dtype)
 
     @property
     def handle(self):
         return self._h
-
-    @property
-    def moment_dtypes(self):
-        import torch
-        return (torch.int8, torch.uint8) if self.state_bits == 8 else (self.real_dtype, self.real_dtype)
 
     def state(self, device, params=None):
         """(m, v, scales, master) at the start: zero moments, and master copies of ``params``."""
@@ -967,6 +994,8 @@ def _list(opt, tensors):
 def grad_norm(opt: AdamW, grads, norm=None, workspace=None, stream=None):
     """The global norm of the gradients (a TensorList or tensors; None ones are left out): a device
     float64 tensor of one element."""
+    if stream is not None:
+        return _in_stream(stream, grad_norm, opt, grads, norm, workspace)
     import torch
     grads = _list(opt, grads)
     dev = grads.device_index
@@ -976,7 +1005,7 @@ def grad_norm(opt: AdamW, grads, norm=None, workspace=None, stream=None):
     norm = like.new_empty(1, dtype=torch.float64) if norm is None else norm
     ws, ws_bytes, workspace = _workspace(workspace, "workspace", opt.norm_workspace, like, dev)
     _check(lib().cgtp_grad_norm(opt.handle, grads.pointers(), _addr(norm, "norm", torch.float64, (1,), dev), ws,
-                                ws_bytes, _raw_stream(stream, dev)))
+                                ws_bytes, _raw_stream(dev)))
     return norm
 
 
@@ -986,6 +1015,10 @@ def adamw_step(opt: AdamW, params, grads, m, v, scales=None, master=None, *, lr=
     ``norm`` (as of grad_norm) a step whose norm is not finite changes nothing, and max_norm > 0
     clips by it.  ``schedule``: a device float64 tensor {step, lr, 1 - beta1^step, 1 - beta2^step}
     in the place of ``step`` and ``lr`` (adamw_schedule advances it)."""
+    if stream is not None:
+        return _in_stream(stream, adamw_step, opt, params, grads, m, v, scales, master, lr=lr, beta1=beta1, beta2=beta2,
+                          eps=eps, weight_decay=weight_decay, step=step, max_norm=max_norm, grad_scale=grad_scale,
+                          norm=norm, schedule=schedule)
     import torch
     params, grads = _list(opt, params), _list(opt, grads)
     if len(params._given) != len(opt.sizes):
@@ -999,37 +1032,43 @@ def adamw_step(opt: AdamW, params, grads, m, v, scales=None, master=None, *, lr=
         _addr_or_null(scales, "scales", torch.float32, (2, opt.blocks), dev),
         _addr_or_null(master, "master", torch.float32, el, dev), ctypes.byref(hyper),
         _addr_or_null(norm, "norm", torch.float64, (1,), dev),
-        _addr_or_null(schedule, "schedule", torch.float64, (4,), dev), _raw_stream(stream, dev)))
+        _addr_or_null(schedule, "schedule", torch.float64, (4,), dev), _raw_stream(dev)))
 
 
 def adamw_schedule(schedule, beta1=0.9, beta2=0.999, stream=None):
     """Advance a device schedule {step, lr, 1 - beta1^step, 1 - beta2^step} by one step."""
+    if stream is not None:
+        return _in_stream(stream, adamw_schedule, schedule, beta1, beta2)
     import torch
-    _check(lib().cgtp_adamw_schedule(_dev(schedule, "schedule", torch.float64, (4,)), beta1, beta2,
-                                     _stream(stream, schedule.device)))
+    dev = _device_index(schedule, "schedule")
+    _check(lib().cgtp_adamw_schedule(_addr(schedule, "schedule", torch.float64, (4,), dev), beta1, beta2,
+                                     _raw_stream(dev)))
     return schedule
 
 
 def adamw_state_read(opt: AdamW, m, v, scales, m_out=None, v_out=None, stream=None):
     """The values that 8-bit moments stand for: (m, v) in float32."""
+    if stream is not None:
+        return _in_stream(stream, adamw_state_read, opt, m, v, scales, m_out, v_out)
     import torch
-    el, (mt, vt) = opt.elements, opt.moment_dtypes
-    m_out = torch.empty(el, dtype=torch.float32, device=m.device) if m_out is None else m_out
-    v_out = torch.empty(el, dtype=torch.float32, device=m.device) if v_out is None else v_out
-    _check(lib().cgtp_adamw_state_read(opt.handle, _dev(m, "m", mt, (el,)), _dev(v, "v", vt, (el,)),
-                                       _ptr_or_null(scales, "scales", torch.float32, (2, opt.blocks)),
-                                       _dev(m_out, "m_out", torch.float32, (el,)),
-                                       _dev(v_out, "v_out", torch.float32, (el,)), _stream(stream, m.device)))
+    dev, el, (mt, vt), f32 = _device_index(m, "m"), (opt.elements,), opt.moment_dtypes, torch.float32
+    m_out = m.new_empty(el, dtype=f32) if m_out is None else m_out
+    v_out = m.new_empty(el, dtype=f32) if v_out is None else v_out
+    _check(lib().cgtp_adamw_state_read(opt.handle, _addr(m, "m", mt, el, dev), _addr(v, "v", vt, el, dev),
+                                       _addr_or_null(scales, "scales", f32, (2, opt.blocks), dev),
+                                       _addr(m_out, "m_out", f32, el, dev), _addr(v_out, "v_out", f32, el, dev),
+                                       _raw_stream(dev)))
     return m_out, v_out
 
 
 def adamw_state_write(opt: AdamW, m_in, v_in, m, v, scales, stream=None):
     """8-bit moments from float32 values (both in the flat layout)."""
+    if stream is not None:
+        return _in_stream(stream, adamw_state_write, opt, m_in, v_in, m, v, scales)
     import torch
-    el, (mt, vt) = opt.elements, opt.moment_dtypes
-    _check(lib().cgtp_adamw_state_write(opt.handle, _dev(m_in, "m_in", torch.float32, (el,)),
-                                        _dev(v_in, "v_in", torch.float32, (el,)), _dev(m, "m", mt, (el,)),
-                                        _dev(v, "v", vt, (el,)),
-                                        _ptr_or_null(scales, "scales", torch.float32, (2, opt.blocks)),
-                                        _stream(stream, m.device)))
+    dev, el, (mt, vt), f32 = _device_index(m, "m"), (opt.elements,), opt.moment_dtypes, torch.float32
+    _check(lib().cgtp_adamw_state_write(opt.handle, _addr(m_in, "m_in", f32, el, dev),
+                                        _addr(v_in, "v_in", f32, el, dev), _addr(m, "m", mt, el, dev),
+                                        _addr(v, "v", vt, el, dev),
+                                        _addr_or_null(scales, "scales", f32, (2, opt.blocks), dev), _raw_stream(dev)))
     return m, v, scales
