@@ -213,7 +213,7 @@ void check_rows(const Block &b, int64_t N, const Rows &r)
     require(r.ld >= r.width && r.ld < INT_MAX,
             std::string(r.name) + ": row pitch " + std::to_string(r.ld) + " is below the row's " +
                 std::to_string(r.width) + " elements or above 2^31-1");
-    (void)N;
+    require(N <= ((int64_t)1 << 56) / (r.ld * b.elem), std::string(r.name) + ": more than 2^56 bytes");
 }
 
 // No row of one may overlap a row of the other: their ranges are apart, or both have the same

@@ -25,8 +25,11 @@ size_t moment_bytes(const cgtp_adamw &o) { return o.cfg.state_bits == 8 ? 1 : o.
 
 int64_t elements(const cgtp_adamw &o) { return o.units * kUnit; }
 
-// Calls `use` with tables of at most kTableTensors tensors, the ones without a gradient and the
-// empty ones left out.
+// Units of one launch: 256 threads each, and a launch's threads are counted in 32 bits.
+constexpr int64_t kLaunchUnits = (int64_t)1 << 23;
+
+// Calls `use` with tables of at most kTableTensors tensors and kLaunchUnits units, longer tensors in
+// parts, the ones without a gradient and the empty ones left out.
 template <class F> void each_table(const cgtp_adamw &o, void *const *params, const void *const *grads, F &&use)
 {
     TensorTable t;
@@ -39,14 +42,18 @@ template <class F> void each_table(const cgtp_adamw &o, void *const *params, con
         units = 0;
     };
     for (size_t i = 0; i < o.sizes.size(); ++i) {
-        if (o.sizes[i] == 0 || !grads[i]) continue;
-        t.unit[t.n] = (int32_t)units;
-        t.state[t.n] = (int32_t)o.first[i];
-        t.numel[t.n] = o.sizes[i];
-        t.param[t.n] = params ? params[i] : nullptr;
-        t.grad[t.n] = grads[i];
-        units += (o.sizes[i] + kUnit - 1) / kUnit;
-        if (++t.n == kTableTensors) flush();
+        if (!grads[i]) continue;
+        for (int64_t done = 0; done < o.sizes[i];) {
+            const int64_t part = std::min(o.sizes[i] - done, (kLaunchUnits - units) * kUnit);
+            t.unit[t.n] = (int32_t)units;
+            t.state[t.n] = (int32_t)(o.first[i] + done / kUnit);
+            t.numel[t.n] = part;
+            t.param[t.n] = params ? static_cast<char *>(params[i]) + done * o.elem : nullptr;
+            t.grad[t.n] = static_cast<const char *>(grads[i]) + done * o.elem;
+            units += (part + kUnit - 1) / kUnit;
+            done += part;
+            if (++t.n == kTableTensors || units == kLaunchUnits) flush();
+        }
     }
     flush();
 }
@@ -86,10 +93,11 @@ void check_extents(std::vector<Extent> &all)
     }
 }
 
+// one partial per workgroup of each launch; a launch ends at a full table or at kLaunchUnits
 size_t norm_workspace(const cgtp_adamw &o)
 {
-    const size_t tables = (o.sizes.size() + kTableTensors - 1) / kTableTensors;
-    return tables * 2048 * sizeof(double);
+    const int64_t launches = ((int64_t)o.sizes.size() + kTableTensors - 1) / kTableTensors + o.units / kLaunchUnits;
+    return (size_t)launches * kNormGroups * sizeof(double);
 }
 
 }  // namespace

@@ -11,6 +11,8 @@ namespace cgtp {
 constexpr int kUnit = 2048;
 // Values that share a scale in the 8-bit form.
 constexpr int kScaleBlock = 64;
+// Most workgroups of a launch of the gradients' norm, and so partial sums of it.
+constexpr int kNormGroups = 2048;
 // Tensors of one launch: their table is a kernel argument, which may take 4 KB.
 constexpr int kTableTensors = 112;
 

@@ -127,10 +127,11 @@ template <int LANES, int N> __device__ __forceinline__ float block_most(const fl
     return a < 1.17549435e-38f ? 0.0f : a;  // below it 1 / a is infinite
 }
 
-// Codes of N values.  The code is defined by the correctly rounded root; the hardware's is a bit off, which
-// matters only where the scaled root lies next to the middle between two codes (2^-24 of 255,
-// twice, is 3e-5): a wave in which any does takes the exact root.  About one wave in ten does; the exact
-// root everywhere is 16 instructions more a code, of some 75 an element.
+// Codes of N values.  The code is defined by the correctly rounded root; the hardware's is off by up to a
+// step of its last bit, which matters only where the scaled root lies next to the middle between two
+// codes (255 times 1.5 steps of 2^-24, and a rounding of the product: 4e-5): a wave in which any
+// does takes the exact root.  About one wave in ten does; the exact root everywhere is 16 instructions more a
+// code, of some 75 an element.
 template <bool SIGNED, int N> __device__ __forceinline__ void codes_of(const float (&x)[N], float most, float (&q)[N])
 {
     constexpr float top = SIGNED ? 127.0f : 255.0f;
@@ -333,24 +334,24 @@ __global__ void __launch_bounds__(256) state_read_kernel(const signed char *m, c
                                                          const float *scales, int64_t elements, float *m_out,
                                                          float *v_out)
 {
-    const int64_t at = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
-    if (at >= elements) return;
-    const float am = scales[at / kScaleBlock], as = scales[(elements + at) / kScaleBlock];
-    float x[4];
-    if (m_out) {
-        load_vec(m + at, x);
+    for (int64_t at = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4; at < elements; at += (int64_t)gridDim.x * 1024) {
+        const float am = scales[at / kScaleBlock], as = scales[(elements + at) / kScaleBlock];
+        float x[4];
+        if (m_out) {
+            load_vec(m + at, x);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) x[j] = value_of<true>(x[j], am);
-        store_vec(m_out + at, x);
-    }
-    if (v_out) {
-        load_vec(v + at, x);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const float s = value_of<false>(x[j], as);
-            x[j] = s * s;
+            for (int j = 0; j < 4; ++j) x[j] = value_of<true>(x[j], am);
+            store_vec(m_out + at, x);
         }
-        store_vec(v_out + at, x);
+        if (v_out) {
+            load_vec(v + at, x);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float s = value_of<false>(x[j], as);
+                x[j] = s * s;
+            }
+            store_vec(v_out + at, x);
+        }
     }
 }
 
@@ -358,21 +359,21 @@ __global__ void __launch_bounds__(256) state_read_kernel(const signed char *m, c
 __global__ void __launch_bounds__(256) state_write_kernel(const float *m_in, const float *v_in, int64_t elements,
                                                           signed char *m, unsigned char *v, float *scales)
 {
-    const int64_t at = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
-    if (at >= elements) return;
-    float x[4], c[4];
-    load_vec(m_in + at, x);
-    float most = block_most<16>(x);
-    codes_of<true>(x, most, c);
-    store_vec(m + at, c);
-    if (threadIdx.x % 16 == 0) scales[at / kScaleBlock] = most;
-    load_vec(v_in + at, x);
+    for (int64_t at = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4; at < elements; at += (int64_t)gridDim.x * 1024) {
+        float x[4], c[4];
+        load_vec(m_in + at, x);
+        float most = block_most<16>(x);
+        codes_of<true>(x, most, c);
+        store_vec(m + at, c);
+        if (threadIdx.x % 16 == 0) scales[at / kScaleBlock] = most;
+        load_vec(v_in + at, x);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) x[j] = __builtin_sqrtf(x[j]);
-    most = block_most<16>(x);
-    codes_of<false>(x, most, c);
-    store_vec(v + at, c);
-    if (threadIdx.x % 16 == 0) scales[(elements + at) / kScaleBlock] = most;
+        for (int j = 0; j < 4; ++j) x[j] = __builtin_sqrtf(x[j]);
+        most = block_most<16>(x);
+        codes_of<false>(x, most, c);
+        store_vec(v + at, c);
+        if (threadIdx.x % 16 == 0) scales[(elements + at) / kScaleBlock] = most;
+    }
 }
 
 // {step, lr, 1 - b1^step, 1 - b2^step}: one more step
@@ -428,7 +429,7 @@ hipError_t launch_adamw(Elem elem, bool codes, const TensorTable &t, const Momen
     return hipErrorInvalidValue;
 }
 
-int grad_norm_groups(int64_t units) { return (int)std::min<int64_t>(units, 2048); }
+int grad_norm_groups(int64_t units) { return (int)std::min<int64_t>(units, kNormGroups); }
 
 hipError_t launch_square_sums(Elem elem, const TensorTable &t, double *partial, hipStream_t st)
 {
@@ -450,11 +451,14 @@ hipError_t launch_norm(const double *partial, int64_t n, double *norm, hipStream
     return hipGetLastError();
 }
 
+// 1024 elements to a workgroup, and more to each where a launch's threads would not fit 32 bits
+static dim3 flat_grid(int64_t elements) { return dim3((unsigned)std::min<int64_t>(elements / 1024, 1 << 23)); }
+
 hipError_t launch_state_read(const void *m, const void *v, const float *scales, int64_t elements, float *m_out,
                              float *v_out, hipStream_t st)
 {
     if (elements == 0) return hipSuccess;
-    state_read_kernel<<<dim3((unsigned)(elements / 1024)), dim3(256), 0, st>>>(
+    state_read_kernel<<<flat_grid(elements), dim3(256), 0, st>>>(
         static_cast<const signed char *>(m), static_cast<const unsigned char *>(v), scales, elements, m_out, v_out);
     return hipGetLastError();
 }
@@ -463,7 +467,7 @@ hipError_t launch_state_write(const float *m_in, const float *v_in, int64_t elem
                               hipStream_t st)
 {
     if (elements == 0) return hipSuccess;
-    state_write_kernel<<<dim3((unsigned)(elements / 1024)), dim3(256), 0, st>>>(
+    state_write_kernel<<<flat_grid(elements), dim3(256), 0, st>>>(
         m_in, v_in, elements, static_cast<signed char *>(m), static_cast<unsigned char *>(v), scales);
     return hipGetLastError();
 }

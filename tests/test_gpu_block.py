@@ -8,7 +8,7 @@ from oracle import block as ob
 from oracle import wigner
 from oracle.irreps import parse_irreps
 
-from block_cases import CONFIGS, DTYPES, EPS, LADDER, ODD, ROW, SHAPES, WIDE, bound, inputs, weight_roundings, wide
+from block_cases import CHANGING, CONFIGS, DTYPES, EPS, LADDER, ODD, ROW, SHAPES, WIDE, bound, inputs, weight_roundings, wide
 
 pytestmark = pytest.mark.gpu
 
@@ -99,6 +99,12 @@ def test_join_shapes(device, irreps, rows, dtype):
 def test_join_wide_scalar_rows(device, irreps, rows, dtype):
     for config in (CONFIGS[0], CONFIGS[3], CONFIGS[5]):
         check_join(irreps, rows, dtype, config, device, 23)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_join_with_a_degree_for_every_channel(device, dtype):
+    for config in (CONFIGS[0], CONFIGS[3]):
+        check_join(CHANGING, 300, dtype, config, device, 24)
 
 
 def test_rows_with_a_pitch_side_by_side_and_unaligned(device):
