@@ -34,11 +34,13 @@ const char *type_name(int dtype)
 // Of every pair, the cost of a row in lane operations is taken: its lanes times a lane's elements,
 // which idle lanes and channels past an irrep's end raise, more where loads are narrow (below 16 bytes
 // in a flat layout, below 8 in runs of channels, which are neighbours in the same cache lines), where a
-// lane holds over 16 words (fewer waves fit a SIMD), and where waves must meet at barriers; the most
-// lanes of equal cost.  The weights are fitted to times of 12 shapes at 3 to 9 pairs each.  The join's
-// backward, fp32: 20,000 rows of 128x(0e,1o,2e,3o), 64 lanes of 32 elements 210 us, 128 of 16 201 us, 512
-// of 16, half idle, 216 us; 5,000 rows of 32x(0e,1o,2e), 32 lanes of 9 13.7 us, 16 of 18 15.9 us.  The
-// norm, 200,000 flat rows of 65 in fp16: 4 lanes of 9 loads of 4 bytes 25.7 us, of 3 loads of 16 11.7 us.
+// lane holds over 48 bytes (fewer waves fit a SIMD), and where waves must meet at barriers; the most
+// lanes of equal cost.  The weights are fitted to times of 14 shapes at 2 to 9 pairs each.  The
+// join's backward, fp32: 20,000 rows of 128x(0e,1o,2e,3o), 64 lanes of 32 elements 210 us, 128 of 16 201
+// us, 512 of 16, half idle, 216 us; 5,000 rows of 32x(0e,1o,2e), 32 lanes of 9 13.3 us, 16 of 18 15.9 us.
+// The norm: backward, 200,000 flat rows of 576 in fp32, 32 lanes of 20 elements 356 us, 64 of 12, a
+// quarter idle, 340 us; 200,000 rows of 65 in fp16, 4 lanes of 9 loads of 4 bytes 25.7 us, of 3 loads of 16
+// 12.3 us.
 void pick_lanes(Block &b)
 {
     double best = 0;
@@ -56,9 +58,9 @@ void pick_lanes(Block &b)
                     if (run & piece) bytes += slots * std::max(b.flat ? 16 : 8, piece * b.elem);
             }
             if (elems > most) continue;
-            const double words = (double)elems * b.real / 4;
+            const double held = (double)elems * b.elem;
             double cost = (double)g * elems / b.d;
-            cost *= 1 + 0.02 * std::max(0.0, words - 16);
+            cost *= 1 + 0.01 * std::max(0.0, held - 48);
             cost *= 1 + (b.flat ? 0.3 : 0.1) * ((double)bytes / (elems * b.elem) - 1);
             if (g > 64) cost *= 1 + 0.04 * std::log2(g / 64);
             if (b.lanes == 0 || cost <= best) {
@@ -192,11 +194,16 @@ void unload_block(Block &b)
 // At most two waves to each of the 1,024 SIMDs, which then take rows in turn: the weights are read and
 // the partial sums written once by each (the join's backward, 200,000 rows of 64x(0e,1o,2e) bf16: 345, 289,
 // 304, 313 us at 1, 2, 4, 8 waves to a SIMD; the norm's, 8,192 rows of 4,096 bf16: 54, 43, 45, 53 us).
-int64_t block_groups(const Block &b, int64_t N)
+int64_t block_groups(const Block &b, int64_t N, int waves_per_simd)
 {
     const int64_t rows = b.rows_per_group();
-    return std::max<int64_t>(1, std::min<int64_t>((N + rows - 1) / rows, 2048 / (b.block / 64)));
+    return std::max<int64_t>(1, std::min<int64_t>((N + rows - 1) / rows, 1024 * waves_per_simd / (b.block / 64)));
 }
+
+// The norm's forward has one row to wait for at a time and no partial sums: four waves where a barrier
+// makes several wait together, or where 16-bit elements take more arithmetic by the byte (20,000 rows
+// of 2,048 fp64 113 us against 120 with two, 200,000 of 576 bf16 87 against 108; but fp32 176 against 161).
+int norm_waves(const Block &b) { return b.lanes > 64 || b.elem == 2 ? 4 : 2; }
 
 namespace {
 
@@ -361,7 +368,7 @@ cgtp_status cgtp_norm_forward(const cgtp_block *block, int64_t N, const void *x,
         long ld = (long)x_ld, rows = (long)N;
         Real eps(b, b.cfg.eps);
         void *args[] = {&x, &ld, &w, &u, &rstd, &rows, eps.arg()};
-        run(F.norm_fwd, block_groups(b, N), b.block, args, stream);
+        run(F.norm_fwd, block_groups(b, N, norm_waves(b)), b.block, args, stream);
     });
 }
 

@@ -47,6 +47,6 @@ void build_block(Block &b, const std::string &irreps);
 const Block::Fns &block_for_current_device(Block &b);
 void unload_block(Block &b);
 // workgroups of a pass over N rows; a backward's write one partial of the weight gradients each
-int64_t block_groups(const Block &b, int64_t N);
+int64_t block_groups(const Block &b, int64_t N, int waves_per_simd = 2);
 
 }  // namespace cgtp
