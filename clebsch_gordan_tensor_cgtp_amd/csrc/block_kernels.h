@@ -32,7 +32,7 @@ constexpr int RPB = BLOCK / G;                     // rows of a workgroup at a t
 // channels of 2l+1 components are one run of memory, the runs of the row's lanes follow one another, and
 // what is per channel (weights, gates, their gradients) meets its components in the lane's own
 // registers.  Dealing columns to the lanes and passing gates and their gradients through LDS took 775
-// us for the join's backward on 200,000 rows of 64x(0e,1o,2e) in bf16, this 289 us.  Without such a
+// us for the join's backward on 200,000 rows of 64x(0e,1o,2e) in bf16, this 285 us.  Without such a
 // gate columns are dealt (FLAT): every load is as wide as it can be, and weights are spread over columns once
 // per workgroup (norm, 20,000 rows of 128x(0e,1o,2e,3o) in fp64: 116 us, 136 us by channels).
 // Rows start at any element, so the vector types claim no more than the element's alignment.
