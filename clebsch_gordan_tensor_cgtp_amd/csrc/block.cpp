@@ -152,6 +152,8 @@ void build_block(Block &b, const std::string &irreps)
         ch += ir.mul;
         if (col > (1 << 20)) throw Error(CGTP_ERR_UNSUPPORTED, "block: a row of more than 1048576 columns");
     }
+    if (b.segs.size() > 128)
+        throw Error(CGTP_ERR_UNSUPPORTED, "block: more than 128 runs of equal degrees along a row");
     b.d = (int)col;
     b.c = (int)ch;
     b.elem = b.cfg.dtype == CGTP_F64 ? 8 : b.cfg.dtype == CGTP_F32 ? 4 : 2;

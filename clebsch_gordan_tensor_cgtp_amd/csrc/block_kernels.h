@@ -34,7 +34,7 @@ constexpr int RPB = BLOCK / G;                     // rows of a workgroup at a t
 // registers.  Dealing columns to the lanes and passing gates and their gradients through LDS took 775
 // us for the join's backward on 200,000 rows of 64x(0e,1o,2e) in bf16, this 285 us.  Without such a
 // gate columns are dealt (FLAT): every load is as wide as it can be, and weights are spread over columns once
-// per workgroup (norm, 20,000 rows of 128x(0e,1o,2e,3o) in fp64: 116 us, 136 us by channels).
+// per workgroup (norm, 20,000 rows of 128x(0e,1o,2e,3o) in fp64: 113 us, 136 us by channels).
 // Rows start at any element, so the vector types claim no more than the element's alignment.
 // Channels past an irrep's end read as 0 and are not written.
 

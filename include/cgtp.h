@@ -539,9 +539,9 @@ cgtp_status cgtp_spherical_harmonics(int32_t lmax, cgtp_dtype dtype, int64_t E, 
  *
  * The kernels of a block are compiled for its irreps and configuration when it is created (as a
  * plan's: same compiler, cache and cgtp_last_error log).  Allocates no device memory.
- * CGTP_ERR_UNSUPPORTED: rows of which a lane would hold more than 128 elements (up to 1024 lanes share a
- * row, each of them holds a channel of every run of equal degrees), or whose sums over channels exceed
- * a workgroup's LDS.
+ * CGTP_ERR_UNSUPPORTED: rows of more than 128 runs of equal degrees, of which a lane would hold more than
+ * 128 elements (up to 1024 lanes share a row; with a gate per channel each of them holds a channel of every
+ * run), or whose sums over channels exceed a workgroup's LDS.
  */
 typedef enum cgtp_gate { CGTP_GATE_NONE = 0, CGTP_GATE_ROW = 1, CGTP_GATE_CHANNEL = 2 } cgtp_gate;
 typedef enum cgtp_act { CGTP_ACT_IDENTITY = 0, CGTP_ACT_SIGMOID = 1, CGTP_ACT_SILU = 2, CGTP_ACT_TANH = 3 } cgtp_act;

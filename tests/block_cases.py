@@ -19,6 +19,8 @@ CONFIGS = [("channel", "sigmoid", True, True), ("channel", "silu", False, True),
 # wide scalar rows, over waves of one workgroup in every dtype
 WIDE = [("4100x0e", 7, "bf16"), ("8192x0e", 1, "f16"), ("2050x0e", 9, "f32"), ("1100x0e", 6, "f64"),
         ("40000x0e", 3, "f32")]
+# without a gate per channel: the sums over columns take 144 KB of LDS
+BROAD = "9000x0e+9000x1o"
 # a degree that changes at every channel: one lane holds a row where the gate is per channel
 CHANGING = "+".join(["1x0e+1x1o"] * 20)
 

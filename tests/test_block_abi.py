@@ -75,6 +75,8 @@ def test_block_creation_refusals():
     assert create(b"131073x0e") == UNSUP                      # over 1024 lanes x 128 elements
     many = b"+".join([b"1x0e+1x1o"] * 33)   # with a gate per channel, 132 elements in a lane
     assert create(many, gate=2) == UNSUP and create(many, gate=1) == 0 and L.cgtp_block_destroy(h) == 0
+    assert create(b"+".join([b"1x0e+1x1o"] * 65), gate=1) == UNSUP   # 130 runs of equal degrees
+    assert create(b"30000x0e+6000x1o") == UNSUP               # 48,000 sums over columns: 192 KB of LDS
     assert L.cgtp_block_destroy(None) == 0
     with pytest.raises(cg.CgtpError, match="irreps"):
         cg.Block("nonsense")

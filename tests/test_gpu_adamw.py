@@ -266,6 +266,32 @@ def test_large_tensor(device):
     assert not m[n:].any() and not v[n:].any()
 
 
+@pytest.mark.parametrize("bits", [32, 8])
+def test_a_tensor_past_two_to_the_31(device, bits):
+    """Offsets of 64 bits: the last units of a tensor of 2.2e9 elements step as a tensor of their own does."""
+    import torch
+    n, tail = (1 << 31) + 2048 * 7 + 5, 2048 * 9 + 5
+    gen = torch.Generator(device=device).manual_seed(3)
+    p, g = (torch.zeros(n, dtype=torch.bfloat16, device=device) for _ in range(2))
+    for t in (p, g):
+        t[-tail:] = torch.randn(tail, generator=gen, device=device).to(torch.bfloat16)
+    ps, gs = p[-tail:].clone(), g[-tail:].clone()
+    for q, h, size in ((p, g, n), (ps, gs, tail)):
+        opt = cg.AdamW([size], "bf16", bits)
+        m, v, scales, _ = opt.state(device)
+        norm = cg.grad_norm(opt, [h])
+        for step in (1, 2):
+            cg.adamw_step(opt, [q], [h], m, v, scales, step=step, norm=norm, max_norm=0.5, **HYPER)
+        last = opt.elements - (tail + 2048 - 5)
+        if size == n:
+            kept = (norm, m[last:].clone(), v[last:].clone())
+        else:
+            assert abs(norm.item() / kept[0].item() - 1) < 1e-12
+            assert torch.equal(m[last:], kept[1]) and torch.equal(v[last:], kept[2])
+        del m, v, scales
+    assert torch.equal(p[-tail:], ps) and not p[:-tail].any()
+
+
 def test_state_round_trip(device):
     import torch
     net = Net(device, "f32", 8, False, seed=11)

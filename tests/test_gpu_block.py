@@ -8,7 +8,8 @@ from oracle import block as ob
 from oracle import wigner
 from oracle.irreps import parse_irreps
 
-from block_cases import CHANGING, CONFIGS, DTYPES, EPS, LADDER, ODD, ROW, SHAPES, WIDE, bound, inputs, weight_roundings, wide
+from block_cases import (BROAD, CHANGING, CONFIGS, DTYPES, EPS, LADDER, ODD, ROW, SHAPES, WIDE, bound, inputs,
+                         weight_roundings, wide)
 
 pytestmark = pytest.mark.gpu
 
@@ -105,6 +106,11 @@ def test_join_wide_scalar_rows(device, irreps, rows, dtype):
 def test_join_with_a_degree_for_every_channel(device, dtype):
     for config in (CONFIGS[0], CONFIGS[3]):
         check_join(CHANGING, 300, dtype, config, device, 24)
+
+
+def test_join_whose_sums_fill_the_lds(device):
+    for config in (CONFIGS[3], CONFIGS[5]):
+        check_join(BROAD, 4, "f32", config, device, 25)
 
 
 def test_rows_with_a_pitch_side_by_side_and_unaligned(device):
@@ -295,6 +301,17 @@ def test_rows_past_two_to_the_31(device):
     dx, dw = cg.norm_backward(block, x, None, rstd, u, grad_x=x.new_empty(x.shape))
     dx2, _ = cg.norm_backward(block, x[-40:].clone(), None, rstd2, u2)
     assert torch.equal(dx[-40:], dx2) and torch.isfinite(dw).all()
+    del dx
+    join = make(irreps, "bf16", CONFIGS[0])
+    small = x[-40:].clone()
+    h, v, rf, rh = cg.join_forward(join, x, u, u, None, None, None)
+    h2, v2, rf2, rh2 = cg.join_forward(join, small, u2, u2, None, None, None)
+    assert torch.equal(h[-40:], h2) and torch.equal(v[-40:], v2) and torch.equal(rh[-40:], rh2)
+    need = (True, True, True, False, False, False)
+    got = cg.join_backward(join, x, u, h, u, u, None, None, None, rf, rh, need=need)
+    want = cg.join_backward(join, small, u2, h2, u2, u2, None, None, None, rf2, rh2, need=need)
+    for a, b in zip(got[:3], want[:3]):
+        assert torch.equal(a[-40:], b)
 
 
 def test_same_bits_again_on_another_stream_and_in_a_graph(device):
