@@ -161,6 +161,25 @@ def lib():
     return _lib
 
 
+_compiled = None
+
+
+def _calls():
+    """The compiled calls (csrc/torch/calls.cpp): checks, new outputs and the entry point of the block
+    and optimizer calls (raises if they have not been built)."""
+    global _compiled
+    if _compiled is None:
+        import torch  # noqa: F401  (whose libraries the module links)
+        lib()
+        try:
+            from . import _calls as module
+        except ImportError as e:
+            raise ImportError(f"{HERE}/_calls.so is missing or does not load ({e}): "
+                              "run `python -m clebsch_gordan_tensor_cgtp_amd.build`") from e
+        _compiled = module
+    return _compiled
+
+
 def last_error() -> str:
     return lib().cgtp_last_error().decode()
 
@@ -168,6 +187,13 @@ def last_error() -> str:
 def _check(status):
     if status != 0:
         raise CgtpError(status, last_error())
+
+
+def _answer(got):
+    """What a compiled call returns: its outputs, or the status of a failure."""
+    if type(got) is int:
+        _check(got)
+    return got
 
 
 # ------------------------------------------------------------------------------------ plans
@@ -667,6 +693,9 @@ class Block:
         self.lanes, self.lane_elements = info.lanes, info.elements
         self.torch_dtype = _torch_dtype(dtype)                              # of rows
         self.real_dtype = _torch_dtype("f64" if dtype == "f64" else "f32")  # of statistics and weights
+        self._calls = _calls()
+        self._meta = self._calls.block(h.value, self.d, self.channels, self.gate_width, self.post_norm, self.next_norm,
+                                       DTYPES[dtype])
 
     @property
     def handle(self):
@@ -800,6 +829,10 @@ def _workspace(t, name, nbytes, like, index):
 
 def norm_forward(block: Block, x, w, u=None, rstd=None, need_rstd=True, stream=None):
     """(u, rstd): u = x * rstd(x) * w per channel.  x may have a row pitch; w None stands for ones."""
+    if u is None and rstd is None and stream is None:
+        got = block._calls.norm_forward(block._meta, x, w, need_rstd)
+        if got is not None:
+            return _answer(got)
     if stream is not None:
         return _in_stream(stream, norm_forward, block, x, w, u, rstd, need_rstd)
     dev = _device_index(x, "x")
@@ -817,6 +850,10 @@ def norm_backward(block: Block, x, w, rstd, grad_u, grad_add=None, grad_x=None, 
                   workspace=None, stream=None):
     """(grad_x, grad_w); entries not in ``need`` are None and not computed.  grad_add, when given,
     is added to grad_x (the gradient that reaches x past the norm)."""
+    if grad_x is None and grad_w is None and workspace is None and stream is None:
+        got = block._calls.norm_backward(block._meta, x, w, rstd, grad_u, grad_add, *need)
+        if got is not None:
+            return _answer(got)
     if stream is not None:
         return _in_stream(stream, norm_backward, block, x, w, rstd, grad_u, grad_add, grad_x, grad_w, need, workspace)
     dev = _device_index(x, "x")
@@ -840,6 +877,10 @@ def join_forward(block: Block, res, f, gate, w_post, scale, w_next, h=None, u=No
     """(h, u, rstd_f, rstd_h): h = alpha*res + scale*act(gate)*w_post*f*rstd(f), u = h*rstd(h)*w_next.
     f and gate may have a row pitch (both in one buffer, say); weights given as None are ones; what
     the block's configuration leaves out is None."""
+    if h is None and u is None and rstd_f is None and rstd_h is None and stream is None:
+        got = block._calls.join_forward(block._meta, res, f, gate, w_post, scale, w_next, need_rstd)
+        if got is not None:
+            return _answer(got)
     if stream is not None:
         return _in_stream(stream, join_forward, block, res, f, gate, w_post, scale, w_next, h, u, rstd_f, rstd_h, need_rstd)
     dev = _device_index(f, "f")
@@ -858,12 +899,20 @@ def join_forward(block: Block, res, f, gate, w_post, scale, w_next, h=None, u=No
     return h, u, rstd_f, rstd_h
 
 
+_NO_OUTS = (None,) * 6
+
+
 def join_backward(block: Block, grad_h, grad_u, h, f, gate, w_post, scale, w_next, rstd_f, rstd_h,
-                  outs=(None,) * 6, need=(True,) * 6, workspace=None, stream=None):
+                  outs=_NO_OUTS, need=(True,) * 6, workspace=None, stream=None):
     """(grad_res, grad_f, grad_gate, grad_w_post, grad_scale, grad_w_next) from the gradients of h
     (None: zero) and u and the forward's h and statistics; entries not in ``need``, or that the
     block's configuration leaves out, are None and not computed.  grad_f and grad_gate given in
     ``outs`` may have a row pitch."""
+    if outs is _NO_OUTS and workspace is None and stream is None:
+        got = block._calls.join_backward(block._meta, grad_h, grad_u, h, f, gate, w_post, scale, w_next, rstd_f, rstd_h,
+                                         need)
+        if got is not None:
+            return _answer(got)
     if stream is not None:
         return _in_stream(stream, join_backward, block, grad_h, grad_u, h, f, gate, w_post, scale, w_next, rstd_f,
                           rstd_h, outs, need, workspace)
@@ -918,6 +967,9 @@ class AdamW:
         self.real_dtype = _torch_dtype("f64" if dtype == "f64" else "f32")
         import torch
         self.moment_dtypes = (torch.int8, torch.uint8) if state_bits == 8 else (self.real_dtype, self.real_dtype)
+        self._calls = _calls()
+        self._meta = self._calls.adamw(h.value, self.sizes, self.elements, self.blocks, self.norm_workspace, state_bits,
+                                       DTYPES[dtype])
 
     @property
     def handle(self):
@@ -991,11 +1043,23 @@ def _list(opt, tensors):
     return tensors
 
 
+def _tuple(opt, tensors):
+    if not isinstance(tensors, TensorList):
+        return tuple(tensors)
+    if tensors.opt is not opt:
+        raise ValueError("the tensors were listed for another layout")
+    return tensors.tensors
+
+
 def grad_norm(opt: AdamW, grads, norm=None, workspace=None, stream=None):
     """The global norm of the gradients (a TensorList or tensors; None ones are left out): a device
     float64 tensor of one element."""
     if stream is not None:
         return _in_stream(stream, grad_norm, opt, grads, norm, workspace)
+    if norm is None and workspace is None:
+        got = opt._calls.grad_norm(opt._meta, _tuple(opt, grads))
+        if got is not None:
+            return _answer(got)[0]
     import torch
     grads = _list(opt, grads)
     dev = grads.device_index
@@ -1019,6 +1083,11 @@ def adamw_step(opt: AdamW, params, grads, m, v, scales=None, master=None, *, lr=
         return _in_stream(stream, adamw_step, opt, params, grads, m, v, scales, master, lr=lr, beta1=beta1, beta2=beta2,
                           eps=eps, weight_decay=weight_decay, step=step, max_norm=max_norm, grad_scale=grad_scale,
                           norm=norm, schedule=schedule)
+    got = opt._calls.adamw_step(opt._meta, _tuple(opt, params), _tuple(opt, grads), m, v, scales, master, norm, schedule,
+                                step, lr, beta1, beta2, eps, weight_decay, max_norm, grad_scale)
+    if got is not None:
+        _answer(got)
+        return
     import torch
     params, grads = _list(opt, params), _list(opt, grads)
     if len(params._given) != len(opt.sizes):

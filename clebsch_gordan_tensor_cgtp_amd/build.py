@@ -3,7 +3,8 @@
     python -m clebsch_gordan_tensor_cgtp_amd.build [--warm c1 c2 ...]
 
 The host planner/ABI (C++) and the fixed kernels (HIP) are compiled into one
-shared library next to this file.  ``--warm`` additionally creates the plans
+shared library next to this file, and the compiled calls of the block and
+optimizer entry points (``csrc/torch``) into a Python module beside it.  ``--warm`` additionally creates the plans
 of the named workloads so that their generated modules are compiled by hipRTC
 now and stored in the on-disk cache (``jit_cache`` next to the library).
 """
@@ -16,6 +17,7 @@ import sys
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 LIB = os.path.join(HERE, "libcgtp.so")
+CALLS = os.path.join(HERE, "_calls.so")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 ROCM_INC = os.path.join(os.environ.get("ROCM_PATH", "/opt/rocm"), "include")
@@ -63,7 +65,29 @@ def build(verbose: bool = False) -> str:
         sys.stderr.write(log)
         raise RuntimeError("linking libcgtp.so failed")
     os.replace(tmp, LIB)
+    build_calls(verbose)
     return LIB
+
+
+def build_calls(verbose: bool = False) -> str:
+    """The Python module of the block and optimizer calls (torch's headers, linked against libcgtp)."""
+    import importlib.util
+    import sysconfig
+    torch = os.path.dirname(importlib.util.find_spec("torch").origin)
+    obj = os.path.join(HERE, "_build", "calls.cpp.o")
+    inc = [os.path.join(torch, "include"), os.path.join(torch, "include", "torch", "csrc", "api", "include"),
+           sysconfig.get_paths()["include"], ROCM_INC, os.path.join(ROOT, "include")]
+    tmp = CALLS + f".tmp{os.getpid()}"
+    for cmd in ([HIPCC, "-O2", "-std=c++17", "-fPIC", "-x", "c++", "-D__HIP_PLATFORM_AMD__", "-DUSE_ROCM",
+                 *[f"-I{i}" for i in inc], "-c", os.path.join(HERE, "csrc", "torch", "calls.cpp"), "-o", obj],
+                [HIPCC, "-shared", "-fPIC", obj, "-L" + HERE, "-l:libcgtp.so", "-Wl,-rpath,$ORIGIN",
+                 "-L" + os.path.join(torch, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_hip", "-o", tmp]):
+        rc, log = _compile((cmd, verbose))
+        if rc != 0:
+            sys.stderr.write(log)
+            raise RuntimeError("building _calls.so failed")
+    os.replace(tmp, CALLS)
+    return CALLS
 
 
 def warm(names):
