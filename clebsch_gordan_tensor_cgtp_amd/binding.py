@@ -5,6 +5,10 @@ and the stream (``torch.cuda.current_stream().cuda_stream``); when an output
 tensor is not given, it is allocated here with ``torch.empty`` -- the only
 allocation on the path, and one the library itself never makes.  If
 ``libcgtp.so`` is missing the first call raises: there is no fallback.
+
+The block and optimizer calls (norm, join, AdamW) go through a small compiled module
+(``csrc/torch/calls.cpp``) when their outputs are all new: the same checks, outputs and entry points
+at half the cost of a call.  What it does not take comes back here.
 """
 import ctypes
 import os

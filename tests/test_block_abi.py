@@ -213,3 +213,27 @@ def test_binding_refuses_what_is_not_a_device_tensor():
     with pytest.raises(KeyError):
         cg.Block("4x0e", "f8")
     assert np.isclose(b.eps, 1e-6)
+
+
+def test_compiled_calls_leave_what_they_do_not_take_to_the_binding():
+    """They answer None, and the binding says what is wrong; wrong use of the module itself raises."""
+    torch = pytest.importorskip("torch")
+    b, o = cg.Block("4x0e+2x1o", gate="channel", post_norm=True, next_norm=True), cg.AdamW([4, 3])
+    calls, x, g = b._calls, torch.zeros(2, 10), torch.zeros(2, 6)
+    assert calls.norm_forward(b._meta, x, None, True) is None          # not on a device
+    assert calls.norm_forward(b._meta, "x", None, True) is None
+    assert calls.join_forward(b._meta, x, x, g, None, None, None, True) is None
+    assert calls.join_backward(b._meta, x, x, x, x, g, None, None, None, None, None, (True,) * 6) is None
+    assert calls.norm_backward(b._meta, x, None, None, x, None, True, True) is None
+    assert calls.grad_norm(o._meta, (torch.zeros(4), torch.zeros(3))) is None
+    assert calls.grad_norm(o._meta, (None, None)) is None and calls.grad_norm(o._meta, "ab") is None
+    assert calls.adamw_step(o._meta, (torch.zeros(4),), (None,), x, x, None, None, None, None, 1, *[0.5] * 7) is None
+    for bad in (lambda: calls.norm_forward(b._meta, x, None), lambda: calls.block(1, 2), lambda: calls.adamw(1)):
+        with pytest.raises(TypeError, match="wanted"):
+            bad()
+    with pytest.raises(ValueError):
+        calls.norm_forward(o._meta, x, None, True)                     # another kind of handle
+    with pytest.raises(TypeError, match="CUDA"):
+        cg.join_forward(b, x, x, g, None, None, None)
+    with pytest.raises(ValueError, match="no gradient"):
+        cg.grad_norm(o, [None, None])
