@@ -962,11 +962,7 @@ class AdamW:
         info = AdamWInfo()
         _check(lib().cgtp_adamw_info_get(h, ctypes.byref(info)))
         self.elements, self.blocks, self.norm_workspace = info.elements, info.blocks, info.norm_workspace
-        off, at = [], ctypes.c_int64()
-        for t in range(len(self.sizes)):
-            _check(lib().cgtp_adamw_offset(h, t, ctypes.byref(at)))
-            off.append(at.value)
-        self.offsets = tuple(off)
+        self._offsets = None
         self.torch_dtype = _torch_dtype(dtype)
         self.real_dtype = _torch_dtype("f64" if dtype == "f64" else "f32")
         import torch
@@ -978,6 +974,16 @@ class AdamW:
     @property
     def handle(self):
         return self._h
+
+    @property
+    def offsets(self):
+        if self._offsets is None:
+            at, off = ctypes.c_int64(), []
+            for t in range(len(self.sizes)):
+                _check(lib().cgtp_adamw_offset(self._h, t, ctypes.byref(at)))
+                off.append(at.value)
+            self._offsets = tuple(off)
+        return self._offsets
 
     def state(self, device, params=None):
         """(m, v, scales, master) at the start: zero moments, and master copies of ``params``."""
@@ -1006,33 +1012,30 @@ class AdamW:
 
 
 class TensorList:
-    """Tensors of an AdamW layout (parameters or gradients, None where a gradient is absent), checked,
-    with their addresses as the library takes them.  The tensors are held; the addresses are read
-    again at every use, and tensors that moved are checked again."""
+    """Tensors of an AdamW layout (parameters or gradients, None where a gradient is absent), checked
+    when they are listed and again at every use."""
 
     def __init__(self, opt: AdamW, tensors):
         self.opt, self.tensors = opt, tuple(tensors)
         if len(self.tensors) != len(opt.sizes):
             raise ValueError(f"{len(self.tensors)} tensors, the layout has {len(opt.sizes)}")
         self._given = [t for t in self.tensors if t is not None]
-        self._at = None
         self.device_index = _device_index(self._given[0], "tensor") if self._given else None
-        self.pointers()
+        if self._given and not opt._calls.takes_tensors(opt._meta, self.tensors):
+            self.pointers()
 
     def pointers(self):
-        at = [t.data_ptr() for t in self._given]
-        if at != self._at:
-            for i, (t, n) in enumerate(zip(self.tensors, self.opt.sizes)):
-                if t is None:
-                    continue
-                _dev(t, f"tensor {i}", self.opt.torch_dtype)
-                if t.numel() != n:
-                    raise ValueError(f"tensor {i} has {t.numel()} elements, the layout {n}")
-                if t.get_device() != self.device_index:
-                    raise ValueError(f"tensor {i} is on {t.device}, expected cuda:{self.device_index}")
-            every = [None if t is None else t.data_ptr() for t in self.tensors]
-            self._array, self._at = (ctypes.c_void_p * max(1, len(every)))(*every), at
-        return self._array
+        """The tensors' addresses as the entry points take them."""
+        for i, (t, n) in enumerate(zip(self.tensors, self.opt.sizes)):
+            if t is None:
+                continue
+            _dev(t, f"tensor {i}", self.opt.torch_dtype)
+            if t.numel() != n:
+                raise ValueError(f"tensor {i} has {t.numel()} elements, the layout {n}")
+            if t.get_device() != self.device_index:
+                raise ValueError(f"tensor {i} is on {t.device}, expected cuda:{self.device_index}")
+        at = [None if t is None else t.data_ptr() for t in self.tensors]
+        return (ctypes.c_void_p * max(1, len(at)))(*at)
 
 
 def tensor_list(opt: AdamW, tensors) -> TensorList:

@@ -78,11 +78,13 @@ template <int J, int K, typename S> DEV void load_slot(const S *irrep, int lane,
 {
     const int unit = S_UNIT[J] + lane, left = S_MUL[J] - unit * CV;
     const S *p = irrep + unit * (CV * K);
+    constexpr int LAST = S_MUL[J] % CV;  // channels of an irrep's short last group
     if ((S_UNIT[J] + G) * CV <= S_MUL[J] || left >= CV) {
         load_run<CV * K>(p, x);
     } else {
 #pragma unroll
-        for (int i = 0; i < CV * K; ++i) x[i] = (CV > 1 && i < left * K) ? (R)p[i] : (R)0;
+        for (int i = 0; i < CV * K; ++i) x[i] = (R)0;
+        if (LAST > 0 && left > 0) load_run<LAST * K>(p, x);
     }
 }
 
@@ -90,13 +92,11 @@ template <int J, int K, typename S> DEV void store_slot(S *irrep, int lane, cons
 {
     const int unit = S_UNIT[J] + lane, left = S_MUL[J] - unit * CV;
     S *p = irrep + unit * (CV * K);
-    if ((S_UNIT[J] + G) * CV <= S_MUL[J] || left >= CV) {
+    constexpr int LAST = S_MUL[J] % CV;
+    if ((S_UNIT[J] + G) * CV <= S_MUL[J] || left >= CV)
         store_run<CV * K>(p, x);
-    } else if (CV > 1) {
-#pragma unroll
-        for (int i = 0; i < CV * K; ++i)
-            if (i < left * K) p[i] = (S)x[i];
-    }
+    else if (LAST > 0 && left > 0)
+        store_run<LAST * K>(p, x);
 }
 
 template <int J = 0> DEV void load_cols(const T *row, int lane, R (&x)[EPL])
@@ -269,10 +269,22 @@ constexpr int SUMS = NW > 1 ? 1 : BLOCK / 64;
 constexpr int WIDTH = FLAT ? D : C;
 constexpr int SUM_LDS = SUMS == 1 && !FLAT ? 1 : SUMS * WIDTH;
 
+// v summed over the lanes of a wave that agree in lane % G: halves and rows by the swaps, then rotations
+// inside a row of 16, whose halves, quarters and eighths are equal by then
+DEV R group_sum(R v)
+{
+    if (G < 64) v = swap32(v);
+    if (G < 32) v = swap16(v);
+    if (G < 16) v += dpp<0x128>(v);  // row_ror:8
+    if (G < 8) v += dpp<0x124>(v);
+    if (G < 4) v += dpp<0x122>(v);
+    if (G < 2) v += dpp<0x121>(v);
+    return v;
+}
+
 DEV void write_partial(R (&acc)[NC], int lane, R *lds, R *out)
 {
-#pragma unroll
-    for (int s = G; s < 64; s *= 2) EACH_C(c) acc[c] += __shfl_xor(acc[c], s);
+    EACH_C(c) acc[c] = group_sum(acc[c]);
     if (SUMS == 1 && !FLAT) {
         store_channels(out, lane, acc);
         return;

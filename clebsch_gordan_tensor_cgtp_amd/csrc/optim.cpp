@@ -4,6 +4,7 @@
 #include <algorithm>
 #include <climits>
 #include <cmath>
+#include <iterator>
 #include <memory>
 #include <vector>
 
@@ -78,14 +79,22 @@ struct Extent {
 
 // What is written overlaps nothing else: in the order of their starts, each extent begins after the
 // end of every written one before it, a written one after the end of all.
-void check_extents(std::vector<Extent> &all)
+// Each of the lists mostly comes in that order (tensors of one buffer): it is sorted only if not.
+void check_extents(std::vector<Extent> &state, std::vector<Extent> &params, std::vector<Extent> &grads)
 {
     auto at = [](const Extent &e) { return reinterpret_cast<uintptr_t>(e.p); };
-    all.erase(std::remove_if(all.begin(), all.end(), [](const Extent &e) { return !e.p || !e.n; }), all.end());
-    std::sort(all.begin(), all.end(), [&](const Extent &a, const Extent &b) { return at(a) < at(b); });
+    auto before = [&](const Extent &a, const Extent &b) { return at(a) < at(b); };
+    std::vector<Extent> both, all;
+    for (auto *list : {&state, &params, &grads})
+        if (!std::is_sorted(list->begin(), list->end(), before)) std::sort(list->begin(), list->end(), before);
+    both.reserve(params.size() + grads.size());
+    all.reserve(both.capacity() + state.size());
+    std::merge(params.begin(), params.end(), grads.begin(), grads.end(), std::back_inserter(both), before);
+    std::merge(both.begin(), both.end(), state.begin(), state.end(), std::back_inserter(all), before);
     const Extent *any = nullptr, *written = nullptr;  // the ones that reach furthest
     auto ends = [&](const Extent *e) { return at(*e) + e->n; };
     for (const Extent &e : all) {
+        if (!e.p || !e.n) continue;
         const Extent *last = e.written ? any : written;
         if (last && ends(last) > at(e)) require(false, std::string(e.name) + " overlaps " + last->name);
         if (!any || ends(&e) > ends(any)) any = &e;
@@ -218,22 +227,24 @@ cgtp_status cgtp_adamw_step(const cgtp_adamw *opt, void *const *params, const vo
         require(codes || !scales, "scales given to moments in 32 bits");
         if (o.cfg.master) require_ptr(master, "master", 16);
         require(o.cfg.master || !master, "master given to an optimizer without master copies");
-        std::vector<Extent> all = {{m, mbytes, true, "m"},
-                                   {v, mbytes, true, "v"},
-                                   {scales, codes ? el / kScaleBlock * 8 : 0, true, "scales"},
-                                   {master, master ? el * 4 : 0, true, "master"},
-                                   {norm, norm ? (size_t)8 : 0, false, "norm"},
-                                   {schedule, schedule ? (size_t)32 : 0, false, "schedule"}};
-        all.reserve(6 + 2 * o.sizes.size());
+        std::vector<Extent> state = {{m, mbytes, true, "m"},
+                                     {v, mbytes, true, "v"},
+                                     {scales, codes ? el / kScaleBlock * 8 : 0, true, "scales"},
+                                     {master, master ? el * 4 : 0, true, "master"},
+                                     {norm, norm ? (size_t)8 : 0, false, "norm"},
+                                     {schedule, schedule ? (size_t)32 : 0, false, "schedule"}};
+        std::vector<Extent> tensors, gradients;
+        tensors.reserve(o.sizes.size());
+        gradients.reserve(o.sizes.size());
         for (size_t i = 0; i < o.sizes.size(); ++i) {
             if (o.sizes[i] == 0 || !grads[i]) continue;
             const size_t bytes = (size_t)o.sizes[i] * o.elem;
             if (!params[i] || reinterpret_cast<uintptr_t>(params[i]) % o.elem)
                 require(false, "params[" + std::to_string(i) + "] is NULL or not aligned to its elements");
-            all.push_back({params[i], bytes, true, "a tensor"});
-            all.push_back({grads[i], bytes, false, "a gradient"});
+            tensors.push_back({params[i], bytes, true, "a tensor"});
+            gradients.push_back({grads[i], bytes, false, "a gradient"});
         }
-        check_extents(all);
+        check_extents(state, tensors, gradients);
         StepScalars s{h.max_norm, h.grad_scale, h.lr, h.beta1, h.beta2, h.eps, h.weight_decay, 1, 1};
         if (!schedule) {
             s.bias1 = 1 - std::pow(h.beta1, (double)h.step);

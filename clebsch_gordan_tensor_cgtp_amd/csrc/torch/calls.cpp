@@ -320,6 +320,19 @@ bool addresses(const AdamWMeta *m, const Args &in, PyObject *tuple, bool optiona
     return true;
 }
 
+// (layout, tensors, None among them allowed) -> whether the layout's calls take them
+PyObject *takes_tensors(PyObject *, PyObject *const *a, Py_ssize_t n_args)
+{
+    HANDLE_TH_ERRORS
+    if (!takes(n_args, 2)) return nullptr;
+    const AdamWMeta *m = adamw_of(a[0]);
+    if (!m) return nullptr;
+    Args in(first_of(a[1]));
+    std::vector<void *> at;
+    return PyBool_FromLong(in.fine && addresses(m, in, a[1], true, &at));
+    END_HANDLE_TH_ERRORS
+}
+
 // (layout, gradients) -> (norm,)
 PyObject *grad_norm(PyObject *, PyObject *const *a, Py_ssize_t n_args)
 {
@@ -370,7 +383,8 @@ PyObject *adamw_step(PyObject *, PyObject *const *a, Py_ssize_t n_args)
 #define CGTP_CALL(name) {#name, (PyCFunction)(void (*)(void))name, METH_FASTCALL, nullptr}
 PyMethodDef kMethods[] = {CGTP_CALL(block),        CGTP_CALL(norm_forward),  CGTP_CALL(norm_backward),
                           CGTP_CALL(join_forward), CGTP_CALL(join_backward), CGTP_CALL(adamw),
-                          CGTP_CALL(grad_norm),    CGTP_CALL(adamw_step),    {nullptr, nullptr, 0, nullptr}};
+                          CGTP_CALL(grad_norm),    CGTP_CALL(adamw_step),    CGTP_CALL(takes_tensors),
+                          {nullptr, nullptr, 0, nullptr}};
 #undef CGTP_CALL
 
 PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_calls", nullptr, -1, kMethods, nullptr, nullptr, nullptr, nullptr};
