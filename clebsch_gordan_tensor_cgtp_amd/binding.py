@@ -678,7 +678,8 @@ def _torch_dtype(dtype: str):
 
 class Block:
     """The row norm at a block's entry and the join at its end (norm, gate, residual sum, the next
-    block's norm) for one irreps row and configuration; compiled when it is created."""
+    block's norm) for one irreps row and configuration; compiled when it is created.  Like a Plan, it is
+    closed (or dropped) only after the kernels launched with it have finished; block_for keeps it."""
 
     def __init__(self, irreps, dtype="f32", gate=None, act="sigmoid", post_norm=False, next_norm=False, eps=1e-6,
                  alpha=1.0):
@@ -710,6 +711,7 @@ class Block:
         return lib().cgtp_block_source(self._h).decode()
 
     def close(self):
+        self._meta = None
         if self._h is not None and _lib is not None:
             lib().cgtp_block_destroy(self._h)
         self._h = None
@@ -1000,6 +1002,7 @@ class AdamW:
         return m, v, scales, master
 
     def close(self):
+        self._meta = None
         if self._h is not None and _lib is not None:
             lib().cgtp_adamw_destroy(self._h)
         self._h = None

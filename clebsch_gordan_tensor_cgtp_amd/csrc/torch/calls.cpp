@@ -145,6 +145,7 @@ PyObject *norm_forward(PyObject *, PyObject *const *a, Py_ssize_t n_args)
 {
     HANDLE_TH_ERRORS
     if (!takes(n_args, 4)) return nullptr;
+    if (a[0] == Py_None) Py_RETURN_NONE;  // closed
     const BlockMeta *m = block_of(a[0]);
     if (!m) return nullptr;
     const at::Tensor *x = tensor(a[1]);
@@ -173,6 +174,7 @@ PyObject *norm_backward(PyObject *, PyObject *const *a, Py_ssize_t n_args)
 {
     HANDLE_TH_ERRORS
     if (!takes(n_args, 8)) return nullptr;
+    if (a[0] == Py_None) Py_RETURN_NONE;  // closed
     const BlockMeta *m = block_of(a[0]);
     if (!m) return nullptr;
     const at::Tensor *x = tensor(a[1]);
@@ -204,6 +206,7 @@ PyObject *join_forward(PyObject *, PyObject *const *a, Py_ssize_t n_args)
 {
     HANDLE_TH_ERRORS
     if (!takes(n_args, 8)) return nullptr;
+    if (a[0] == Py_None) Py_RETURN_NONE;  // closed
     const BlockMeta *m = block_of(a[0]);
     if (!m) return nullptr;
     const at::Tensor *f = tensor(a[2]);
@@ -233,6 +236,7 @@ PyObject *join_backward(PyObject *, PyObject *const *a, Py_ssize_t n_args)
 {
     HANDLE_TH_ERRORS
     if (!takes(n_args, 12)) return nullptr;
+    if (a[0] == Py_None) Py_RETURN_NONE;  // closed
     const BlockMeta *m = block_of(a[0]);
     if (!m) return nullptr;
     const at::Tensor *f = tensor(a[4]);
@@ -325,6 +329,7 @@ PyObject *takes_tensors(PyObject *, PyObject *const *a, Py_ssize_t n_args)
 {
     HANDLE_TH_ERRORS
     if (!takes(n_args, 2)) return nullptr;
+    if (a[0] == Py_None) Py_RETURN_NONE;  // closed
     const AdamWMeta *m = adamw_of(a[0]);
     if (!m) return nullptr;
     Args in(first_of(a[1]));
@@ -338,6 +343,7 @@ PyObject *grad_norm(PyObject *, PyObject *const *a, Py_ssize_t n_args)
 {
     HANDLE_TH_ERRORS
     if (!takes(n_args, 2)) return nullptr;
+    if (a[0] == Py_None) Py_RETURN_NONE;  // closed
     const AdamWMeta *m = adamw_of(a[0]);
     if (!m) return nullptr;
     const at::Tensor *first = first_of(a[1]);
@@ -358,6 +364,7 @@ PyObject *adamw_step(PyObject *, PyObject *const *a, Py_ssize_t n_args)
 {
     HANDLE_TH_ERRORS
     if (!takes(n_args, 17)) return nullptr;
+    if (a[0] == Py_None) Py_RETURN_NONE;  // closed
     const AdamWMeta *m = adamw_of(a[0]);
     if (!m) return nullptr;
     Args in(first_of(a[1]));

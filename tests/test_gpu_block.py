@@ -363,3 +363,18 @@ def test_same_bits_again_on_another_stream_and_in_a_graph(device):
         torch.cuda.synchronize()
         for a, b in zip(out, want):
             assert torch.equal(a, b), f"replay {rep}"
+
+
+def test_closed_handles_are_refused(device):
+    import torch
+    b, o = cg.Block("4x0e", "f32"), cg.AdamW([4])
+    x, p = torch.zeros(3, 4, device=device), torch.zeros(4, device=device)
+    m, v, _, _ = o.state(device)
+    cg.norm_forward(b, x, None)
+    torch.cuda.synchronize()   # a block's kernels end before their code is unloaded
+    b.close()
+    o.close()
+    with pytest.raises(cg.CgtpError, match="block is NULL"):
+        cg.norm_forward(b, x, None)
+    with pytest.raises(cg.CgtpError, match="NULL"):
+        cg.adamw_step(o, [p], [p.clone()], m, v, step=1)
