@@ -1127,6 +1127,10 @@ def adamw_schedule(schedule, beta1=0.9, beta2=0.999, stream=None):
 
 def adamw_state_read(opt: AdamW, m, v, scales, m_out=None, v_out=None, stream=None):
     """The values that 8-bit moments stand for: (m, v) in float32."""
+    if m_out is None and v_out is None and stream is None:
+        got = opt._calls.adamw_state_read(opt._meta, m, v, scales)
+        if got is not None:
+            return _answer(got)
     if stream is not None:
         return _in_stream(stream, adamw_state_read, opt, m, v, scales, m_out, v_out)
     import torch

@@ -387,10 +387,32 @@ PyObject *adamw_step(PyObject *, PyObject *const *a, Py_ssize_t n_args)
     END_HANDLE_TH_ERRORS
 }
 
+// (layout, m, v, scales) -> (m, v) in float
+PyObject *adamw_state_read(PyObject *, PyObject *const *a, Py_ssize_t n_args)
+{
+    HANDLE_TH_ERRORS
+    if (!takes(n_args, 4)) return nullptr;
+    if (a[0] == Py_None) Py_RETURN_NONE;  // closed
+    const AdamWMeta *m = adamw_of(a[0]);
+    if (!m) return nullptr;
+    const at::Tensor *first = tensor(a[1]);
+    Args in(first);
+    if (!in.fine || !m->codes) Py_RETURN_NONE;
+    const void *mp = in.at(a[1], at::kChar, {m->elements}), *vp = in.at(a[2], at::kByte, {m->elements});
+    const void *sc = in.at(a[3], at::kFloat, {2, m->blocks});
+    if (!in.fine) Py_RETURN_NONE;
+    at::Tensor mo = at::empty({m->elements}, first->options().dtype(at::kFloat)), vo = at::empty_like(mo);
+    return answer(cgtp_adamw_state_read(m->opt, mp, vp, static_cast<const float *>(sc), static_cast<float *>(address(mo)),
+                                        static_cast<float *>(address(vo)), in.stream()),
+                  {&mo, &vo});
+    END_HANDLE_TH_ERRORS
+}
+
 #define CGTP_CALL(name) {#name, (PyCFunction)(void (*)(void))name, METH_FASTCALL, nullptr}
 PyMethodDef kMethods[] = {CGTP_CALL(block),        CGTP_CALL(norm_forward),  CGTP_CALL(norm_backward),
                           CGTP_CALL(join_forward), CGTP_CALL(join_backward), CGTP_CALL(adamw),
                           CGTP_CALL(grad_norm),    CGTP_CALL(adamw_step),    CGTP_CALL(takes_tensors),
+                          CGTP_CALL(adamw_state_read),
                           {nullptr, nullptr, 0, nullptr}};
 #undef CGTP_CALL
 

@@ -229,6 +229,7 @@ def test_compiled_calls_leave_what_they_do_not_take_to_the_binding():
     assert calls.takes_tensors(o._meta, (torch.zeros(4), torch.zeros(3))) is False
     assert calls.grad_norm(o._meta, (None, None)) is None and calls.grad_norm(o._meta, "ab") is None
     assert calls.adamw_step(o._meta, (torch.zeros(4),), (None,), x, x, None, None, None, None, 1, *[0.5] * 7) is None
+    assert calls.adamw_state_read(o._meta, x, x, x) is None
     for bad in (lambda: calls.norm_forward(b._meta, x, None), lambda: calls.block(1, 2), lambda: calls.adamw(1)):
         with pytest.raises(TypeError, match="wanted"):
             bad()
