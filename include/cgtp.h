@@ -538,7 +538,8 @@ cgtp_status cgtp_spherical_harmonics(int32_t lmax, cgtp_dtype dtype, int64_t E, 
  * u is formed from h before that rounding.
  *
  * The kernels of a block are compiled for its irreps and configuration when it is created (as a
- * plan's: same compiler, cache and cgtp_last_error log).  Allocates no device memory.
+ * plan's: same compiler, cache and cgtp_last_error log) and loaded on a device at the first launch there, which
+ * a captured graph has to come after.  Allocates no device memory.
  * CGTP_ERR_UNSUPPORTED: rows of more than 128 runs of equal degrees, of which a lane would hold more than
  * 128 elements (up to 1024 lanes share a row; with a gate per channel each of them holds a channel of every
  * run), or whose sums over channels exceed a workgroup's LDS.
