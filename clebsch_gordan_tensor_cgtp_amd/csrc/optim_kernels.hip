@@ -110,9 +110,10 @@ template <int CTRL> __device__ __forceinline__ unsigned dpp_max(unsigned v)
     return max(v, (unsigned)__builtin_amdgcn_mov_dpp((int)v, CTRL, 15, 15, false));
 }
 
-// Largest magnitude of the values of `LANES` neighbouring lanes.  Compared as bit patterns, in
-// which an infinity is above every number and a NaN above that: either reaches the scale, and
-// the block then reads as NaN.
+// Largest magnitude of the values of `LANES` neighbouring lanes, NaN where one of them is not finite:
+// the scale is NaN then, the codes are 0 and the block reads as NaN.  (An infinite scale would not do: a
+// second moment's codes above 0 would read as infinite, and their weights stop without a sign.)
+// Compared as bit patterns, in which an infinity is above every number and a NaN above that.
 template <int LANES, int N> __device__ __forceinline__ float block_most(const float (&x)[N])
 {
     unsigned most = 0;
@@ -123,6 +124,7 @@ template <int LANES, int N> __device__ __forceinline__ float block_most(const fl
     most = dpp_max<0x4E>(most);   // quad_perm 2,3,0,1
     most = dpp_max<0x141>(most);  // row_half_mirror
     if (LANES == 16) most = dpp_max<0x140>(most);  // row_mirror
+    if (most >= 0x7f800000u) return __builtin_nanf("");
     const float a = __uint_as_float(most);
     return a < 1.17549435e-38f ? 0.0f : a;  // below it 1 / a is infinite
 }
@@ -149,7 +151,7 @@ template <bool SIGNED, int N> __device__ __forceinline__ void codes_of(const flo
     }
 #pragma unroll
     for (int j = 0; j < N; ++j) {
-        // NaN becomes 0: the block's scale is NaN or infinite then
+        // NaN becomes 0: the block's scale is NaN then
         q[j] = fminf(fmaxf(q[j], !SIGNED && x[j] > 0.0f && most > 0.0f ? 1.0f : 0.0f), top);
         if (SIGNED && x[j] < 0.0f) q[j] = -q[j];
     }

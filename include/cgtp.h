@@ -638,7 +638,9 @@ cgtp_status cgtp_join_backward(const cgtp_block *block, int64_t N, const void *g
  * state_bits 32: m, v float (double for CGTP_F64).  state_bits 8: m int8, v uint8 codes and scales
  * [2][blocks] float, one for 64 values each: m = scales[0] sign (code / 127)^2, v = s^2 with
  * s = scales[1] (code / 255)^2; a code is the nearest one, and never 0 for a v above 0; all zeros are the start.
- * A block that holds a value that is not finite reads as NaN.  master = 1 (16-bit tensors): `master`
+ * A block that holds a value that is not finite reads as NaN, both in the step and through
+ * cgtp_adamw_state_read; a gradient whose square overflows a float (above 1.8e19 after its scaling and
+ * clipping) makes such a value.  master = 1 (16-bit tensors): `master`
  * [elements] float holds the weights, and the tensors receive its rounding; without it the 16-bit tensors
  * are the weights and are rounded to nearest each step.
  * m, v, master: 16-byte aligned.  Arithmetic is float (double for CGTP_F64).

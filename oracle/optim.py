@@ -23,9 +23,12 @@ def clip_factor(norm, max_norm, grad_scale=1.0):
 
 
 def codes(x, top, signed):
-    """(codes, scales) of an array of whole blocks."""
+    """(codes, scales) of an array of whole blocks; NaN and codes of 0 for a block with a value that is
+    not finite."""
     f = x.dtype.type
     a = np.abs(x).reshape(-1, BLOCK)
+    finite = np.isfinite(a).all(1)
+    a = np.where(finite[:, None], a, f(0))
     most = a.max(1)
     most = np.where(most < np.finfo(np.float32).tiny, f(0), most)
     inv = np.where(most > 0, f(1) / np.where(most > 0, most, f(1)), f(0))
@@ -33,7 +36,7 @@ def codes(x, top, signed):
     if not signed:
         q = np.where((a > 0) & (most > 0)[:, None], np.maximum(q, f(1)), q)
     q = q.reshape(-1)
-    return (np.where(x < 0, -q, q) if signed else q).astype(np.int32), most
+    return (np.where(x < 0, -q, q) if signed else q).astype(np.int32), np.where(finite, most, f(np.nan))
 
 
 def values(q, most, top):
