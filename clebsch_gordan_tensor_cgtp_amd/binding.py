@@ -40,8 +40,8 @@ EXPORTS = ("cgtp_plan_create", "cgtp_plan_destroy", "cgtp_plan_info_get", "cgtp_
            "cgtp_block_create", "cgtp_block_destroy", "cgtp_block_info_get", "cgtp_block_source",
            "cgtp_block_workspace_size", "cgtp_norm_forward", "cgtp_norm_backward", "cgtp_join_forward",
            "cgtp_join_backward", "cgtp_adamw_create", "cgtp_adamw_destroy", "cgtp_adamw_info_get", "cgtp_adamw_offset",
-           "cgtp_grad_norm", "cgtp_adamw_step", "cgtp_adamw_schedule", "cgtp_adamw_state_read",
-           "cgtp_adamw_state_write")
+           "cgtp_grad_norm", "cgtp_adamw_step", "cgtp_adamw_schedule", "cgtp_adamw_schedule_norm",
+           "cgtp_adamw_state_read", "cgtp_adamw_state_write")
 _STRING_RESULTS = ("cgtp_last_error", "cgtp_plan_source", "cgtp_plan_radial_source", "cgtp_plan_uvw_backward_source",
                    "cgtp_plan_conv_uvw_backward_source", "cgtp_block_source")
 
@@ -156,6 +156,7 @@ def lib():
         L.cgtp_grad_norm.argtypes = [vp, vp, vp, vp, sz, vp]
         L.cgtp_adamw_step.argtypes = [vp] * 7 + [ctypes.POINTER(AdamWHyper), vp, vp, vp]
         L.cgtp_adamw_schedule.argtypes = [vp, dbl, dbl, vp]
+        L.cgtp_adamw_schedule_norm.argtypes = [vp, dbl, dbl, vp, dbl, vp]
         L.cgtp_adamw_state_read.argtypes = [vp] * 7
         L.cgtp_adamw_state_write.argtypes = [vp] * 7
         for name in EXPORTS:
@@ -1088,7 +1089,8 @@ def adamw_step(opt: AdamW, params, grads, m, v, scales=None, master=None, *, lr=
     """One AdamW step in place: params, m, v (and scales, master).  ``step`` counts from 1; with
     ``norm`` (as of grad_norm) a step whose norm is not finite changes nothing, and max_norm > 0
     clips by it.  ``schedule``: a device float64 tensor {step, lr, 1 - beta1^step, 1 - beta2^step}
-    in the place of ``step`` and ``lr`` (adamw_schedule advances it)."""
+    in the place of ``step`` and ``lr`` (adamw_schedule advances it; where steps may be skipped, give it
+    the same ``norm`` and ``grad_scale``)."""
     if stream is not None:
         return _in_stream(stream, adamw_step, opt, params, grads, m, v, scales, master, lr=lr, beta1=beta1, beta2=beta2,
                           eps=eps, weight_decay=weight_decay, step=step, max_norm=max_norm, grad_scale=grad_scale,
@@ -1114,14 +1116,16 @@ def adamw_step(opt: AdamW, params, grads, m, v, scales=None, master=None, *, lr=
         _addr_or_null(schedule, "schedule", torch.float64, (4,), dev), _raw_stream(dev)))
 
 
-def adamw_schedule(schedule, beta1=0.9, beta2=0.999, stream=None):
-    """Advance a device schedule {step, lr, 1 - beta1^step, 1 - beta2^step} by one step."""
+def adamw_schedule(schedule, beta1=0.9, beta2=0.999, stream=None, norm=None, grad_scale=1.0):
+    """Advance a device schedule {step, lr, 1 - beta1^step, 1 - beta2^step} by one step.  With the ``norm``
+    and ``grad_scale`` that the step is given after it, a step that changes nothing is not counted."""
     if stream is not None:
-        return _in_stream(stream, adamw_schedule, schedule, beta1, beta2)
+        return _in_stream(stream, adamw_schedule, schedule, beta1, beta2, norm=norm, grad_scale=grad_scale)
     import torch
     dev = _device_index(schedule, "schedule")
-    _check(lib().cgtp_adamw_schedule(_addr(schedule, "schedule", torch.float64, (4,), dev), beta1, beta2,
-                                     _raw_stream(dev)))
+    _check(lib().cgtp_adamw_schedule_norm(_addr(schedule, "schedule", torch.float64, (4,), dev), beta1, beta2,
+                                          _addr_or_null(norm, "norm", torch.float64, (1,), dev), grad_scale,
+                                          _raw_stream(dev)))
     return schedule
 
 

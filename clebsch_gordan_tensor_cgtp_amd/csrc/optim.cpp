@@ -260,10 +260,20 @@ cgtp_status cgtp_adamw_step(const cgtp_adamw *opt, void *const *params, const vo
 
 cgtp_status cgtp_adamw_schedule(double *schedule, double beta1, double beta2, void *stream)
 {
+    return cgtp_adamw_schedule_norm(schedule, beta1, beta2, nullptr, 1, stream);
+}
+
+cgtp_status cgtp_adamw_schedule_norm(double *schedule, double beta1, double beta2, const double *norm,
+                                     double grad_scale, void *stream)
+{
     return guarded([&] {
         require_ptr(schedule, "schedule", 8);
         require(beta1 >= 0 && beta1 < 1 && beta2 >= 0 && beta2 < 1, "betas must lie in [0, 1)");
-        check_hip(launch_schedule(schedule, beta1, beta2, static_cast<hipStream_t>(stream)), "schedule launch");
+        require(std::isfinite(grad_scale), "grad_scale must be finite");
+        if (norm) require_ptr(norm, "norm", 8);
+        require_disjoint(schedule, 32, "schedule", norm, 8, "norm");
+        check_hip(launch_schedule(schedule, beta1, beta2, norm, grad_scale, static_cast<hipStream_t>(stream)),
+                  "schedule launch");
     });
 }
 

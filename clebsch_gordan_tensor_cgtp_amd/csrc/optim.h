@@ -49,6 +49,7 @@ hipError_t launch_state_read(const void *m, const void *v, const float *scales, 
                              float *v_out, hipStream_t st);
 hipError_t launch_state_write(const float *m_in, const float *v_in, int64_t elements, void *m, void *v, float *scales,
                               hipStream_t st);
-hipError_t launch_schedule(double *schedule, double beta1, double beta2, hipStream_t st);
+hipError_t launch_schedule(double *schedule, double beta1, double beta2, const double *norm, double grad_scale,
+                           hipStream_t st);
 
 }  // namespace cgtp

@@ -166,6 +166,10 @@ template <bool SIGNED> __device__ __forceinline__ float value_of(float code, flo
 // ------------------------------------------------------------------------------------------
 // the step
 
+// What decides whether a step is taken, for the step and for the schedule that counts it.
+__device__ __forceinline__ double scaled_norm(const double *norm, double grad_scale) { return fabs(grad_scale) * *norm; }
+__device__ __forceinline__ bool is_finite(double n) { return fabs(n) < __builtin_inf(); }
+
 // Bounded by HBM: 28 bytes an element in 32 bits, 16.25 in 8 bits (f32 tensors).  What is read and
 // written once bypasses the last-level cache, and the units are taken from the last one down, so that of
 // the gradients, which the norm has just read from the first one up, the end is still there: 111.6M f32
@@ -187,8 +191,8 @@ __global__ void __launch_bounds__(256) adamw_kernel(const TensorTable t, const M
 
     double factor = s.grad_scale;
     if (norm) {
-        const double n = fabs(s.grad_scale) * *norm;
-        if (!(n < __builtin_inf())) return;  // a gradient is not finite: nothing is changed
+        const double n = scaled_norm(norm, s.grad_scale);
+        if (!is_finite(n)) return;  // a gradient is not finite: nothing is changed
         if (s.max_norm > 0 && n > s.max_norm) factor *= s.max_norm / n;
     }
     double lr = s.lr, bias1 = s.bias1, bias2 = s.bias2;
@@ -378,10 +382,11 @@ __global__ void __launch_bounds__(256) state_write_kernel(const float *m_in, con
     }
 }
 
-// {step, lr, 1 - b1^step, 1 - b2^step}: one more step
-__global__ void schedule_kernel(double *schedule, double beta1, double beta2)
+// {step, lr, 1 - b1^step, 1 - b2^step}: one more step, if it is one that the moments take
+__global__ void schedule_kernel(double *schedule, double beta1, double beta2, const double *norm, double grad_scale)
 {
     if (threadIdx.x != 0) return;
+    if (norm && !is_finite(scaled_norm(norm, grad_scale))) return;
     const double step = schedule[0] + 1;
     schedule[0] = step;
     schedule[2] = 1 - pow(beta1, step);
@@ -474,9 +479,10 @@ hipError_t launch_state_write(const float *m_in, const float *v_in, int64_t elem
     return hipGetLastError();
 }
 
-hipError_t launch_schedule(double *schedule, double beta1, double beta2, hipStream_t st)
+hipError_t launch_schedule(double *schedule, double beta1, double beta2, const double *norm, double grad_scale,
+                           hipStream_t st)
 {
-    schedule_kernel<<<dim3(1), dim3(64), 0, st>>>(schedule, beta1, beta2);
+    schedule_kernel<<<dim3(1), dim3(64), 0, st>>>(schedule, beta1, beta2, norm, grad_scale);
     return hipGetLastError();
 }
 

@@ -105,7 +105,7 @@ def train(steps=60, bits=32, lr=1e-2, max_norm=1.0, graph=True, device="cuda:0",
         torch.sub(u, want, out=off)
         net.backward(off * (2.0 / off.numel()), kept)
         norm = cg.grad_norm(opt, grads)
-        cg.adamw_schedule(schedule)
+        cg.adamw_schedule(schedule, norm=norm)
         cg.adamw_step(opt, params, grads, m, v, scales, master, weight_decay=1e-4, max_norm=max_norm, norm=norm,
                       schedule=schedule)
 

@@ -649,7 +649,7 @@ cgtp_status cgtp_join_backward(const cgtp_block *block, int64_t N, const void *g
  * gradient has its type; any alignment to it).  A tensor whose gradient is NULL is left as it is, its moments too.
  * step counts from 1.  For captured graphs, `schedule` (device, double[4]: step, lr, 1 - beta1^step,
  * 1 - beta2^step; NULL otherwise) takes the place of hyper's lr and step; cgtp_adamw_schedule adds
- * one to its step and sets the last two.  `norm` is a device double, as of cgtp_grad_norm, or NULL.
+ * one to its step and sets the last two, cgtp_adamw_schedule_norm only where the norm is finite.  `norm` is a device double, as of cgtp_grad_norm, or NULL.
  * Errors: CGTP_ERR_INVALID_ARG (also where memory that is written overlaps any other),
  * CGTP_ERR_UNSUPPORTED (8-bit moments of double precision tensors).
  */
@@ -688,6 +688,10 @@ cgtp_status cgtp_adamw_step(const cgtp_adamw *opt, void *const *params, const vo
                             float *scales, float *master, const cgtp_adamw_hyper *hyper, const double *norm,
                             const double *schedule, void *stream);
 cgtp_status cgtp_adamw_schedule(double *schedule, double beta1, double beta2, void *stream);
+/* The same where steps may be skipped: with the norm and grad_scale that the step is given after it, a
+ * schedule whose step will change nothing stays as it is (norm NULL: it advances). */
+cgtp_status cgtp_adamw_schedule_norm(double *schedule, double beta1, double beta2, const double *norm,
+                                     double grad_scale, void *stream);
 /* 8-bit moments as float values (`elements` each; either output may be NULL) and back. */
 cgtp_status cgtp_adamw_state_read(const cgtp_adamw *opt, const void *m, const void *v, const float *scales,
                                   float *m_out, float *v_out, void *stream);
