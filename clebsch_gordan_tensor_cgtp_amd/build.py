@@ -4,9 +4,10 @@
 
 The host planner/ABI (C++) and the fixed kernels (HIP) are compiled into one
 shared library next to this file, and the compiled calls of the block and
-optimizer entry points (``csrc/torch``) into a Python module beside it.  ``--warm`` additionally creates the plans
-of the named workloads so that their generated modules are compiled by hipRTC
-now and stored in the on-disk cache (``jit_cache`` next to the library).
+optimizer entry points (``csrc/torch``) into a Python module beside it (left out
+where there is no torch).  ``--warm`` additionally creates the plans of the named
+workloads so that their generated modules are compiled by hipRTC now and stored
+in the on-disk cache (``jit_cache`` next to the library).
 """
 import argparse
 import glob
@@ -69,11 +70,16 @@ def build(verbose: bool = False) -> str:
     return LIB
 
 
-def build_calls(verbose: bool = False) -> str:
-    """The Python module of the block and optimizer calls (torch's headers, linked against libcgtp)."""
+def build_calls(verbose: bool = False):
+    """The Python module of the block and optimizer calls (torch's headers, linked against libcgtp); None
+    where there is no torch, which the library itself does not need."""
     import importlib.util
     import sysconfig
-    torch = os.path.dirname(importlib.util.find_spec("torch").origin)
+    spec = importlib.util.find_spec("torch")
+    if spec is None or spec.origin is None:
+        print("torch is not installed: libcgtp.so is built, the Python calls (_calls.so) are not", file=sys.stderr)
+        return None
+    torch = os.path.dirname(spec.origin)
     obj = os.path.join(HERE, "_build", "calls.cpp.o")
     inc = [os.path.join(torch, "include"), os.path.join(torch, "include", "torch", "csrc", "api", "include"),
            sysconfig.get_paths()["include"], ROCM_INC, os.path.join(ROOT, "include")]
