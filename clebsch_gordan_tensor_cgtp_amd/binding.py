@@ -750,6 +750,12 @@ def _in_stream(stream, call, *args, **kw):
         return call(*args, **kw)
 
 
+def _current(index):
+    """The tensors' device as the current one: launches go there, and a block's code is loaded there."""
+    import torch
+    return torch.cuda.device(index)
+
+
 def _raw_stream(index):
     global _current_raw_stream
     if _current_raw_stream is None:
@@ -848,8 +854,9 @@ def norm_forward(block: Block, x, w, u=None, rstd=None, need_rstd=True, stream=N
     xp, x_ld = _rows(x, "x", dt, rows, dev)
     u, up = _output(u, True, "u", dt, rows, x, dev)
     rstd, rp = _output(rstd, need_rstd, "rstd", rt, (n,), x, dev)
-    _check(lib().cgtp_norm_forward(block.handle, n, xp, x_ld, _addr_or_null(w, "w", rt, (block.channels,), dev), up, rp,
-                                   _raw_stream(dev)))
+    with _current(dev):
+        _check(lib().cgtp_norm_forward(block.handle, n, xp, x_ld, _addr_or_null(w, "w", rt, (block.channels,), dev), up,
+                                       rp, _raw_stream(dev)))
     return u, rstd
 
 
@@ -872,10 +879,11 @@ def norm_backward(block: Block, x, w, rstd, grad_u, grad_add=None, grad_x=None, 
     ws, ws_bytes = None, 0
     if gw is not None:
         ws, ws_bytes, workspace = _workspace(workspace, "workspace", block_workspace_size(block, n), x, dev)
-    _check(lib().cgtp_norm_backward(block.handle, n, xp, x_ld, _addr_or_null(w, "w", rt, cs, dev),
-                                    _addr(rstd, "rstd", rt, (n,), dev), _addr(grad_u, "grad_u", dt, rows, dev),
-                                    _addr_or_null(grad_add, "grad_add", dt, rows, dev), gxp, gwp, ws, ws_bytes,
-                                    _raw_stream(dev)))
+    with _current(dev):
+        _check(lib().cgtp_norm_backward(block.handle, n, xp, x_ld, _addr_or_null(w, "w", rt, cs, dev),
+                                        _addr(rstd, "rstd", rt, (n,), dev), _addr(grad_u, "grad_u", dt, rows, dev),
+                                        _addr_or_null(grad_add, "grad_add", dt, rows, dev), gxp, gwp, ws, ws_bytes,
+                                        _raw_stream(dev)))
     return gx, gw
 
 
@@ -899,10 +907,11 @@ def join_forward(block: Block, res, f, gate, w_post, scale, w_next, h=None, u=No
     u, up = _output(u, block.next_norm, "u", dt, rows, f, dev)
     rstd_f, rfp = _output(rstd_f, need_rstd and block.post_norm, "rstd_f", rt, stat, f, dev)
     rstd_h, rhp = _output(rstd_h, need_rstd and block.next_norm, "rstd_h", rt, stat, f, dev)
-    _check(lib().cgtp_join_forward(
-        block.handle, n, _addr(res, "res", dt, rows, dev), fp, f_ld, gp, g_ld,
-        _addr_or_null(w_post, "w_post", rt, cs, dev), _addr_or_null(scale, "scale", rt, cs, dev),
-        _addr_or_null(w_next, "w_next", rt, cs, dev), hp, up, rfp, rhp, _raw_stream(dev)))
+    with _current(dev):
+        _check(lib().cgtp_join_forward(
+            block.handle, n, _addr(res, "res", dt, rows, dev), fp, f_ld, gp, g_ld,
+            _addr_or_null(w_post, "w_post", rt, cs, dev), _addr_or_null(scale, "scale", rt, cs, dev),
+            _addr_or_null(w_next, "w_next", rt, cs, dev), hp, up, rfp, rhp, _raw_stream(dev)))
     return h, u, rstd_f, rstd_h
 
 
@@ -939,12 +948,13 @@ def join_backward(block: Block, grad_h, grad_u, h, f, gate, w_post, scale, w_nex
     ws, ws_bytes = None, 0
     if g3 is not None or g4 is not None or g5 is not None:
         ws, ws_bytes, workspace = _workspace(workspace, "workspace", block_workspace_size(block, n), f, dev)
-    _check(lib().cgtp_join_backward(
-        block.handle, n, _addr_or_null(grad_h, "grad_h", dt, rows, dev), _addr_or_null(grad_u, "grad_u", dt, rows, dev),
-        _addr_or_null(h, "h", dt, rows, dev), fp, f_ld, gp, g_ld, _addr_or_null(w_post, "w_post", rt, cs, dev),
-        _addr_or_null(scale, "scale", rt, cs, dev), _addr_or_null(w_next, "w_next", rt, cs, dev),
-        _addr_or_null(rstd_f, "rstd_f", rt, stat, dev), _addr_or_null(rstd_h, "rstd_h", rt, stat, dev),
-        grp, gfp, gf_ld, ggp, gg_ld, g3, g4, g5, ws, ws_bytes, _raw_stream(dev)))
+    with _current(dev):
+        _check(lib().cgtp_join_backward(
+            block.handle, n, _addr_or_null(grad_h, "grad_h", dt, rows, dev),
+            _addr_or_null(grad_u, "grad_u", dt, rows, dev), _addr_or_null(h, "h", dt, rows, dev), fp, f_ld, gp, g_ld, _addr_or_null(w_post, "w_post", rt, cs, dev),
+            _addr_or_null(scale, "scale", rt, cs, dev), _addr_or_null(w_next, "w_next", rt, cs, dev),
+            _addr_or_null(rstd_f, "rstd_f", rt, stat, dev), _addr_or_null(rstd_h, "rstd_h", rt, stat, dev),
+            grp, gfp, gf_ld, ggp, gg_ld, g3, g4, g5, ws, ws_bytes, _raw_stream(dev)))
     return gr, gf, gg, gp3, gp4, gp5
 
 
@@ -1079,8 +1089,9 @@ def grad_norm(opt: AdamW, grads, norm=None, workspace=None, stream=None):
     like = grads._given[0]
     norm = like.new_empty(1, dtype=torch.float64) if norm is None else norm
     ws, ws_bytes, workspace = _workspace(workspace, "workspace", opt.norm_workspace, like, dev)
-    _check(lib().cgtp_grad_norm(opt.handle, grads.pointers(), _addr(norm, "norm", torch.float64, (1,), dev), ws,
-                                ws_bytes, _raw_stream(dev)))
+    with _current(dev):
+        _check(lib().cgtp_grad_norm(opt.handle, grads.pointers(), _addr(norm, "norm", torch.float64, (1,), dev), ws,
+                                    ws_bytes, _raw_stream(dev)))
     return norm
 
 
@@ -1108,12 +1119,13 @@ def adamw_step(opt: AdamW, params, grads, m, v, scales=None, master=None, *, lr=
     if dev is None or grads.device_index not in (None, dev):
         raise ValueError("parameters and gradients are not on one device" if params._given else "there is no parameter")
     hyper = AdamWHyper(lr, beta1, beta2, eps, weight_decay, max_norm, grad_scale, step)
-    _check(lib().cgtp_adamw_step(
-        opt.handle, params.pointers(), grads.pointers(), _addr(m, "m", mt, el, dev), _addr(v, "v", vt, el, dev),
-        _addr_or_null(scales, "scales", torch.float32, (2, opt.blocks), dev),
-        _addr_or_null(master, "master", torch.float32, el, dev), ctypes.byref(hyper),
-        _addr_or_null(norm, "norm", torch.float64, (1,), dev),
-        _addr_or_null(schedule, "schedule", torch.float64, (4,), dev), _raw_stream(dev)))
+    with _current(dev):
+        _check(lib().cgtp_adamw_step(
+            opt.handle, params.pointers(), grads.pointers(), _addr(m, "m", mt, el, dev), _addr(v, "v", vt, el, dev),
+            _addr_or_null(scales, "scales", torch.float32, (2, opt.blocks), dev),
+            _addr_or_null(master, "master", torch.float32, el, dev), ctypes.byref(hyper),
+            _addr_or_null(norm, "norm", torch.float64, (1,), dev),
+            _addr_or_null(schedule, "schedule", torch.float64, (4,), dev), _raw_stream(dev)))
 
 
 def adamw_schedule(schedule, beta1=0.9, beta2=0.999, stream=None, norm=None, grad_scale=1.0):
@@ -1123,9 +1135,10 @@ def adamw_schedule(schedule, beta1=0.9, beta2=0.999, stream=None, norm=None, gra
         return _in_stream(stream, adamw_schedule, schedule, beta1, beta2, norm=norm, grad_scale=grad_scale)
     import torch
     dev = _device_index(schedule, "schedule")
-    _check(lib().cgtp_adamw_schedule_norm(_addr(schedule, "schedule", torch.float64, (4,), dev), beta1, beta2,
-                                          _addr_or_null(norm, "norm", torch.float64, (1,), dev), grad_scale,
-                                          _raw_stream(dev)))
+    with _current(dev):
+        _check(lib().cgtp_adamw_schedule_norm(_addr(schedule, "schedule", torch.float64, (4,), dev), beta1, beta2,
+                                              _addr_or_null(norm, "norm", torch.float64, (1,), dev), grad_scale,
+                                              _raw_stream(dev)))
     return schedule
 
 
@@ -1141,10 +1154,11 @@ def adamw_state_read(opt: AdamW, m, v, scales, m_out=None, v_out=None, stream=No
     dev, el, (mt, vt), f32 = _device_index(m, "m"), (opt.elements,), opt.moment_dtypes, torch.float32
     m_out = m.new_empty(el, dtype=f32) if m_out is None else m_out
     v_out = m.new_empty(el, dtype=f32) if v_out is None else v_out
-    _check(lib().cgtp_adamw_state_read(opt.handle, _addr(m, "m", mt, el, dev), _addr(v, "v", vt, el, dev),
-                                       _addr_or_null(scales, "scales", f32, (2, opt.blocks), dev),
-                                       _addr(m_out, "m_out", f32, el, dev), _addr(v_out, "v_out", f32, el, dev),
-                                       _raw_stream(dev)))
+    with _current(dev):
+        _check(lib().cgtp_adamw_state_read(opt.handle, _addr(m, "m", mt, el, dev), _addr(v, "v", vt, el, dev),
+                                           _addr_or_null(scales, "scales", f32, (2, opt.blocks), dev),
+                                           _addr(m_out, "m_out", f32, el, dev), _addr(v_out, "v_out", f32, el, dev),
+                                           _raw_stream(dev)))
     return m_out, v_out
 
 
@@ -1154,8 +1168,10 @@ def adamw_state_write(opt: AdamW, m_in, v_in, m, v, scales, stream=None):
         return _in_stream(stream, adamw_state_write, opt, m_in, v_in, m, v, scales)
     import torch
     dev, el, (mt, vt), f32 = _device_index(m, "m"), (opt.elements,), opt.moment_dtypes, torch.float32
-    _check(lib().cgtp_adamw_state_write(opt.handle, _addr(m_in, "m_in", f32, el, dev),
-                                        _addr(v_in, "v_in", f32, el, dev), _addr(m, "m", mt, el, dev),
-                                        _addr(v, "v", vt, el, dev),
-                                        _addr_or_null(scales, "scales", f32, (2, opt.blocks), dev), _raw_stream(dev)))
+    with _current(dev):
+        _check(lib().cgtp_adamw_state_write(opt.handle, _addr(m_in, "m_in", f32, el, dev),
+                                            _addr(v_in, "v_in", f32, el, dev), _addr(m, "m", mt, el, dev),
+                                            _addr(v, "v", vt, el, dev),
+                                            _addr_or_null(scales, "scales", f32, (2, opt.blocks), dev),
+                                            _raw_stream(dev)))
     return m, v, scales

@@ -6,6 +6,7 @@
 #include <Python.h>
 
 #include <ATen/ATen.h>
+#include <c10/hip/HIPFunctions.h>
 #include <c10/hip/HIPStream.h>
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -40,14 +41,15 @@ at::ScalarType elem_type(long dtype)
 
 const at::Tensor *tensor(PyObject *o) { return THPVariable_Check(o) ? &THPVariable_Unpack(o) : nullptr; }
 
-// Addresses of a call's tensors; `fine` while every one is as it has to be.
+// Addresses of a call's tensors; `fine` while every one is as it has to be, on the device that is the
+// current one, where launches go (binding.py makes another device the current one).
 struct Args {
     int64_t device;
     bool fine = true;
 
     explicit Args(const at::Tensor *first) : device(first && first->is_cuda() ? first->get_device() : -1)
     {
-        fine = device >= 0;
+        fine = device >= 0 && device == c10::hip::current_device();
     }
 
     bool here(const at::Tensor *x, at::ScalarType t) const
