@@ -1064,6 +1064,11 @@ def _list(opt, tensors):
     return tensors
 
 
+def _held(tensors):
+    """A TensorList, or the tensors of any iterable, which may be read once only."""
+    return tensors if isinstance(tensors, TensorList) else tuple(tensors)
+
+
 def _tuple(opt, tensors):
     if not isinstance(tensors, TensorList):
         return tuple(tensors)
@@ -1077,6 +1082,7 @@ def grad_norm(opt: AdamW, grads, norm=None, workspace=None, stream=None):
     float64 tensor of one element."""
     if stream is not None:
         return _in_stream(stream, grad_norm, opt, grads, norm, workspace)
+    grads = _held(grads)
     if norm is None and workspace is None:
         got = opt._calls.grad_norm(opt._meta, _tuple(opt, grads))
         if got is not None:
@@ -1106,8 +1112,9 @@ def adamw_step(opt: AdamW, params, grads, m, v, scales=None, master=None, *, lr=
         return _in_stream(stream, adamw_step, opt, params, grads, m, v, scales, master, lr=lr, beta1=beta1, beta2=beta2,
                           eps=eps, weight_decay=weight_decay, step=step, max_norm=max_norm, grad_scale=grad_scale,
                           norm=norm, schedule=schedule)
-    got = opt._calls.adamw_step(opt._meta, _tuple(opt, params), _tuple(opt, grads), m, v, scales, master, norm, schedule,
-                                step, lr, beta1, beta2, eps, weight_decay, max_norm, grad_scale)
+    params, grads = _held(params), _held(grads)
+    got = opt._calls.adamw_step(opt._meta, _tuple(opt, params), _tuple(opt, grads), m, v, scales, master, norm,
+                                schedule, step, lr, beta1, beta2, eps, weight_decay, max_norm, grad_scale)
     if got is not None:
         _answer(got)
         return

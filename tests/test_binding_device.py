@@ -95,3 +95,13 @@ def test_every_call_runs_on_the_device_of_its_tensors(launches):
         "cgtp_norm_forward", "cgtp_norm_backward", "cgtp_join_forward", "cgtp_join_backward", "cgtp_grad_norm",
         "cgtp_adamw_schedule_norm", "cgtp_adamw_step", "cgtp_adamw_state_read", "cgtp_adamw_state_write"]
     assert all(device == 1 for _, device in launches.seen), launches.seen
+
+
+def test_tensors_may_come_from_a_generator(launches):
+    """What the compiled calls do not take is listed again."""
+    o, f32 = launches.opt, torch.float32
+    m, v = Fake((o.elements,), torch.int8), Fake((o.elements,), torch.uint8)
+    one = lambda: (Fake((n,), f32) for n in (4, 3))  # noqa: E731
+    cg.grad_norm(o, one())
+    cg.adamw_step(o, one(), one(), m, v, Fake((2, o.blocks), f32), step=1)
+    assert [name for name, _ in launches.seen] == ["cgtp_grad_norm", "cgtp_adamw_step"]
