@@ -327,26 +327,38 @@ DEV R gate_value(R g)
     return ACT == 1 ? s : g * s;
 }
 
-// act'(g) and act(g).  With e = exp(-|g|) and r = 1 / (1 + e) the sigmoid and its complement are r and e r,
-// the larger one for g >= 0: slopes of open gates are products of both, where 1 - s or 1 - tanh^2 would leave a
-// rounding of 1 (17% of the sigmoid's slope at 15, all of it at 17).  tanh itself, which small g needs exact, is a
-// function of its own: 8,192 scalar rows of 4,096 in fp32 with a tanh gate 212 us by 1 - tanh^2, 221 us; no other
-// act or type changed by 2%.
+// tanh(g) from e = exp(-2 |g|) and r = 1 / (1 + e); below 1/4, where 1 - e would cancel, its series to g^9 (what
+// follows is under 2^-26 of it there).  Doubles take the function itself.
+DEV float tanh_from(float g, float e, float r)
+{
+    const float t = (1.0f - e) * r, g2 = g * g;
+    const float small = g * (1.0f + g2 * (-1.0f / 3 + g2 * (2.0f / 15 + g2 * (-17.0f / 315 + g2 * (62.0f / 2835)))));
+    return g2 < 0.0625f ? small : g < 0 ? -t : t;
+}
+DEV double tanh_from(double g, double, double) { return tanh(g); }
+
+// act'(g) and act(g).  The sigmoid and its complement are q = e / (1 + e) and 1 - q, e = exp(-|g|), and the slope
+// their product; with 1 - s from s it would carry a rounding of 1 (17% of it at 15, all of it at 17).  tanh's
+// slope is 4 e / (1 + e)^2 with e = exp(-2 |g|), not 1 - tanh^2.  SiLU's complement is a small term beside 1 there.
 DEV R gate_slope(R g, R &value)
 {
     if (ACT == 0) {
         value = g;
         return (R)1;
     }
-    const R a = g < 0 ? -g : g;
-    const R e = exp_of(ACT == 3 ? -2 * a : -a), r = inverse((R)1 + e), er = e * r;
     if (ACT == 3) {
-        value = tanh_of(g);
-        return 4 * (er * r);
+        const R e = exp_of(g < 0 ? 2 * g : -2 * g), r = inverse((R)1 + e);
+        value = tanh_from(g, e, r);
+        return 4 * (e * r * r);
     }
-    const R s = g < 0 ? er : r, rest = g < 0 ? r : er;
-    value = ACT == 1 ? s : g * s;
-    return ACT == 1 ? s * rest : s * ((R)1 + g * rest);
+    if (ACT == 1) {
+        const R e = exp_of(g < 0 ? g : -g), q = e * inverse((R)1 + e);
+        value = g < 0 ? q : (R)1 - q;
+        return q * ((R)1 - q);
+    }
+    const R s = inverse((R)1 + exp_of(-g));
+    value = g * s;
+    return s * ((R)1 + g * ((R)1 - s));
 }
 
 #define ROW_SETUP                                                       \
@@ -471,6 +483,13 @@ cgtp_join_fwd(const T *__restrict__ res, const T *__restrict__ f, long f_ld, con
     }
 }
 
+// Where 1,024 lanes share a row a lane has 128 registers, and the slope of such a gate is one more a channel to
+// hold: there the gate and f are loaded after the next norm's sum.  Wide rows, gate and f before the sum and after
+// it: 8,192 x 8,192 fp32 sigmoid 508, 479 us, tanh 521, 500; 4,096 x 8,192 fp64 sigmoid 1,146, 999, tanh 1,331, 1,144;
+// 4,096 x 16,384 fp32 1,032, 1,012 and 1,237, 1,049; bf16 sigmoid 705, 695.  (By 1 - s and 1 - tanh^2, which are wrong
+// for open gates: 496, 490, 921, 1,144, 945, 903, 572.)
+constexpr bool LATE = BLOCK == 1024 && NEXT && GATE == 2 && (ACT == 1 || ACT == 3);
+
 // With z = h rstd_h, q = w_next du:  e = dh + rstd_h (q - z mean(q z)) is the whole gradient of h,
 //   dr = alpha e,  t[c] = sum_m e y,  P[c] = sum_n act t,  dgate = act' scale w_post t,
 //   p = e b,  df = rstd_f (p - y mean(p y)) (p without the norm),  Q[c] = sum_n sum_m du z.
@@ -490,9 +509,9 @@ cgtp_join_bwd(const T *__restrict__ dh, const T *__restrict__ du, const T *__res
     EACH_ROW(n, on)
     {
         R e[EPL], y[EPL], g[NC], t[NC], a = 1, slope = 0, dot = 0;
-        if (GATE == 2) load_channels(gate + n * gate_ld, lane, g);
+        if (GATE == 2 && !LATE) load_channels(gate + n * gate_ld, lane, g);
         if (GATE == 1) slope = gate_slope((R)gate[n * gate_ld], a);
-        load_cols(f + n * f_ld, lane, y);
+        if (!LATE) load_cols(f + n * f_ld, lane, y);
         if (dh) {
             load_cols(dh + n * D, lane, e);
         } else {
@@ -522,6 +541,10 @@ cgtp_join_bwd(const T *__restrict__ dh, const T *__restrict__ du, const T *__res
             R o[EPL];
             EACH_E(i) o[i] = alpha * e[i];
             store_cols(dres + n * D, lane, o);
+        }
+        if (LATE) {
+            load_channels(gate + n * gate_ld, lane, g);
+            load_cols(f + n * f_ld, lane, y);
         }
         const R rf = POST ? rstd_f[n] : (R)1;
         dot = 0;
