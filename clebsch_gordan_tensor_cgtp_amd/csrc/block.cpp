@@ -34,8 +34,11 @@ const char *type_name(int dtype)
 // Of every pair, the cost of a row in lane operations is taken: its lanes times a lane's elements,
 // which idle lanes and channels past an irrep's end raise, more where loads are narrow (below 16 bytes
 // in a flat layout, below 8 in runs of channels, which are neighbours in the same cache lines), where a
-// lane holds over 48 bytes (fewer waves fit a SIMD), and where waves must meet at barriers; the most
-// lanes of equal cost.  The weights are fitted to times of 14 shapes at 2 to 9 pairs each.  The
+// lane holds over 48 bytes of the row as it is stored (fewer waves fit a SIMD; 16-bit elements take twice
+// that in registers, which the rule does not count: a flat 16-bit row of 576 gets 24 elements a lane, and the
+// join's backward then 248 registers), and where waves must meet at barriers; the most
+// lanes of equal cost.  One rule serves all four passes; its weights are fitted to times of 14 shapes at 2 to 9
+// pairs each.  The
 // join's backward, fp32: 20,000 rows of 128x(0e,1o,2e,3o), 64 lanes of 32 elements 210 us, 128 of 16 201
 // us, 512 of 16, half idle, 216 us; 5,000 rows of 32x(0e,1o,2e), 32 lanes of 9 13.3 us, 16 of 18 15.9 us.
 // The norm: backward, 200,000 flat rows of 576 in fp32, 32 lanes of 20 elements 356 us, 64 of 12, a
@@ -193,9 +196,11 @@ void unload_block(Block &b)
     if (have_prev) (void)hipSetDevice(prev);
 }
 
-// At most two waves to each of the 1,024 SIMDs, which then take rows in turn: the weights are read and
+// At most 2,048 waves, two for each of the 1,024 SIMDs, which then take rows in turn: the weights are read and
 // the partial sums written once by each (the join's backward, 200,000 rows of 64x(0e,1o,2e) bf16: 345, 289,
 // 304, 313 us at 1, 2, 4, 8 waves to a SIMD; the norm's, 8,192 rows of 4,096 bf16: 54, 43, 45, 53 us).
+// A workgroup stays on one CU: where 1,024 lanes share a row these are 128 workgroups, on half of the 256 CUs
+// (8,192 rows of 8,192 fp32, the norm's backward 185 us, 4.3 TB/s, where 576 columns reach 5.5).
 int64_t block_groups(const Block &b, int64_t N, int waves_per_simd)
 {
     const int64_t need = (N + b.rows_per_group() - 1) / b.rows_per_group();
