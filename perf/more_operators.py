@@ -165,7 +165,7 @@ def prepare(case, seed):
         st["w"], st["b"] = 1 + 0.1 * normal(c), 0.1 * normal(c)
         if case["dir"] == "bwd":
             st["grad_y"] = normal(n, c).to(dt)
-            st["mean"], st["rstd"] = _stats(st)
+            st["mean"], st["rstd"] = (t.contiguous() for t in _stats(st))  # as the forward leaves them
         if own:
             from clebsch_gordan_tensor_cgtp_amd import binding as cg
             st["plan"] = cg.group_norm_for(c, case["groups"], case["dtype"], act=case["act"], eps=EPS)
