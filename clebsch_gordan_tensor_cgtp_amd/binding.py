@@ -13,6 +13,7 @@ at half the cost of a call.  What it does not take comes back here.
 import ctypes
 import os
 from functools import lru_cache
+from typing import NamedTuple
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libcgtp.so")
@@ -21,6 +22,7 @@ CGTP_UVU, CGTP_UVW = 0, 1
 CGTP_F32, CGTP_F64, CGTP_BF16, CGTP_F16 = 0, 1, 2, 3
 DTYPES = {"f32": CGTP_F32, "f64": CGTP_F64, "bf16": CGTP_BF16, "f16": CGTP_F16}
 GATES = {None: 0, "row": 1, "channel": 2}
+SCORES = {"softmax": 0, "sigmoid": 1}
 ACTS = {"identity": 0, "sigmoid": 1, "silu": 2, "tanh": 3}
 STATUS = {0: "CGTP_OK", 1: "CGTP_ERR_INVALID_ARG", 2: "CGTP_ERR_IRREPS", 3: "CGTP_ERR_UNSUPPORTED",
           4: "CGTP_ERR_COMPILE", 5: "CGTP_ERR_HIP", 6: "CGTP_ERR_INTERNAL"}
@@ -41,9 +43,16 @@ EXPORTS = ("cgtp_plan_create", "cgtp_plan_destroy", "cgtp_plan_info_get", "cgtp_
            "cgtp_block_workspace_size", "cgtp_norm_forward", "cgtp_norm_backward", "cgtp_join_forward",
            "cgtp_join_backward", "cgtp_adamw_create", "cgtp_adamw_destroy", "cgtp_adamw_info_get", "cgtp_adamw_offset",
            "cgtp_grad_norm", "cgtp_adamw_step", "cgtp_adamw_schedule", "cgtp_adamw_schedule_norm",
-           "cgtp_adamw_state_read", "cgtp_adamw_state_write")
+           "cgtp_adamw_state_read", "cgtp_adamw_state_write",
+           "cgtp_group_norm_create", "cgtp_group_norm_destroy", "cgtp_group_norm_source",
+           "cgtp_group_norm_workspace_size", "cgtp_group_norm_forward", "cgtp_group_norm_backward",
+           "cgtp_router_create", "cgtp_router_destroy", "cgtp_router_source", "cgtp_route_forward",
+           "cgtp_route_backward", "cgtp_route_order_workspace_size", "cgtp_route_order",
+           "cgtp_linear_create", "cgtp_linear_destroy", "cgtp_linear_info_get", "cgtp_linear_source",
+           "cgtp_linear_forward", "cgtp_linear_workspace_size", "cgtp_linear_backward")
 _STRING_RESULTS = ("cgtp_last_error", "cgtp_plan_source", "cgtp_plan_radial_source", "cgtp_plan_uvw_backward_source",
-                   "cgtp_plan_conv_uvw_backward_source", "cgtp_block_source")
+                   "cgtp_plan_conv_uvw_backward_source", "cgtp_block_source", "cgtp_group_norm_source",
+                   "cgtp_router_source", "cgtp_linear_source")
 
 
 class CgtpError(RuntimeError):
@@ -85,6 +94,23 @@ class AdamWInfo(ctypes.Structure):
 class AdamWHyper(ctypes.Structure):
     _fields_ = [(n, ctypes.c_double) for n in ("lr", "beta1", "beta2", "eps", "weight_decay", "max_norm",
                                                "grad_scale")] + [("step", ctypes.c_int64)]
+
+
+class GroupNormConfig(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("dtype", "channels", "groups", "act")] + [("eps", ctypes.c_double)]
+
+
+class RouterConfig(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("dtype", "score", "experts", "top_k", "groups", "top_groups",
+                                              "renormalise")] + [("scale", ctypes.c_double)]
+
+
+class LinearConfig(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("dtype", "experts", "top_k")]
+
+
+class LinearInfo(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("d_in", "d_out", "num_paths", "dtype")] + [("weight_numel", ctypes.c_int64)]
 
 
 _lib = None
@@ -159,6 +185,26 @@ def lib():
         L.cgtp_adamw_schedule_norm.argtypes = [vp, dbl, dbl, vp, dbl, vp]
         L.cgtp_adamw_state_read.argtypes = [vp] * 7
         L.cgtp_adamw_state_write.argtypes = [vp] * 7
+        for name in ("cgtp_group_norm", "cgtp_router", "cgtp_linear"):
+            getattr(L, name + "_source").restype = ctypes.c_char_p
+            getattr(L, name + "_source").argtypes = [vp]
+            getattr(L, name + "_destroy").argtypes = [vp]
+        L.cgtp_group_norm_create.argtypes = [ctypes.POINTER(GroupNormConfig), ctypes.POINTER(vp)]
+        L.cgtp_group_norm_workspace_size.argtypes = [vp, i64, i64, i32, szp]
+        L.cgtp_group_norm_forward.argtypes = [vp, i64, i64, vp, vp, i64, vp, vp, vp, i64, i32, vp, vp, vp, sz, vp]
+        L.cgtp_group_norm_backward.argtypes = [vp, i64, i64, vp, vp, i64] + [vp] * 5 + [i64, vp, i64, i32] + \
+            [vp] * 3 + [sz, vp]
+        L.cgtp_router_create.argtypes = [ctypes.POINTER(RouterConfig), ctypes.POINTER(vp)]
+        L.cgtp_route_forward.argtypes = [vp, i64, vp, i64] + [vp] * 4
+        L.cgtp_route_backward.argtypes = [vp, i64, vp, i64] + [vp] * 4
+        L.cgtp_route_order_workspace_size.argtypes = [vp, i64, szp]
+        L.cgtp_route_order.argtypes = [vp, i64] + [vp] * 5 + [sz, vp]
+        L.cgtp_linear_create.argtypes = [ctypes.c_char_p, ctypes.c_char_p, ctypes.POINTER(LinearConfig),
+                                         ctypes.POINTER(vp)]
+        L.cgtp_linear_info_get.argtypes = [vp, ctypes.POINTER(LinearInfo)]
+        L.cgtp_linear_forward.argtypes = [vp, i64, vp, i64, vp, vp, vp, vp, vp, i64, vp]
+        L.cgtp_linear_workspace_size.argtypes = [vp, i64, szp]
+        L.cgtp_linear_backward.argtypes = [vp, i64, vp, i64] + [vp] * 6 + [vp, i64, vp, i64] + [vp] * 3 + [sz, vp]
         for name in EXPORTS:
             if name not in _STRING_RESULTS:
                 getattr(L, name).restype = ctypes.c_int
@@ -956,6 +1002,296 @@ def join_backward(block: Block, grad_h, grad_u, h, f, gate, w_post, scale, w_nex
             _addr_or_null(rstd_f, "rstd_f", rt, stat, dev), _addr_or_null(rstd_h, "rstd_h", rt, stat, dev),
             grp, gfp, gf_ld, ggp, gg_ld, g3, g4, g5, ws, ws_bytes, _raw_stream(dev)))
     return gr, gf, gg, gp3, gp4, gp5
+
+
+# ------------------------------------------------------------------------------------ graphs of a batch
+
+class _Compiled:
+    """A handle of kernels that are compiled for a configuration when it is created.  Like a Plan, it is
+    closed (or dropped) only after the kernels launched with it have finished."""
+
+    _name = None
+
+    def _create(self, *args):
+        self._h = None
+        h = ctypes.c_void_p()
+        _check(getattr(lib(), self._name + "_create")(*args, ctypes.byref(h)))
+        self._h = h
+        self.torch_dtype = _torch_dtype(self.dtype)                              # of rows
+        self.real_dtype = _torch_dtype("f64" if self.dtype == "f64" else "f32")  # of statistics and weights
+
+    @property
+    def handle(self):
+        return self._h
+
+    @property
+    def source(self) -> str:
+        return getattr(lib(), self._name + "_source")(self._h).decode()
+
+    def close(self):
+        if self._h is not None and _lib is not None:
+            getattr(lib(), self._name + "_destroy")(self._h)
+        self._h = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+class GroupNorm(_Compiled):
+    """Group norm with an activation over the graphs of a batch, channels last."""
+
+    _name = "cgtp_group_norm"
+
+    def __init__(self, channels, groups, dtype="f32", act="identity", eps=1e-6):
+        self.channels, self.groups, self.dtype, self.act, self.eps = int(channels), int(groups), dtype, act, float(eps)
+        self._create(ctypes.byref(GroupNormConfig(DTYPES[dtype], self.channels, self.groups, ACTS[act], self.eps)))
+
+
+@lru_cache(maxsize=None)
+def group_norm_for(channels, groups, dtype="f32", act="identity", eps=1e-6) -> GroupNorm:
+    """The group norm of a configuration (cached per process)."""
+    return GroupNorm(channels, groups, dtype, act, eps)
+
+
+def group_norm_workspace_size(norm: GroupNorm, n: int, graphs: int, backward: bool = False) -> int:
+    v = ctypes.c_size_t()
+    _check(lib().cgtp_group_norm_workspace_size(norm.handle, n, graphs, int(backward), ctypes.byref(v)))
+    return v.value
+
+
+def _graphs(ptr, index):
+    """(graphs, address) of the graphs' row pointers."""
+    import torch
+    if len(ptr.shape) != 1 or ptr.shape[0] < 1:
+        raise ValueError(f"ptr has shape {tuple(ptr.shape)}, expected (graphs + 1,)")
+    return ptr.shape[0] - 1, _addr(ptr, "ptr", torch.int32, ptr.shape, index)
+
+
+def group_norm_forward(norm: GroupNorm, x, ptr, w, bias, y=None, mean=None, rstd=None, need_stats=True, workspace=None,
+                       stream=None):
+    """(y, mean, rstd): y = act((x - mean) * rstd * w + bias), mean and rstd [graphs][groups] over the rows
+    ptr[b]..ptr[b+1] of a graph and the channels of a group.  x and y may have a row pitch; w and bias
+    None stand for ones and zeros.  Rows of no graph are left as they were in a given y, and zeros in a new one."""
+    if stream is not None:
+        return _in_stream(stream, group_norm_forward, norm, x, ptr, w, bias, y, mean, rstd, need_stats, workspace)
+    dev = _device_index(x, "x")
+    n, dt, rt, c = x.shape[0], norm.torch_dtype, norm.real_dtype, norm.channels
+    s, pp = _graphs(ptr, dev)
+    xp, x_ld = _rows(x, "x", dt, (n, c), dev)
+    fill = y is None
+    y, yp, y_ld = _row_output(y, True, "y", dt, (n, c), x, dev)
+    need_stats = need_stats or mean is not None or rstd is not None
+    mean, mp = _output(mean, need_stats, "mean", rt, (s, norm.groups), x, dev)
+    rstd, rp = _output(rstd, need_stats, "rstd", rt, (s, norm.groups), x, dev)
+    ws, ws_bytes, workspace = _workspace(workspace, "workspace", group_norm_workspace_size(norm, n, s), x, dev)
+    with _current(dev):
+        _check(lib().cgtp_group_norm_forward(norm.handle, n, s, pp, xp, x_ld, _addr_or_null(w, "w", rt, (c,), dev),
+                                             _addr_or_null(bias, "bias", rt, (c,), dev), yp, y_ld, fill, mp, rp, ws,
+                                             ws_bytes, _raw_stream(dev)))
+    return y, mean, rstd
+
+
+def group_norm_backward(norm: GroupNorm, x, ptr, w, bias, mean, rstd, grad_y, grad_x=None, grad_w=None, grad_bias=None,
+                        need=(True,) * 3, workspace=None, stream=None):
+    """(grad_x, grad_w, grad_bias) from the forward's mean and rstd; entries not in ``need`` are None and not
+    computed.  x, grad_y and grad_x may have a row pitch.  Rows of no graph are left as they were in a given
+    grad_x, and zeros in a new one."""
+    if stream is not None:
+        return _in_stream(stream, group_norm_backward, norm, x, ptr, w, bias, mean, rstd, grad_y, grad_x, grad_w,
+                          grad_bias, need, workspace)
+    dev = _device_index(x, "x")
+    n, dt, rt, c = x.shape[0], norm.torch_dtype, norm.real_dtype, norm.channels
+    s, pp = _graphs(ptr, dev)
+    xp, x_ld = _rows(x, "x", dt, (n, c), dev)
+    dyp, dy_ld = _rows(grad_y, "grad_y", dt, (n, c), dev)
+    fill = grad_x is None
+    gx, gxp, gx_ld = _row_output(grad_x if need[0] else None, need[0], "grad_x", dt, (n, c), x, dev)
+    gw, gwp = _output(grad_w if need[1] else None, need[1], "grad_w", rt, (c,), x, dev)
+    gb, gbp = _output(grad_bias if need[2] else None, need[2], "grad_bias", rt, (c,), x, dev)
+    ws, ws_bytes, workspace = _workspace(workspace, "workspace", group_norm_workspace_size(norm, n, s, True), x, dev)
+    stat = (s, norm.groups)
+    with _current(dev):
+        _check(lib().cgtp_group_norm_backward(
+            norm.handle, n, s, pp, xp, x_ld, _addr_or_null(w, "w", rt, (c,), dev),
+            _addr_or_null(bias, "bias", rt, (c,), dev), _addr(mean, "mean", rt, stat, dev),
+            _addr(rstd, "rstd", rt, stat, dev), dyp, dy_ld, gxp, gx_ld, fill, gwp, gbp, ws, ws_bytes, _raw_stream(dev)))
+    return gx, gw, gb
+
+
+# ------------------------------------------------------------------------------------ experts
+
+class Router(_Compiled):
+    """The choice of top_k of E experts for each row, from softmax or sigmoid scores."""
+
+    _name = "cgtp_router"
+
+    def __init__(self, experts, top_k, dtype="f32", score="softmax", groups=1, top_groups=1, renormalise=True, scale=1.0):
+        self.experts, self.top_k, self.dtype, self.score = int(experts), int(top_k), dtype, score
+        self.groups, self.top_groups = int(groups), int(top_groups)
+        self.renormalise, self.scale = bool(renormalise), float(scale)
+        self._create(ctypes.byref(RouterConfig(DTYPES[dtype], SCORES[score], self.experts, self.top_k, self.groups,
+                                               self.top_groups, int(self.renormalise), self.scale)))
+
+
+@lru_cache(maxsize=None)
+def router_for(experts, top_k, dtype="f32", score="softmax", groups=1, top_groups=1, renormalise=True,
+               scale=1.0) -> Router:
+    """The router of a configuration (cached per process)."""
+    return Router(experts, top_k, dtype, score, groups, top_groups, renormalise, scale)
+
+
+class RouteOrder(NamedTuple):
+    """Rows by the pair of their lowest experts, slots (row * top_k + choice) by expert, and each expert's
+    first place among the slots: int32 tensors."""
+    rows: object
+    slots: object
+    offsets: object
+
+
+def route_forward(router: Router, logits, bias=None, experts=None, weights=None, stream=None):
+    """(experts, weights), both [N][top_k]: the chosen experts (int32, -1 where too few are not masked) and their
+    weights.  ``bias`` takes part in the choice alone.  logits may have a row pitch."""
+    if stream is not None:
+        return _in_stream(stream, route_forward, router, logits, bias, experts, weights)
+    import torch
+    dev = _device_index(logits, "logits")
+    n, e, k, rt = logits.shape[0], router.experts, router.top_k, router.real_dtype
+    lp, ld = _rows(logits, "logits", router.torch_dtype, (n, e), dev)
+    experts, ep = _output(experts, True, "experts", torch.int32, (n, k), logits, dev)
+    weights, wp = _output(weights, True, "weights", rt, (n, k), logits, dev)
+    with _current(dev):
+        _check(lib().cgtp_route_forward(router.handle, n, lp, ld, _addr_or_null(bias, "bias", rt, (e,), dev), ep, wp,
+                                        _raw_stream(dev)))
+    return experts, weights
+
+
+def route_backward(router: Router, logits, experts, grad_weights, grad_logits=None, stream=None):
+    """grad_logits [N][E] from the gradient of the weights, the choice held fixed."""
+    if stream is not None:
+        return _in_stream(stream, route_backward, router, logits, experts, grad_weights, grad_logits)
+    import torch
+    dev = _device_index(logits, "logits")
+    n, e, k, dt = logits.shape[0], router.experts, router.top_k, router.torch_dtype
+    lp, ld = _rows(logits, "logits", dt, (n, e), dev)
+    grad_logits, gp = _output(grad_logits, True, "grad_logits", dt, (n, e), logits, dev)
+    with _current(dev):
+        _check(lib().cgtp_route_backward(router.handle, n, lp, ld, _addr(experts, "experts", torch.int32, (n, k), dev),
+                                         _addr(grad_weights, "grad_weights", router.real_dtype, (n, k), dev), gp,
+                                         _raw_stream(dev)))
+    return grad_logits
+
+
+def route_order_workspace_size(router: Router, n: int) -> int:
+    v = ctypes.c_size_t()
+    _check(lib().cgtp_route_order_workspace_size(router.handle, n, ctypes.byref(v)))
+    return v.value
+
+
+def route_order(router: Router, experts, outs=(None, None, None), workspace=None, stream=None) -> RouteOrder:
+    """The lists that the experts' products go by (rows, slots, offsets), from experts [N][top_k]."""
+    if stream is not None:
+        return _in_stream(stream, route_order, router, experts, outs, workspace)
+    import torch
+    dev = _device_index(experts, "experts")
+    n, k, i32 = experts.shape[0], router.top_k, torch.int32
+    ep = _addr(experts, "experts", i32, (n, k), dev)
+    rows, rp = _output(outs[0], True, "rows", i32, (n,), experts, dev)
+    slots, sp = _output(outs[1], True, "slots", i32, (n * k,), experts, dev)
+    offsets, op = _output(outs[2], True, "offsets", i32, (router.experts + 1,), experts, dev)
+    ws, ws_bytes, workspace = _workspace(workspace, "workspace", route_order_workspace_size(router, n), experts, dev)
+    with _current(dev):
+        _check(lib().cgtp_route_order(router.handle, n, ep, rp, sp, op, ws, ws_bytes, _raw_stream(dev)))
+    return RouteOrder(rows, slots, offsets)
+
+
+class Linear(_Compiled):
+    """Products of irreps rows with the experts' matrices, one for each pair of equal irreps; without a choice
+    (top_k 0) the plain linear layer.  Weights are [experts][weight_numel]."""
+
+    _name = "cgtp_linear"
+
+    def __init__(self, in_irreps, out_irreps, dtype="f32", experts=1, top_k=0):
+        self.in_irreps, self.out_irreps, self.dtype = in_irreps, out_irreps, dtype
+        self.experts, self.top_k = int(experts), int(top_k)
+        self._create(in_irreps.encode(), out_irreps.encode(),
+                     ctypes.byref(LinearConfig(DTYPES[dtype], self.experts, self.top_k)))
+        info = LinearInfo()
+        _check(lib().cgtp_linear_info_get(self._h, ctypes.byref(info)))
+        self.d_in, self.d_out, self.num_paths, self.weight_numel = info.d_in, info.d_out, info.num_paths, info.weight_numel
+
+
+@lru_cache(maxsize=None)
+def linear_for(in_irreps, out_irreps, dtype="f32", experts=1, top_k=0) -> Linear:
+    """The linear of a configuration (cached per process)."""
+    return Linear(in_irreps, out_irreps, dtype, experts, top_k)
+
+
+def linear_workspace_size(linear: Linear, n: int) -> int:
+    v = ctypes.c_size_t()
+    _check(lib().cgtp_linear_workspace_size(linear.handle, n, ctypes.byref(v)))
+    return v.value
+
+
+def _choice(linear, n, experts, weights, order, dev):
+    """Addresses of (experts, weights, rows, slots, offsets)."""
+    import torch
+    k = linear.top_k
+    if k == 0:
+        if experts is not None or weights is not None or order is not None:
+            raise ValueError("experts, weights or order given to a linear without a choice of experts")
+        return (None,) * 5
+    i32 = torch.int32
+    lists = (None,) * 3
+    if order is not None:
+        lists = (_addr_or_null(order[0], "rows", i32, (n,), dev), _addr_or_null(order[1], "slots", i32, (n * k,), dev),
+                 _addr_or_null(order[2], "offsets", i32, (linear.experts + 1,), dev))
+    return (_addr(experts, "experts", i32, (n, k), dev), _addr(weights, "weights", linear.real_dtype, (n, k), dev)) + lists
+
+
+def linear_forward(linear: Linear, x, w, experts=None, weights=None, order=None, out=None, stream=None):
+    """out[n] = sum_j weights[n][j] * W[experts[n][j]] x[n] (W x without a choice).  ``order`` is
+    route_order's for these experts; without it rows are taken as they lie.  x and out may have a row pitch."""
+    if stream is not None:
+        return _in_stream(stream, linear_forward, linear, x, w, experts, weights, order, out)
+    dev = _device_index(x, "x")
+    n, dt = x.shape[0], linear.torch_dtype
+    xp, x_ld = _rows(x, "x", dt, (n, linear.d_in), dev)
+    wp = _addr(w, "w", dt, (linear.experts, linear.weight_numel), dev)
+    ep, pp, rows, _, _ = _choice(linear, n, experts, weights, order, dev)
+    out, op, o_ld = _row_output(out, True, "out", dt, (n, linear.d_out), x, dev)
+    with _current(dev):
+        _check(lib().cgtp_linear_forward(linear.handle, n, xp, x_ld, wp, ep, pp, rows, op, o_ld, _raw_stream(dev)))
+    return out
+
+
+def linear_backward(linear: Linear, x, w, grad_out, experts=None, weights=None, order=None, outs=(None,) * 3,
+                    need=(True,) * 3, workspace=None, stream=None):
+    """(grad_x, grad_w, grad_weights); entries not in ``need`` (and grad_weights without a choice) are None
+    and not computed.  ``order`` as in linear_forward; grad_w needs it.  x, grad_out and grad_x may have a
+    row pitch."""
+    if stream is not None:
+        return _in_stream(stream, linear_backward, linear, x, w, grad_out, experts, weights, order, outs, need, workspace)
+    dev = _device_index(x, "x")
+    n, dt, k = x.shape[0], linear.torch_dtype, linear.top_k
+    xp, x_ld = _rows(x, "x", dt, (n, linear.d_in), dev)
+    gp, g_ld = _rows(grad_out, "grad_out", dt, (n, linear.d_out), dev)
+    ws_shape = (linear.experts, linear.weight_numel)
+    wp = _addr(w, "w", dt, ws_shape, dev)
+    ep, pp, rows, slots, offsets = _choice(linear, n, experts, weights, order, dev)
+    if need[1] and k and order is None:
+        raise ValueError("the gradient of the weights needs the order (route_order)")
+    gx, gxp, gx_ld = _row_output(outs[0] if need[0] else None, need[0], "grad_x", dt, (n, linear.d_in), x, dev)
+    gw, gwp = _output(outs[1] if need[1] else None, need[1], "grad_w", dt, ws_shape, x, dev)
+    third = need[2] and k > 0
+    gs, gsp = _output(outs[2] if third else None, third, "grad_weights", linear.real_dtype, (n, k), x, dev)
+    ws, ws_bytes, workspace = _workspace(workspace, "workspace", linear_workspace_size(linear, n), x, dev)
+    with _current(dev):
+        _check(lib().cgtp_linear_backward(linear.handle, n, xp, x_ld, wp, ep, pp, rows, slots, offsets, gp, g_ld, gxp,
+                                          gx_ld, gwp, gsp, ws, ws_bytes, _raw_stream(dev)))
+    return gx, gw, gs
 
 
 # ------------------------------------------------------------------------------------ optimizer

@@ -9,6 +9,9 @@
 
 #include "abi_util.h"
 #include "block_kernels.h"
+#include "config_module.h"
+#include "row_kernels.h"
+#include "rows.h"
 
 struct cgtp_block {
     cgtp::Block b;
@@ -19,16 +22,6 @@ namespace cgtp {
 namespace {
 
 constexpr int kLds = 160 * 1024;  // bytes of a workgroup
-
-const char *type_name(int dtype)
-{
-    switch (dtype) {
-    case CGTP_F64: return "double";
-    case CGTP_BF16: return "__bf16";
-    case CGTP_F16: return "_Float16";
-    default: return "float";
-    }
-}
 
 // The lanes' share of a row: G lanes, CV neighbouring channels (columns in a flat layout) to a slot.
 // Of every pair, the cost of a row in lane operations is taken: its lanes times a lane's elements,
@@ -164,7 +157,7 @@ void build_block(Block &b, const std::string &irreps)
     b.vec = 16 / b.elem;
     b.flat = b.d != b.c && b.cfg.gate != CGTP_GATE_CHANNEL;
     pick_lanes(b);
-    b.source = constants(b) + kBlockKernels;
+    b.source = constants(b) + kRowKernels + kBlockKernels;
     b.code = compile_source(b.source);
 }
 
@@ -221,58 +214,6 @@ int64_t forward_groups(const Block &b, int64_t N, int waves_per_simd)
 int norm_waves(const Block &b) { return b.lanes > 64 || b.elem == 2 ? 4 : 2; }
 
 namespace {
-
-// Rows of `width` elements every `ld` elements.
-struct Rows {
-    const void *p;
-    int64_t width, ld;
-    const char *name;
-};
-
-void check_rows(const Block &b, int64_t N, const Rows &r)
-{
-    require_ptr(r.p, r.name, b.elem);
-    require(r.ld >= r.width && r.ld < INT_MAX,
-            std::string(r.name) + ": row pitch " + std::to_string(r.ld) + " is below the row's " +
-                std::to_string(r.width) + " elements or above 2^31-1");
-    require(N <= ((int64_t)1 << 56) / (r.ld * b.elem), std::string(r.name) + ": more than 2^56 bytes");
-}
-
-// No row of one may overlap a row of the other: their ranges are apart, or both have the same
-// pitch and lie side by side inside it (a block's output and its gates in one buffer).
-void rows_apart(const Block &b, int64_t N, const Rows &x, const Rows &y)
-{
-    if (!x.p || !y.p || !N || !x.width || !y.width) return;
-    const int64_t es = b.elem;
-    const uint64_t a = reinterpret_cast<uintptr_t>(x.p), c = reinterpret_cast<uintptr_t>(y.p);
-    const uint64_t na = (uint64_t)((N - 1) * x.ld + x.width) * es, nc = (uint64_t)((N - 1) * y.ld + y.width) * es;
-    if (a + na <= c || c + nc <= a) return;
-    if (x.ld == y.ld) {
-        const int64_t pitch = x.ld * es;
-        int64_t m = (int64_t)(c - a) % pitch;
-        if (m < 0) m += pitch;
-        if (m >= x.width * es && m + y.width * es <= pitch) return;
-    }
-    throw Error(CGTP_ERR_INVALID_ARG, std::string(x.name) + " overlaps " + y.name);
-}
-
-void rows_apart(const Block &b, int64_t N, const Rows &x, const void *p, size_t bytes, const char *name)
-{
-    if (!x.p || !p || !N) return;
-    require_disjoint(x.p, (size_t)((N - 1) * x.ld + x.width) * b.elem, x.name, p, bytes, name);
-}
-
-void check_count(int64_t N)
-{
-    require(N >= 0 && N < INT_MAX, "N must be in [0, 2^31-1)");
-}
-
-void run(hipFunction_t f, int64_t groups, int threads, void **args, void *stream)
-{
-    check_hip(hipModuleLaunchKernel(f, (unsigned)groups, 1, 1, (unsigned)threads, 1, 1, 0,
-                                    static_cast<hipStream_t>(stream), args, nullptr),
-              "hipModuleLaunchKernel");
-}
 
 void reduce_partials(const Block &b, const Block::Fns &F, const void *part, int64_t parts, bool join, const void *w_post,
                      const void *scale, void *g_post, void *g_scale, void *g_next, void *stream)
@@ -369,15 +310,15 @@ cgtp_status cgtp_norm_forward(const cgtp_block *block, int64_t N, const void *x,
         check_count(N);
         if (N == 0) return;
         const Rows X{x, b.d, x_ld, "x"}, U{u, b.d, b.d, "u"};
-        check_rows(b, N, X);
-        check_rows(b, N, U);
+        check_rows(b.elem, N, X);
+        check_rows(b.elem, N, U);
         if (w) require_ptr(w, "w", b.real);
         if (rstd) require_ptr(rstd, "rstd", b.real);
         const size_t nw = (size_t)b.c * b.real, ns = (size_t)N * b.real;
-        rows_apart(b, N, U, X);
-        rows_apart(b, N, U, w, nw, "w");
-        rows_apart(b, N, U, rstd, ns, "rstd");
-        rows_apart(b, N, X, rstd, ns, "rstd");
+        rows_apart(b.elem, N, U, X);
+        rows_apart(b.elem, N, U, w, nw, "w");
+        rows_apart(b.elem, N, U, rstd, ns, "rstd");
+        rows_apart(b.elem, N, X, rstd, ns, "rstd");
         require_disjoint(rstd, rstd ? ns : 0, "rstd", w, w ? nw : 0, "w");
         const auto &F = block_for_current_device(b);
         long ld = (long)x_ld, rows = (long)N;
@@ -406,10 +347,10 @@ cgtp_status cgtp_norm_backward(const cgtp_block *block, int64_t N, const void *x
         }
         const Rows X{x, b.d, x_ld, "x"}, DU{grad_u, b.d, b.d, "grad_u"}, ADD{grad_add, b.d, b.d, "grad_add"},
             DX{grad_x, b.d, b.d, "grad_x"};
-        check_rows(b, N, X);
-        check_rows(b, N, DU);
-        if (grad_add) check_rows(b, N, ADD);
-        if (grad_x) check_rows(b, N, DX);
+        check_rows(b.elem, N, X);
+        check_rows(b.elem, N, DU);
+        if (grad_add) check_rows(b.elem, N, ADD);
+        if (grad_x) check_rows(b.elem, N, DX);
         if (w) require_ptr(w, "w", b.real);
         require_ptr(rstd, "rstd", b.real);
         size_t need = 0;
@@ -457,29 +398,29 @@ cgtp_status cgtp_join_forward(const cgtp_block *block, int64_t N, const void *re
         require(post || (!w_post && !rstd_f), "w_post or rstd_f given to a block without a post norm");
         const Rows RES{res, b.d, b.d, "res"}, F_{f, b.d, f_ld, "f"}, GT{gate, gw, gate_ld, "gate"}, H{h, b.d, b.d, "h"},
             U{u, b.d, b.d, "u"};
-        check_rows(b, N, RES);
-        check_rows(b, N, F_);
-        if (gw) check_rows(b, N, GT);
-        check_rows(b, N, H);
-        if (next) check_rows(b, N, U);
+        check_rows(b.elem, N, RES);
+        check_rows(b.elem, N, F_);
+        if (gw) check_rows(b.elem, N, GT);
+        check_rows(b.elem, N, H);
+        if (next) check_rows(b.elem, N, U);
         struct { const void *p; size_t n; const char *name; bool out; } reals[] = {
             {w_post, (size_t)b.c * b.real, "w_post", false}, {scale, (size_t)b.c * b.real, "scale", false},
             {w_next, (size_t)b.c * b.real, "w_next", false}, {rstd_f, (size_t)N * b.real, "rstd_f", true},
             {rstd_h, (size_t)N * b.real, "rstd_h", true}};
         for (auto &r : reals) {
             if (r.p) require_ptr(r.p, r.name, b.real);
-            rows_apart(b, N, H, r.p, r.n, r.name);
-            if (next) rows_apart(b, N, U, r.p, r.n, r.name);
+            rows_apart(b.elem, N, H, r.p, r.n, r.name);
+            if (next) rows_apart(b.elem, N, U, r.p, r.n, r.name);
             if (!r.out) continue;
-            for (const Rows *in : {&RES, &F_, &GT}) rows_apart(b, N, *in, r.p, r.n, r.name);
+            for (const Rows *in : {&RES, &F_, &GT}) rows_apart(b.elem, N, *in, r.p, r.n, r.name);
             for (auto &o : reals)
                 if (&o != &r) require_disjoint(r.p, r.p ? r.n : 0, r.name, o.p, o.p ? o.n : 0, o.name);
         }
         for (const Rows *in : {&RES, &F_, &GT}) {
-            rows_apart(b, N, H, *in);
-            if (next) rows_apart(b, N, U, *in);
+            rows_apart(b.elem, N, H, *in);
+            if (next) rows_apart(b.elem, N, U, *in);
         }
-        if (next) rows_apart(b, N, H, U);
+        if (next) rows_apart(b.elem, N, H, U);
         const auto &F = block_for_current_device(b);
         long fl = (long)f_ld, gl = (long)gate_ld, rows = (long)N;
         Real alpha(b, b.cfg.alpha), eps(b, b.cfg.eps);
@@ -527,17 +468,17 @@ cgtp_status cgtp_join_backward(const cgtp_block *block, int64_t N, const void *g
         const Rows DR{grad_res, b.d, b.d, "grad_res"}, DF{grad_f, b.d, grad_f_ld, "grad_f"},
             DG{grad_gate, gw, grad_gate_ld, "grad_gate"};
         require(grad_h || next, "grad_h is NULL");
-        if (grad_h) check_rows(b, N, DH);
+        if (grad_h) check_rows(b.elem, N, DH);
         if (next) {
-            check_rows(b, N, DU);
-            check_rows(b, N, H);
+            check_rows(b.elem, N, DU);
+            check_rows(b.elem, N, H);
             require_ptr(rstd_h, "rstd_h", b.real);
         }
-        check_rows(b, N, F_);
-        if (gw) check_rows(b, N, GT);
+        check_rows(b.elem, N, F_);
+        if (gw) check_rows(b.elem, N, GT);
         if (post) require_ptr(rstd_f, "rstd_f", b.real);
         for (const Rows *o : {&DR, &DF, &DG})
-            if (o->p) check_rows(b, N, *o);
+            if (o->p) check_rows(b.elem, N, *o);
         size_t need = 0;
         if (weights) {
             need = workspace_bytes_of(b, N);
@@ -552,13 +493,13 @@ cgtp_status cgtp_join_backward(const cgtp_block *block, int64_t N, const void *g
             {grad_scale, nw, "grad_scale", true}, {grad_w_next, nw, "grad_w_next", true},
             {weights ? workspace : nullptr, need, "workspace", true}};
         for (int i = 0; i < 3; ++i) {
-            for (const Rows *in : row_in) rows_apart(b, N, *row_out[i], *in);
-            for (int j = i + 1; j < 3; ++j) rows_apart(b, N, *row_out[i], *row_out[j]);
-            for (auto &r : reals) rows_apart(b, N, *row_out[i], r.p, r.n, r.name);
+            for (const Rows *in : row_in) rows_apart(b.elem, N, *row_out[i], *in);
+            for (int j = i + 1; j < 3; ++j) rows_apart(b.elem, N, *row_out[i], *row_out[j]);
+            for (auto &r : reals) rows_apart(b.elem, N, *row_out[i], r.p, r.n, r.name);
         }
         for (auto &r : reals) {
             if (!r.out || !r.p) continue;
-            for (const Rows *in : row_in) rows_apart(b, N, *in, r.p, r.n, r.name);
+            for (const Rows *in : row_in) rows_apart(b.elem, N, *in, r.p, r.n, r.name);
             for (auto &o : reals)
                 if (&o != &r) require_disjoint(r.p, r.n, r.name, o.p, o.p ? o.n : 0, o.name);
         }

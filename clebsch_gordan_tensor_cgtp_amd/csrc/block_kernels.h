@@ -1,6 +1,6 @@
 // HIP source of the block kernels: the norm at a block's entry and the join at its end (norm,
 // gate, residual sum and the next block's norm), forward and backward.  block.cpp puts a
-// plan's constants in front of this text and compiles it for gfx950.
+// plan's constants and the shared text (row_kernels.h) in front of this one and compiles it for gfx950.
 //
 // Constants of a plan:
 //   T, R         element type in memory; type of statistics, weights and sums (float, or double)
@@ -21,8 +21,6 @@
 namespace cgtp {
 
 static const char kBlockKernels[] = R"HIP(
-#define DEV static __device__ __forceinline__
-
 constexpr int NC = NSLOT * CV;
 constexpr int NW = G > 64 ? G / 64 : 1;            // waves that share a row
 constexpr int RPB = BLOCK / G;                     // rows of a workgroup at a time (1 when NW > 1)
@@ -37,41 +35,6 @@ constexpr int RPB = BLOCK / G;                     // rows of a workgroup at a t
 // per workgroup (norm, 20,000 rows of 128x(0e,1o,2e,3o) in fp64: 113 us, 136 us by channels).
 // Rows start at any element, so the vector types claim no more than the element's alignment.
 // Channels past an irrep's end read as 0 and are not written.
-
-template <int N, typename S> DEV void load_run(const S *p, R *x)
-{
-    if constexpr (N > 0) {
-        constexpr int W = 16 / sizeof(S);
-        constexpr int n = N >= W ? W : N >= 8 ? 8 : N >= 4 ? 4 : N >= 2 ? 2 : 1;
-        typedef S V __attribute__((ext_vector_type(n), aligned(sizeof(S))));
-        if constexpr (n == 1) {
-            x[0] = (R)p[0];
-        } else {
-            const V r = *reinterpret_cast<const V *>(p);
-#pragma unroll
-            for (int i = 0; i < n; ++i) x[i] = (R)r[i];
-        }
-        load_run<N - n>(p + n, x + n);
-    }
-}
-
-template <int N, typename S> DEV void store_run(S *p, const R *x)
-{
-    if constexpr (N > 0) {
-        constexpr int W = 16 / sizeof(S);
-        constexpr int n = N >= W ? W : N >= 8 ? 8 : N >= 4 ? 4 : N >= 2 ? 2 : 1;
-        typedef S V __attribute__((ext_vector_type(n), aligned(sizeof(S))));
-        if constexpr (n == 1) {
-            p[0] = (S)x[0];
-        } else {
-            V r;
-#pragma unroll
-            for (int i = 0; i < n; ++i) r[i] = (S)x[i];
-            *reinterpret_cast<V *>(p) = r;
-        }
-        store_run<N - n>(p + n, x + n);
-    }
-}
 
 // slot J of a row of K-component channels (columns), or of one value per channel (K = 1)
 template <int J, int K, typename S> DEV void load_slot(const S *irrep, int lane, R *x)
@@ -184,55 +147,6 @@ DEV void load_scale(const R *scale, const R *w_post, int lane, R (&x)[NC])
 }
 
 // ---------------------------------------------------------------- sums over a row
-// Exchanges of a butterfly: inside 16 lanes by DPP (quads, then mirrored halves and rows, whose
-// values are equal by then), across them by the permlane swaps.  Every lane ends with the same bits.
-// A swap's results are copied into plain variables first: bit-casting the elements of the builtin's
-// vector made the front end read element 0 for both.
-
-template <int CTRL> DEV float dpp(float v)
-{
-    return __builtin_bit_cast(float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, v), CTRL, 15, 15, false));
-}
-template <int CTRL> DEV double dpp(double v)
-{
-    const unsigned long long b = __builtin_bit_cast(unsigned long long, v);
-    const unsigned lo = __builtin_amdgcn_mov_dpp((int)b, CTRL, 15, 15, false);
-    const unsigned hi = __builtin_amdgcn_mov_dpp((int)(b >> 32), CTRL, 15, 15, false);
-    return __builtin_bit_cast(double, (unsigned long long)hi << 32 | lo);
-}
-DEV float swap16(float v)
-{
-    const unsigned a = __builtin_bit_cast(unsigned, v);
-    const auto r = __builtin_amdgcn_permlane16_swap(a, a, false, false);
-    const unsigned r0 = r[0], r1 = r[1];
-    return __builtin_bit_cast(float, r0) + __builtin_bit_cast(float, r1);
-}
-DEV float swap32(float v)
-{
-    const unsigned a = __builtin_bit_cast(unsigned, v);
-    const auto r = __builtin_amdgcn_permlane32_swap(a, a, false, false);
-    const unsigned r0 = r[0], r1 = r[1];
-    return __builtin_bit_cast(float, r0) + __builtin_bit_cast(float, r1);
-}
-DEV double join64(unsigned lo, unsigned hi)
-{
-    return __builtin_bit_cast(double, (unsigned long long)hi << 32 | lo);
-}
-DEV double swap16(double v)
-{
-    const unsigned long long b = __builtin_bit_cast(unsigned long long, v);
-    const auto lo = __builtin_amdgcn_permlane16_swap((unsigned)b, (unsigned)b, false, false);
-    const auto hi = __builtin_amdgcn_permlane16_swap((unsigned)(b >> 32), (unsigned)(b >> 32), false, false);
-    return join64(lo[0], hi[0]) + join64(lo[1], hi[1]);
-}
-DEV double swap32(double v)
-{
-    const unsigned long long b = __builtin_bit_cast(unsigned long long, v);
-    const auto lo = __builtin_amdgcn_permlane32_swap((unsigned)b, (unsigned)b, false, false);
-    const auto hi = __builtin_amdgcn_permlane32_swap((unsigned)(b >> 32), (unsigned)(b >> 32), false, false);
-    return join64(lo[0], hi[0]) + join64(lo[1], hi[1]);
-}
-
 DEV R lane_sum(R v)
 {
     if (G >= 2) v += dpp<0xB1>(v);    // quad_perm 1,0,3,2
@@ -308,62 +222,6 @@ DEV void write_partial(R (&acc)[NC], int lane, R *lds, R *out)
             for (int w = 0; w < SUMS; ++w) s += lds[w * WIDTH + col + m];
         out[c] = s;
     }
-}
-
-// ---------------------------------------------------------------- the gate
-// Rows of 16 bits take the hardware's exponential and reciprocal: their errors, |g| 2^-23 and 2^-23 of the
-// result, are far below a rounding to 16 bits; the weight gradients, which are float, have them in every row's
-// term, as large as a few of float's own roundings (the join's backward, 8,192 scalar rows
-// of 4,096 in bf16 with a SiLU gate: 131 us with expf and a division, 116 us).
-DEV float exp_of(float v) { return sizeof(T) == 2 ? __builtin_amdgcn_exp2f(v * 1.44269504f) : expf(v); }
-DEV float inverse(float v) { return sizeof(T) == 2 ? __builtin_amdgcn_rcpf(v) : 1.0f / v; }
-DEV double inverse(double v) { return 1.0 / v; }
-DEV double exp_of(double v) { return exp(v); }
-DEV float tanh_of(float v) { return tanhf(v); }
-DEV double tanh_of(double v) { return tanh(v); }
-DEV float root_inverse(float v) { return 1.0f / __builtin_sqrtf(v); }
-DEV double root_inverse(double v) { return 1.0 / __builtin_sqrt(v); }
-
-DEV R gate_value(R g)
-{
-    if (ACT == 0) return g;
-    if (ACT == 3) return tanh_of(g);
-    const R s = inverse((R)1 + exp_of(-g));
-    return ACT == 1 ? s : g * s;
-}
-
-// tanh(g) from e = exp(-2 |g|) and r = 1 / (1 + e); below 1/4, where 1 - e would cancel, its series to g^9 (what
-// follows is under 2^-26 of it there).  Doubles take the function itself.
-DEV float tanh_from(float g, float e, float r)
-{
-    const float t = (1.0f - e) * r, g2 = g * g;
-    const float small = g * (1.0f + g2 * (-1.0f / 3 + g2 * (2.0f / 15 + g2 * (-17.0f / 315 + g2 * (62.0f / 2835)))));
-    return g2 < 0.0625f ? small : g < 0 ? -t : t;
-}
-DEV double tanh_from(double g, double, double) { return tanh(g); }
-
-// act'(g) and act(g).  The sigmoid and its complement are q = e / (1 + e) and 1 - q, e = exp(-|g|), and the slope
-// their product; with 1 - s from s it would carry a rounding of 1 (17% of it at 15, all of it at 17).  tanh's
-// slope is 4 e / (1 + e)^2 with e = exp(-2 |g|), not 1 - tanh^2.  SiLU's complement is a small term beside 1 there.
-DEV R gate_slope(R g, R &value)
-{
-    if (ACT == 0) {
-        value = g;
-        return (R)1;
-    }
-    if (ACT == 3) {
-        const R e = exp_of(g < 0 ? 2 * g : -2 * g), r = inverse((R)1 + e);
-        value = tanh_from(g, e, r);
-        return 4 * (e * r * r);
-    }
-    if (ACT == 1) {
-        const R e = exp_of(g < 0 ? g : -g), q = e * inverse((R)1 + e);
-        value = g < 0 ? q : (R)1 - q;
-        return q * ((R)1 - q);
-    }
-    const R s = inverse((R)1 + exp_of(-g));
-    value = g * s;
-    return s * ((R)1 + g * ((R)1 - s));
 }
 
 #define ROW_SETUP                                                       \
@@ -461,9 +319,9 @@ cgtp_join_fwd(const T *__restrict__ res, const T *__restrict__ f, long f_ld, con
         load_cols(res + n * D, lane, rv);
         if (GATE == 2) {
             load_channels(gate + n * gate_ld, lane, b);
-            EACH_C(c) b[c] = gate_value(b[c]) * ws[c];
+            EACH_C(c) b[c] = act_value(b[c]) * ws[c];
         } else {
-            const R a = GATE == 1 ? gate_value((R)gate[n * gate_ld]) : (R)1;
+            const R a = GATE == 1 ? act_value((R)gate[n * gate_ld]) : (R)1;
             EACH_C(c) b[c] = a * ws[c];
         }
         if (POST) {
@@ -515,7 +373,7 @@ cgtp_join_bwd(const T *__restrict__ dh, const T *__restrict__ du, const T *__res
     {
         R e[EPL], y[EPL], g[NC], t[NC], a = 1, slope = 0, dot = 0;
         if (GATE == 2 && !LATE) load_channels(gate + n * gate_ld, lane, g);
-        if (GATE == 1) slope = gate_slope((R)gate[n * gate_ld], a);
+        if (GATE == 1) slope = act_slope((R)gate[n * gate_ld], a);
         if (!LATE) load_cols(f + n * f_ld, lane, y);
         if (dh) {
             load_cols(dh + n * D, lane, e);
@@ -563,7 +421,7 @@ cgtp_join_bwd(const T *__restrict__ dh, const T *__restrict__ du, const T *__res
         {
             R value = a;
             if (GATE == 2) {
-                const R s = gate_slope(g[c], value);
+                const R s = act_slope(g[c], value);
                 g[c] = s * (t[c] * ws[c]);
             }
             if (part && on) P[c] += t[c] * value;

@@ -1,0 +1,487 @@
+// HIP source of the experts' products over irreps rows, out[n] = sum_j p[n][j] W[e(n, j)] x[n], and of
+// their gradients.  linear.cpp puts a plan's constants and the shared text (row_kernels.h) in front of
+// this text and compiles it for gfx950.
+//
+// Constants of a plan, beside T, R and ACT:
+//   E, K          experts; experts of a row (0: the one expert of every row, with weight 1)
+//   NUMEL         weights of an expert
+//   Forward, Backward: the product's two directions, each a struct of
+//     NOUT, O_COL, O_MUL, O_K, O_P0, O_PN   output irreps: first column, channels, 2l+1, first path, paths
+//     P_COL, P_MUL, P_W                     paths: the input irrep's first column and channels, the matrix
+//                                           [O_MUL][P_MUL] (row major) in the expert's weights
+//     NU, U_OUT, U_N0, U_NN, U_WAVE, WAVES  units: output irrep, first and number of its blocks of 16 channels,
+//                                           the wave that takes it; waves of a workgroup
+//   NPATH, W_*    for the weight gradients, per path: W_XC, W_MI the input's first column and channels, W_GC, W_MO
+//                 the output's, W_K, W_OFF the first weight
+//   NT, T_PATH, T_V, T_U, T_CV, T_CU          tiles of the gradients: path, first output and input channel,
+//                                             channels a lane holds of each (times 16 in the tile)
+#pragma once
+
+namespace cgtp {
+
+static const char kLinearKernels[] = R"HIP(
+typedef R V4 __attribute__((ext_vector_type(4)));
+constexpr bool HALF = sizeof(T) == 2;
+constexpr int KL = HALF ? 8 : 4;  // input channels that a lane holds of a step
+constexpr int STEP = 4 * KL;      // input channels of a step
+constexpr int BIG = 0x7fffffff;
+
+// ---------------------------------------------------------------- matrix instructions
+// 16x16 blocks.  Lane l holds row (or column) l % 16 of an operand and, of the summed index, the values
+// of its quarter l / 16: which ones they are does not matter as long as both operands agree, so a lane takes
+// KL neighbouring channels, all 2l+1 components of each: one run of its row, straight into registers.  The
+// product is formed transposed (rows: output channels, columns: nodes), which leaves a lane with four
+// neighbouring channels of one node, one run again, and with the node's own weight.
+// Of the result, lane l has column l % 16 and rows 4 (l / 16) + i (f64: l / 16 + 4 i).
+DEV int row_channel(int row) { return sizeof(T) == 8 ? row / 4 + 4 * (row % 4) : row; }
+
+#if defined(BITS16)
+typedef T V8 __attribute__((ext_vector_type(8)));
+DEV V4 mfma(V8 a, V8 b, V4 c)
+{
+#if BITS16 == 1
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+#else
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
+#endif
+}
+#endif
+)HIP"
+R"HIP(
+// N neighbouring elements as they are
+template <int N> DEV void load_raw(const T *p, T *x)
+{
+    if constexpr (N > 0) {
+        constexpr int W = 16 / sizeof(T);
+        constexpr int n = N >= W ? W : N >= 8 ? 8 : N >= 4 ? 4 : N >= 2 ? 2 : 1;
+        typedef T V __attribute__((ext_vector_type(n), aligned(sizeof(T))));
+        if constexpr (n == 1) {
+            x[0] = p[0];
+        } else {
+            const V r = *reinterpret_cast<const V *>(p);
+#pragma unroll
+            for (int i = 0; i < n; ++i) x[i] = r[i];
+        }
+        load_raw<N - n>(p + n, x + n);
+    }
+}
+
+// `count` of N channels of KC elements, zeros for the others; ALL: every one is there
+template <int N, int KC, bool ALL> DEV void load_channels(const T *p, int count, T *x)
+{
+    if (ALL || count >= N) {
+        load_raw<N * KC>(p, x);
+    } else {
+#pragma unroll
+        for (int i = 0; i < N * KC; ++i) x[i] = i < count * KC ? p[i] : (T)0;
+    }
+}
+
+// acc[n][m] += A[n] B[m] over a step of STEP channels; a: KL per block, b: KL channels of KC components
+template <int NN, int KC> DEV void step(const T (&a)[NN][KL], const T (&b)[KL * KC], V4 (&acc)[NN][KC])
+{
+#if defined(BITS16)
+    V8 bv[KC];
+#pragma unroll
+    for (int m = 0; m < KC; ++m)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) bv[m][i] = b[i * KC + m];
+#pragma unroll
+    for (int n = 0; n < NN; ++n) {
+        V8 av;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) av[i] = a[n][i];
+#pragma unroll
+        for (int m = 0; m < KC; ++m) acc[n][m] = mfma(av, bv[m], acc[n][m]);
+    }
+#else
+#pragma unroll
+    for (int i = 0; i < KL; ++i)
+#pragma unroll
+        for (int n = 0; n < NN; ++n)
+#pragma unroll
+            for (int m = 0; m < KC; ++m) acc[n][m] = MFMA(a[n][i], b[i * KC + m], acc[n][m]);
+#endif
+}
+
+// One path's product of an expert: w its matrix, x the node's row
+template <class D, int O, int P, int N0, int NN> DEV void path(const T *w, const T *x, int lane, V4 (&acc)[NN][D::O_K[O]])
+{
+    constexpr int KC = D::O_K[O], MI = D::P_MUL[P], MO = D::O_MUL[O];
+    const int g = lane >> 4, v = N0 * 16 + row_channel(lane & 15);
+    x += D::P_COL[P] + g * KL * KC;
+    w += D::P_W[P] + g * KL;
+    int left = MI - g * KL;
+    // channels past the irrep's end: their products are not stored, so any row of the matrix does for them
+    int row[NN];
+#pragma unroll
+    for (int n = 0; n < NN; ++n) row[n] = (v + n * 16 < MO ? v + n * 16 : MO - 1) * MI;
+    for (int k = 0; k < MI / STEP; ++k) {
+        T b[KL * KC], a[NN][KL];
+        load_raw<KL * KC>(x, b);
+#pragma unroll
+        for (int n = 0; n < NN; ++n) load_raw<KL>(w + row[n], a[n]);
+        step<NN, KC>(a, b, acc);
+        x += STEP * KC;
+        w += STEP;
+        left -= STEP;
+    }
+    if constexpr (MI % STEP != 0) {
+        T b[KL * KC], a[NN][KL];
+        load_channels<KL, KC, false>(x, left, b);
+#pragma unroll
+        for (int n = 0; n < NN; ++n) load_channels<KL, 1, false>(w + row[n], left, a[n]);
+        step<NN, KC>(a, b, acc);
+    }
+}
+
+template <class D, int O, int P, int END, int N0, int NN>
+DEV void paths(const T *w, const T *x, int lane, V4 (&acc)[NN][D::O_K[O]])
+{
+    if constexpr (P < END) {
+        path<D, O, P, N0, NN>(w, x, lane, acc);
+        paths<D, O, P + 1, END, N0, NN>(w, x, lane, acc);
+    }
+}
+
+// the smallest over the 16 nodes, the same in every lane of the wave
+DEV int wave_min(int v)
+{
+    int o = __builtin_amdgcn_mov_dpp(v, 0xB1, 15, 15, false);
+    v = o < v ? o : v;
+    o = __builtin_amdgcn_mov_dpp(v, 0x4E, 15, 15, false);
+    v = o < v ? o : v;
+    o = __builtin_amdgcn_mov_dpp(v, 0x141, 15, 15, false);
+    v = o < v ? o : v;
+    o = __builtin_amdgcn_mov_dpp(v, 0x140, 15, 15, false);
+    v = o < v ? o : v;
+    return __builtin_amdgcn_readfirstlane(v);
+}
+
+constexpr int KS = K > 0 ? K : 1;
+
+struct Node {
+    const T *in;   // its row of the product's input
+    const T *dot;  // Backward: its row of x, for the gradient of its weights; NULL without
+    T *out;
+    bool live;
+    int e[KS];     // its experts, BIG where there is none
+    R p[KS];
+};
+
+// A wave's 16 nodes take the experts that any of them has in rising order.  A node's sum is of its own
+// experts alone, each product scaled in R and added to it (others are not added, so what they hold cannot
+// reach it), and so depends neither on its neighbours nor on the order of the rows.
+template <class D, int U> DEV void unit(const Node &node, const T *w, int lane, R (&dp)[KS])
+{
+    constexpr int O = D::U_OUT[U], N0 = D::U_N0[U], NN = D::U_NN[U], KC = D::O_K[O], MO = D::O_MUL[O];
+    constexpr int P0 = D::O_P0[O], PN = D::O_PN[O];
+    const int v0 = N0 * 16 + 4 * (lane >> 4);  // the lane's first channel
+    V4 total[NN][KC];
+#pragma unroll
+    for (int n = 0; n < NN; ++n)
+#pragma unroll
+        for (int m = 0; m < KC; ++m) total[n][m] = (V4)(R)0;
+    if constexpr (PN > 0) {
+        int last = -1;
+        for (;;) {
+            int next = BIG;
+            if (K > 0) {
+#pragma unroll
+                for (int j = 0; j < K; ++j) next = node.e[j] > last && node.e[j] < next ? node.e[j] : next;
+                next = wave_min(next);
+                if (next == BIG) break;
+            }
+            const T *we = w + (K > 0 ? (long)next * NUMEL : 0);
+            V4 acc[NN][KC];
+#pragma unroll
+            for (int n = 0; n < NN; ++n)
+#pragma unroll
+                for (int m = 0; m < KC; ++m) acc[n][m] = (V4)(R)0;
+            paths<D, O, P0, P0 + PN, N0, NN>(we, node.in, lane, acc);
+            if (K == 0) {
+#pragma unroll
+                for (int n = 0; n < NN; ++n)
+#pragma unroll
+                    for (int m = 0; m < KC; ++m) total[n][m] = acc[n][m];
+                break;
+            }
+            R p = 0;
+            bool has = false;
+#pragma unroll
+            for (int j = 0; j < K; ++j)
+                if (node.e[j] == next) {
+                    p += node.p[j];
+                    has = true;
+                }
+#pragma unroll
+            for (int n = 0; n < NN; ++n)
+#pragma unroll
+                for (int m = 0; m < KC; ++m)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) total[n][m][i] = has ? fma(p, acc[n][m][i], total[n][m][i]) : total[n][m][i];
+            if (D::DOT && node.dot) {
+                R s = 0;
+#pragma unroll
+                for (int n = 0; n < NN; ++n) {
+                    T x[4 * KC];
+                    load_channels<4, KC, false>(node.dot + D::O_COL[O] + (v0 + n * 16) * KC, MO - v0 - n * 16, x);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+#pragma unroll
+                        for (int m = 0; m < KC; ++m)
+                            if (v0 + n * 16 + i < MO) s = fma(acc[n][m][i], (R)x[i * KC + m], s);
+                }
+                s = swap32(swap16(s));
+#pragma unroll
+                for (int j = 0; j < K; ++j) dp[j] += node.e[j] == next ? s : (R)0;
+            }
+            last = next;
+        }
+    }
+    if (!node.live || !node.out) return;
+#pragma unroll
+    for (int n = 0; n < NN; ++n) {
+        R v[4 * KC];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int m = 0; m < KC; ++m) v[i * KC + m] = total[n][m][i];
+        const int count = MO - v0 - n * 16;
+        T *out = node.out + D::O_COL[O] + (v0 + n * 16) * KC;
+        if ((N0 + n + 1) * 16 <= MO || count >= 4) {
+            store_run<4 * KC>(out, v);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4 * KC; ++i)
+                if (i < count * KC) out[i] = (T)v[i];
+        }
+    }
+}
+
+template <class D, int U = 0> DEV void units(const Node &node, const T *w, int wave, int lane, R (&dp)[KS])
+{
+    if constexpr (U < D::NU) {
+        if (D::U_WAVE[U] == wave) unit<D, U>(node, w, lane, dp);
+        units<D, U + 1>(node, w, wave, lane, dp);
+    }
+}
+
+template <class D>
+DEV void product(const T *in, long in_ld, const T *w, const int *experts, const R *weights, const int *order, long N,
+                 T *out, long out_ld, const T *dot, long dot_ld, R *grad_weights, R *lds)
+{
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+    const long at = (long)blockIdx.x * 16 + (lane & 15);
+    long n = at < N ? at : N - 1;
+    if (order) n = order[n];
+    Node node;
+    node.live = at < N && n >= 0 && n < N;
+    n = n < 0 ? 0 : n < N ? n : N - 1;
+    node.in = in + n * in_ld;
+    node.out = out ? out + n * out_ld : nullptr;
+    node.dot = dot ? dot + n * dot_ld : nullptr;
+    R dp[KS];
+#pragma unroll
+    for (int j = 0; j < KS; ++j) {
+        const int e = K > 0 ? experts[n * K + j] : BIG;
+        const bool has = node.live && e >= 0 && e < E;
+        node.e[j] = has ? e : BIG;
+        node.p[j] = has ? weights[n * K + j] : (R)0;
+        dp[j] = 0;
+    }
+    units<D>(node, w, wave, lane, dp);
+    if (K > 0 && D::DOT && grad_weights) {
+        // the waves' shares of a node's sum, in the waves' order
+#pragma unroll
+        for (int j = 0; j < K; ++j)
+            if (lane < 16) lds[(wave * 16 + lane) * KS + j] = dp[j];
+        __syncthreads();
+        for (int t = threadIdx.x; t < 16 * K; t += D::WAVES * 64) {
+            const int i = t / KS, j = t % KS;
+            R s = 0;
+#pragma unroll
+            for (int v = 0; v < D::WAVES; ++v) s += lds[(v * 16 + i) * KS + j];
+            const long a = (long)blockIdx.x * 16 + i;
+            const long row = a < N ? (order ? order[a] : a) : -1;
+            if (row >= 0 && row < N) grad_weights[row * K + j] = s;
+        }
+    }
+}
+
+extern "C" __global__ void __launch_bounds__(Forward::WAVES * 64)
+cgtp_linear_fwd(const T *__restrict__ x, long x_ld, const T *__restrict__ w, const int *__restrict__ experts,
+                const R *__restrict__ weights, const int *__restrict__ order, long N, T *__restrict__ out, long out_ld)
+{
+    product<Forward>(x, x_ld, w, experts, weights, order, N, out, out_ld, nullptr, 0, nullptr, nullptr);
+}
+
+// grad_x and the gradient of the weights p: dp[n][j] = <x[n], W^T g[n]>.  w holds the transposed matrices.
+extern "C" __global__ void __launch_bounds__(Backward::WAVES * 64)
+cgtp_linear_bwd_x(const T *__restrict__ g, long g_ld, const T *__restrict__ w, const int *__restrict__ experts,
+                  const R *__restrict__ weights, const int *__restrict__ order, long N, T *__restrict__ grad_x,
+                  long grad_x_ld, const T *__restrict__ x, long x_ld, R *__restrict__ grad_weights)
+{
+    __shared__ R lds[Backward::WAVES * 16 * KS];
+    product<Backward>(g, g_ld, w, experts, weights, order, N, grad_x, grad_x_ld, grad_weights ? x : nullptr, x_ld,
+                      grad_weights, lds);
+}
+
+// every matrix [mul_out][mul_in] transposed, in its place
+extern "C" __global__ void __launch_bounds__(256) cgtp_linear_transpose(const T *__restrict__ w, T *__restrict__ wt)
+{
+    const int i = blockIdx.x * 256 + threadIdx.x;
+    if (i >= NUMEL) return;
+    int p = 0;
+    for (int k = 1; k < NPATH; ++k) p = i >= W_OFF[k] ? k : p;
+    const int at = i - W_OFF[p], u = at / W_MO[p], v = at % W_MO[p];
+    const long base = (long)blockIdx.y * NUMEL;
+    wt[base + i] = w[base + W_OFF[p] + v * W_MI[p] + u];
+}
+)HIP"
+R"HIP(
+// ---------------------------------------------------------------- weight gradients
+// dW[e][v][u] = sum over the expert's slots of p sum_m g[v][m] x[u][m].  A wave takes a stretch of one
+// expert's slots and one tile of a path; nodes are the summed index.  A lane holds neighbouring
+// channels here too, T_CV (T_CU) of them: channel 16-blocks of a tile are interleaved, block j having every
+// T_CV-th channel from j on.  16-bit operands take g p rounded to T: one rounding more of each term.
+constexpr int NL = HALF ? 8 : 1;  // nodes of a lane's quarter in a step
+
+struct Stretch {
+    int expert;
+    long begin, end;
+};
+
+// Stretches are numbered floor(offsets[e] / len) + e upwards for expert e: there is room for each one's
+// ceil(count / len), since floor((o + c) / len) - floor(o / len) + 1 is at least that.
+DEV Stretch stretch_of(const int *offsets, long count, long len, long number, int lane)
+{
+    if (!offsets) {
+        const long b = number * len;
+        return {0, b, b + len < count ? b + len : count};
+    }
+    int below = 0;
+    for (int e0 = 0; e0 < E; e0 += 64) {
+        const int e = e0 + lane;
+        bool is = false;
+        if (e < E) {
+            const long o = offsets[e];
+            is = (o < 0 ? 0 : o > count ? count : o) / len + e <= number;
+        }
+        below += __popcll(__ballot(is));
+    }
+    const int e = below > 0 ? below - 1 : 0;
+    long lo = offsets[e], hi = offsets[e + 1];
+    lo = lo < 0 ? 0 : lo > count ? count : lo;
+    hi = hi < lo ? lo : hi > count ? count : hi;
+    const long b = lo + (number - (lo / len + e)) * len;
+    return {e, b < lo ? hi : b, b + len < hi ? b + len : hi};
+}
+
+template <int I> DEV void tile(const T *x, long x_ld, const T *g, long g_ld, const R *weights, const int *slots,
+                               Stretch s, long N, long count, R *part, int lane)
+{
+    constexpr int P = T_PATH[I], KC = W_K[P], CV = T_CV[I], CU = T_CU[I], MO = W_MO[P], MI = W_MI[P];
+    const int a = lane & 15, quarter = lane >> 4;
+    const int v = T_V[I] + a * CV, u = T_U[I] + a * CU;  // the lane's first channels
+    const int nv = MO - v < 0 ? 0 : MO - v, nu = MI - u < 0 ? 0 : MI - u;
+    V4 acc[CV][CU];
+#pragma unroll
+    for (int j = 0; j < CV; ++j)
+#pragma unroll
+        for (int k = 0; k < CU; ++k) acc[j][k] = (V4)(R)0;
+    for (long s0 = s.begin; s0 < s.end; s0 += 4 * NL) {
+        T gr[NL][CV * KC], xr[NL][CU * KC];
+#pragma unroll
+        for (int t = 0; t < NL; ++t) {
+            const long at = s0 + quarter * NL + t;
+            bool in = at < s.end;
+            long slot = in ? (slots ? slots[at] : at) : 0;
+            in = in && slot >= 0 && slot < count;
+            slot = in ? slot : 0;
+            const long n = slot / KS;
+            const R p = K > 0 ? weights[slot] : (R)1;
+            load_channels<CV, KC, false>(g + n * g_ld + W_GC[P] + v * KC, in ? nv : 0, gr[t]);
+            load_channels<CU, KC, false>(x + n * x_ld + W_XC[P] + u * KC, in ? nu : 0, xr[t]);
+            if (K > 0) {
+#pragma unroll
+                for (int i = 0; i < CV * KC; ++i) gr[t][i] = in ? (T)((R)gr[t][i] * p) : (T)0;
+            }
+        }
+#pragma unroll
+        for (int m = 0; m < KC; ++m) {
+#if defined(BITS16)
+            V8 xv[CU];
+#pragma unroll
+            for (int k = 0; k < CU; ++k)
+#pragma unroll
+                for (int t = 0; t < 8; ++t) xv[k][t] = xr[t][k * KC + m];
+#pragma unroll
+            for (int j = 0; j < CV; ++j) {
+                V8 gv;
+#pragma unroll
+                for (int t = 0; t < 8; ++t) gv[t] = gr[t][j * KC + m];
+#pragma unroll
+                for (int k = 0; k < CU; ++k) acc[j][k] = mfma(gv, xv[k], acc[j][k]);
+            }
+#else
+#pragma unroll
+            for (int j = 0; j < CV; ++j)
+#pragma unroll
+                for (int k = 0; k < CU; ++k) acc[j][k] = MFMA(gr[0][j * KC + m], xr[0][k * KC + m], acc[j][k]);
+#endif
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < CV; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int row = sizeof(T) == 8 ? quarter + 4 * i : 4 * quarter + i, vo = T_V[I] + row * CV + j;
+            if (vo < MO) {
+#pragma unroll
+                for (int k = 0; k < CU; ++k)
+                    if (k < nu) part[W_OFF[P] + vo * MI + u + k] = acc[j][k][i];
+            }
+        }
+}
+
+template <int I = 0> DEV void tiles(int which, const T *x, long x_ld, const T *g, long g_ld, const R *weights,
+                                    const int *slots, Stretch s, long N, long count, R *part, int lane)
+{
+    if constexpr (I < NT) {
+        if (which == I)
+            tile<I>(x, x_ld, g, g_ld, weights, slots, s, N, count, part, lane);
+        else
+            tiles<I + 1>(which, x, x_ld, g, g_ld, weights, slots, s, N, count, part, lane);
+    }
+}
+
+extern "C" __global__ void __launch_bounds__(64)
+cgtp_linear_bwd_w(const T *__restrict__ x, long x_ld, const T *__restrict__ g, long g_ld, const R *__restrict__ weights,
+                  const int *__restrict__ slots, const int *__restrict__ offsets, long N, long count, long len,
+                  R *__restrict__ part)
+{
+    const int lane = threadIdx.x;
+    const Stretch s = stretch_of(offsets, count, len, blockIdx.y, lane);
+    if (s.begin >= s.end) return;
+    tiles(blockIdx.x, x, x_ld, g, g_ld, weights, slots, s, N, count, part + (long)blockIdx.y * NUMEL, lane);
+}
+
+// the stretches of each expert, in their order; zeros for an expert without slots
+extern "C" __global__ void __launch_bounds__(256)
+cgtp_linear_reduce(const R *__restrict__ part, const int *__restrict__ offsets, long count, long len, T *__restrict__ grad_w)
+{
+    const int i = blockIdx.x * 256 + threadIdx.x, e = blockIdx.y;
+    if (i >= NUMEL) return;
+    long lo = offsets ? offsets[e] : 0, hi = offsets ? offsets[e + 1] : count;
+    lo = lo < 0 ? 0 : lo > count ? count : lo;
+    hi = hi < lo ? lo : hi > count ? count : hi;
+    const long first = lo / len + e, n = (hi - lo + len - 1) / len;
+    double sum = 0;
+#pragma unroll 8
+    for (long c = 0; c < n; ++c) sum += (double)part[(first + c) * NUMEL + i];
+    grad_w[(long)e * NUMEL + i] = (T)(R)sum;
+}
+)HIP";
+
+}  // namespace cgtp

@@ -627,6 +627,167 @@ cgtp_status cgtp_join_backward(const cgtp_block *block, int64_t N, const void *g
                                void *workspace, size_t workspace_bytes, void *stream);
 
 /*
+ * Group norm with an activation over a batch of graphs, channels last.  Graph b holds the rows
+ * ptr[b]..ptr[b+1] of N (device, int32[S+1], not decreasing, within [0, N]; an empty graph is none of the
+ * rows); group g the channels g*C/G..(g+1)*C/G.  Over a graph's rows and a group's channels, with m
+ * their mean and v the mean of (x - m)^2:
+ *   z = (x - m) rstd w[c] + bias[c],  rstd = (v + eps)^(-1/2),  y = act(z).
+ * Features are scalars ("Cx0e": a mean has no meaning for higher degrees); they may be the first columns of wider
+ * rows (pitches).  Rows of no graph (before ptr[0], from ptr[S] on) are not read; in y and grad_x they are set to zero
+ * where `fill` is not 0 and left as they were where it is.
+ * Types: x, y and their gradients are of the norm's dtype; statistics, weights and weight gradients are
+ * float (double for CGTP_F64), and so is all arithmetic.
+ * Compiled, loaded and destroyed as a block is (cgtp_block_create).  CGTP_ERR_UNSUPPORTED: over 2048 channels.
+ */
+typedef struct cgtp_group_norm cgtp_group_norm; /* opaque, immutable after creation */
+
+typedef struct cgtp_group_norm_config {
+    int32_t dtype;    /* cgtp_dtype                         */
+    int32_t channels; /* a multiple of groups, at most 2048 */
+    int32_t groups;
+    int32_t act;      /* cgtp_act                           */
+    double eps;       /* > 0                                */
+} cgtp_group_norm_config;
+
+cgtp_status cgtp_group_norm_create(const cgtp_group_norm_config *config, cgtp_group_norm **norm_out);
+cgtp_status cgtp_group_norm_destroy(cgtp_group_norm *norm); /* NULL is ignored */
+const char *cgtp_group_norm_source(const cgtp_group_norm *norm);
+/* Workspace of a pass over N rows in S graphs: 256-byte aligned, caller-owned, contents ignored on entry. */
+cgtp_status cgtp_group_norm_workspace_size(const cgtp_group_norm *norm, int64_t N, int64_t S, int32_t backward,
+                                           size_t *bytes);
+/*
+ * w and bias [C] may be NULL (ones, zeros).  mean and rstd [S][G] receive the statistics for the backward (both
+ * or neither; an empty graph's are 0 and eps^(-1/2)).  S = 0 is a no-op.
+ */
+cgtp_status cgtp_group_norm_forward(const cgtp_group_norm *norm, int64_t N, int64_t S, const int32_t *ptr, const void *x,
+                                    int64_t x_ld, const void *w, const void *bias, void *y, int64_t y_ld, int32_t fill,
+                                    void *mean, void *rstd, void *workspace, size_t workspace_bytes, void *stream);
+/*
+ * Its backward: with xh = (x - mean) rstd, dz = grad_y act'(z), q = dz w and means over a graph's group,
+ *   grad_x = rstd (q - mean q - xh mean(q xh)),  grad_w = sum_rows dz xh,  grad_bias = sum_rows dz.
+ * Any output may be NULL.  No atomics, bitwise deterministic; N = 0 or S = 0 sets the weight gradients to zero.
+ */
+cgtp_status cgtp_group_norm_backward(const cgtp_group_norm *norm, int64_t N, int64_t S, const int32_t *ptr,
+                                     const void *x, int64_t x_ld, const void *w, const void *bias, const void *mean,
+                                     const void *rstd, const void *grad_y, int64_t grad_y_ld, void *grad_x,
+                                     int64_t grad_x_ld, int32_t fill, void *grad_w, void *grad_bias,
+                                     void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * Routing of rows to experts.  From the logits l of a row, over E experts:
+ *   scores   s = softmax(l) or sigmoid(l);  for the choice alone  c = s + bias;
+ *   groups   where top_groups < groups: of `groups` groups of E/groups neighbouring experts, the top_groups
+ *            with the largest sums of their best two c (best one, where there is one) are kept;
+ *   choice   the top_k experts of the kept groups with the largest c, in falling order, of equal ones (groups
+ *            too) the lowest first;
+ *   weights  scale s, or with renormalise scale s / (sum of the chosen s) (0 where that sum is 0).
+ * A logit or a c of -inf masks its expert: it is never chosen and its score is 0; a row with too few others has
+ * -1 in the places that are left, with weight 0.  A c that is not a number comes after every other one that is not masked.
+ * s and c are formed in double for every type.
+ *
+ * Types: logits and their gradient are of the router's dtype; bias, weights and their gradient float (double for
+ * CGTP_F64).  Compiled, loaded and destroyed as a block is (cgtp_block_create).
+ * CGTP_ERR_UNSUPPORTED: over 512 experts, 32 of a row, 64 groups, or so many wide groups that a lane of a wave
+ * would hold more than 16 experts.
+ */
+typedef enum cgtp_score { CGTP_SCORE_SOFTMAX = 0, CGTP_SCORE_SIGMOID = 1 } cgtp_score;
+
+typedef struct cgtp_router cgtp_router; /* opaque, immutable after creation */
+
+typedef struct cgtp_router_config {
+    int32_t dtype;      /* cgtp_dtype of the logits                */
+    int32_t score;      /* cgtp_score                              */
+    int32_t experts;
+    int32_t top_k;
+    int32_t groups;     /* divides experts; 1: none                */
+    int32_t top_groups;
+    int32_t renormalise;
+    double scale;
+} cgtp_router_config;
+
+cgtp_status cgtp_router_create(const cgtp_router_config *config, cgtp_router **router_out);
+cgtp_status cgtp_router_destroy(cgtp_router *router); /* NULL is ignored */
+const char *cgtp_router_source(const cgtp_router *router);
+/* logits: N rows, logits_ld elements apart; bias [E] or NULL; experts, weights [N][top_k].  N = 0 is a no-op. */
+cgtp_status cgtp_route_forward(const cgtp_router *router, int64_t N, const void *logits, int64_t logits_ld,
+                               const void *bias, int32_t *experts, void *weights, void *stream);
+/* grad_logits [N][E]: the gradient of <grad_weights, weights>, the choice held fixed (the bias has none).  An
+ * expert outside [0, E) is a place that was left. */
+cgtp_status cgtp_route_backward(const cgtp_router *router, int64_t N, const void *logits, int64_t logits_ld,
+                                const int32_t *experts, const void *grad_weights, void *grad_logits, void *stream);
+/*
+ * The lists that the experts' products go by, from experts [N][top_k] of a router of this E and top_k:
+ *   slots   [N*top_k]: slot numbers n*top_k + j by expert (those without one last), else in their order;
+ *   offsets [E+1]: each expert's first place in slots, then the end of the last one's;
+ *   rows    [N]: rows by their lowest expert, or for top_k > 1 by the pair (a, b) of their two lowest (b = a for
+ *           one), of which b counts in min(E, 4096/E) bins; else in their order; rows without an expert last.
+ * Stable counting sorts, bitwise deterministic.  N * top_k < 2^31.  N = 0 sets offsets to zero.  Workspace: 256-byte
+ * aligned, caller-owned, contents ignored on entry (size 0 for short lists).
+ */
+cgtp_status cgtp_route_order_workspace_size(const cgtp_router *router, int64_t N, size_t *bytes);
+cgtp_status cgtp_route_order(const cgtp_router *router, int64_t N, const int32_t *experts, int32_t *rows, int32_t *slots,
+                             int32_t *offsets, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * Experts' products over irreps rows: with p = weights[n][j] and e = experts[n][j],
+ *   out[n] = sum_j p W_e x[n],
+ * W_e one matrix [mul_out][mul_in] (row major) for each pair of equal irreps (degree and parity) of input and output,
+ * by input irreps and then output ones; it mixes channels and leaves components alone, so it commutes with rotations.  w
+ * is [experts][weight_numel], the matrices of an expert one after the other; a lane reads neighbouring input
+ * channels of an output channel, which is why they are the inner index.  An output irrep without a pair is zero.  A slot whose
+ * expert lies outside [0, experts) takes no part, and what a row has not chosen does not reach it, finite or not;
+ * an expert that a row names twice counts twice.  top_k = 0 (experts = 1) is the plain linear layer, out = W x, which takes no experts,
+ * weights or lists.
+ *
+ * rows, slots and offsets are those of cgtp_route_order for these experts (a router of this E and top_k).  rows only
+ * sets which rows are worked on together (NULL: as they lie) and changes no bit of any result; an entry of
+ * rows or slots out of range is passed over.
+ *
+ * Types: x, w, out and their gradients are of the linear's dtype; weights and their gradient float (double for
+ * CGTP_F64), and so are all sums.  In 16 bits the weight gradient takes the products p grad_out rounded to the type.
+ * Compiled, loaded and destroyed as a block is (cgtp_block_create).  CGTP_ERR_IRREPS: no equal irreps.
+ * CGTP_ERR_UNSUPPORTED: over 512 experts, 32 of a row, 64 pairs, 2^26 weights of an expert, or thousands of channels.
+ */
+typedef struct cgtp_linear cgtp_linear; /* opaque, immutable after creation */
+
+typedef struct cgtp_linear_config {
+    int32_t dtype;   /* cgtp_dtype                                   */
+    int32_t experts;
+    int32_t top_k;   /* experts of a row; 0: one for all, unweighted */
+} cgtp_linear_config;
+
+typedef struct cgtp_linear_info {
+    int32_t d_in, d_out; /* columns            */
+    int32_t num_paths;   /* pairs              */
+    int32_t dtype;
+    int64_t weight_numel;
+} cgtp_linear_info;
+
+cgtp_status cgtp_linear_create(const char *in_irreps, const char *out_irreps, const cgtp_linear_config *config,
+                               cgtp_linear **linear_out);
+cgtp_status cgtp_linear_destroy(cgtp_linear *linear); /* NULL is ignored */
+cgtp_status cgtp_linear_info_get(const cgtp_linear *linear, cgtp_linear_info *info);
+const char *cgtp_linear_source(const cgtp_linear *linear);
+/* x and out: N rows, x_ld and out_ld elements apart; experts, weights [N][top_k].  N = 0 is a no-op.  N * top_k < 2^31. */
+cgtp_status cgtp_linear_forward(const cgtp_linear *linear, int64_t N, const void *x, int64_t x_ld, const void *w,
+                                const int32_t *experts, const void *weights, const int32_t *rows, void *out,
+                                int64_t out_ld, void *stream);
+/*
+ * Its backward, g = grad_out:
+ *   grad_x[n] = sum_j p W_e^T g[n],  grad_weights[n][j] = <g[n], W_e x[n]> (0 for a slot that takes no part),
+ *   grad_w[e] = sum over the slots of e of p g[n] x[n]^T, summed over components (0 for an expert without rows).
+ * Any output may be NULL; x is read for the last two, w for the first two, slots and offsets for grad_w.  No
+ * atomics, bitwise deterministic; N = 0 sets grad_w to zero.  Workspace: 256-byte aligned, caller-owned,
+ * contents ignored on entry.
+ */
+cgtp_status cgtp_linear_workspace_size(const cgtp_linear *linear, int64_t N, size_t *bytes);
+cgtp_status cgtp_linear_backward(const cgtp_linear *linear, int64_t N, const void *x, int64_t x_ld, const void *w,
+                                 const int32_t *experts, const void *weights, const int32_t *rows, const int32_t *slots,
+                                 const int32_t *offsets, const void *grad_out, int64_t grad_out_ld, void *grad_x,
+                                 int64_t grad_x_ld, void *grad_w, void *grad_weights, void *workspace,
+                                 size_t workspace_bytes, void *stream);
+
+/*
  * AdamW over many tensors at once.  With f = grad_scale, times max_norm / n where the scaled norm
  * n = |grad_scale| norm exceeds max_norm, and g = f grad:
  *   m = beta1 m + (1 - beta1) g,  v = beta2 v + (1 - beta2) g^2,
