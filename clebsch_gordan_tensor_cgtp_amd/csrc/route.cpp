@@ -30,7 +30,8 @@ int pow2_at_least(int n)
     return p;
 }
 
-// A lane holds at most 8 neighbouring experts of one group, 16 where a wave has no more lanes.
+// A lane holds at most 8 neighbouring experts of one group, 16 where a wave has no more lanes (512 experts in g
+// groups, fewer than 2 g of them with the power of two's empty ones, on 64 lanes).
 void lay_out(cgtp_router &r)
 {
     r.elem = elem_bytes(r.cfg.dtype);
@@ -41,7 +42,6 @@ void lay_out(cgtp_router &r)
     r.lanes_per_group = std::min(pow2_at_least((width + 7) / 8), 64 / slots);
     r.lanes = slots * r.lanes_per_group;
     r.epl = (width + r.lanes_per_group - 1) / r.lanes_per_group;
-    if (r.epl > 16) throw Error(CGTP_ERR_UNSUPPORTED, "router: a lane would hold more than 16 experts (too many groups)");
 }
 
 std::string constants(const cgtp_router &r)

@@ -194,6 +194,23 @@ cgtp_route_fwd(const T *__restrict__ logits, long ld, const R *__restrict__ bias
         sum += score[j];
     }
     if (at >= N) return;
+    if (RENORM && sum < 1e-290) {
+        // scores near or below a double's range (far under an unchosen logit, or sigmoids of under -660): their shares
+        // with the largest exponential taken out, as in the backward
+        double x[K], top = lowest(0.0);
+#pragma unroll
+        for (int j = 0; j < K; ++j) {
+            x[j] = chosen[j] < 0 ? lowest(0.0) : (double)(R)logits[row * ld + chosen[j]];
+            top = x[j] > top ? x[j] : top;
+        }
+        if (SIGMOID && top > 0.0) top = 0.0;
+        sum = 0;
+#pragma unroll
+        for (int j = 0; j < K; ++j) {
+            score[j] = chosen[j] < 0 ? 0.0 : SIGMOID ? 1.0 / (exp(top) + exp(top - x[j])) : exp(x[j] - top);
+            sum += score[j];
+        }
+    }
     const double f = RENORM ? (sum == 0.0 ? 0.0 : scale / sum) : scale;
 #pragma unroll
     for (int j = 0; j < K; ++j)

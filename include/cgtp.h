@@ -680,15 +680,14 @@ cgtp_status cgtp_group_norm_backward(const cgtp_group_norm *norm, int64_t N, int
  *            with the largest sums of their best two c (best one, where there is one) are kept;
  *   choice   the top_k experts of the kept groups with the largest c, in falling order, of equal ones (groups
  *            too) the lowest first;
- *   weights  scale s, or with renormalise scale s / (sum of the chosen s) (0 where that sum is 0).
+ *   weights  scale s, or with renormalise scale s / (sum of the chosen s), however small they are.
  * A logit or a c of -inf masks its expert: it is never chosen and its score is 0; a row with too few others has
  * -1 in the places that are left, with weight 0.  A c that is not a number comes after every other one that is not masked.
  * s and c are formed in double for every type.
  *
  * Types: logits and their gradient are of the router's dtype; bias, weights and their gradient float (double for
  * CGTP_F64).  Compiled, loaded and destroyed as a block is (cgtp_block_create).
- * CGTP_ERR_UNSUPPORTED: over 512 experts, 32 of a row, 64 groups, or so many wide groups that a lane of a wave
- * would hold more than 16 experts.
+ * CGTP_ERR_UNSUPPORTED: over 512 experts, 32 of a row, or 64 groups.
  */
 typedef enum cgtp_score { CGTP_SCORE_SOFTMAX = 0, CGTP_SCORE_SIGMOID = 1 } cgtp_score;
 
