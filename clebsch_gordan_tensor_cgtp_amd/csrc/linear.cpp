@@ -17,17 +17,23 @@ struct LinearPath {
 };
 
 struct Unit {
-    int out, first, count, wave;  // output irrep, 16-blocks of channels
-    int64_t cost;
+    int part, out, first, count, wave;  // output irrep, 16-blocks of channels
+};
+
+// an input irrep of a direction, as it lies in LDS
+struct Segment {
+    int part, col, len, lds, pad;
 };
 
 // one direction of the product
 struct Direction {
-    std::vector<int> col, mul, k, p0, pn;     // output irreps
-    std::vector<int> p_col, p_mul;            // paths, by output irrep
+    std::vector<int> col, mul, k, part, lds, p0, pn;  // output irreps
+    std::vector<int> p_lds, p_mul;                    // paths, by output irrep
     std::vector<int64_t> p_w;
+    std::vector<Segment> segments;
+    std::vector<int> in_pitch, out_pitch;             // parts, in elements
     std::vector<Unit> units;
-    int waves = 1;
+    int waves = 1, lds_bytes = 0;
 };
 
 struct Tile {
@@ -52,7 +58,7 @@ namespace cgtp {
 
 namespace {
 
-constexpr int kMaxPaths = 64, kMaxUnits = 128, kMaxWaves = 8;
+constexpr int kMaxPaths = 64, kMaxUnits = 128, kLds = 160 * 1024;
 
 void find_paths(cgtp_linear &l, const std::vector<Irrep> &ins, const std::vector<Irrep> &outs)
 {
@@ -79,45 +85,117 @@ void find_paths(cgtp_linear &l, const std::vector<Irrep> &ins, const std::vector
     if (l.numel > (1 << 26)) throw Error(CGTP_ERR_UNSUPPORTED, "linear: more than 2^26 weights of an expert");
 }
 
-// A unit's sums are held twice, of the expert at hand and of all: 16-blocks times components are
-// bounded by 160 registers of a lane for both.
-void plan_direction(cgtp_linear &l, Direction &d, const std::vector<Irrep> &outs, bool backward)
+int round_up(int n, int to) { return (n + to - 1) / to * to; }
+
+// an odd number of 16 bytes
+int odd_pitch(int elements, int vec) { return (round_up(elements, vec) / vec | 1) * vec; }
+
+// Irreps of one degree and parity belong to one part: no others read what they read.  Parts are filled up to
+// 64 KB of LDS for their rows in and out, so that two workgroups or more share a CU; a wide irrep may take all of it.
+void plan_direction(cgtp_linear &l, Direction &d, const std::vector<Irrep> &ins, const std::vector<Irrep> &outs, bool backward)
 {
+    const int vec = 16 / l.elem, step = l.elem == 2 ? 32 : 16;
+    struct Class {
+        int l, p, in, out, part;
+    };
+    std::vector<Class> classes;
+    auto class_of = [&](const Irrep &ir) -> Class & {
+        for (Class &c : classes)
+            if (c.l == ir.l && c.p == ir.p) return c;
+        classes.push_back({ir.l, ir.p, 0, 0, 0});
+        return classes.back();
+    };
+    for (const Irrep &o : outs) class_of(o).out += round_up(round_up(o.mul, 16) * (2 * o.l + 1), vec);
+    for (const Irrep &i : ins)
+        for (Class &c : classes)
+            if (c.l == i.l && c.p == i.p) c.in += round_up(i.mul, step) * (2 * i.l + 1);
+    const int budget = 64 * 1024;
+    int part = -1;
+    for (Class &c : classes) {
+        auto bytes = [&](int in, int out) { return 16 * l.elem * (odd_pitch(in, vec) + odd_pitch(out, vec)); };
+        if (part < 0 || bytes(d.in_pitch[part] + c.in, d.out_pitch[part] + c.out) > budget) {
+            d.in_pitch.push_back(0);
+            d.out_pitch.push_back(0);
+            ++part;
+        }
+        c.part = part;
+        d.in_pitch[part] += c.in;
+        d.out_pitch[part] += c.out;
+        if (bytes(d.in_pitch[part], d.out_pitch[part]) > kLds - 8 * 1024)
+            throw Error(CGTP_ERR_UNSUPPORTED, "linear: 16 rows of one degree and parity need " +
+                                                  std::to_string(bytes(d.in_pitch[part], d.out_pitch[part])) +
+                                                  " bytes of LDS, a workgroup has 155648 for them");
+    }
+    const int parts = part + 1;
+    std::vector<int> in_at(parts, 0), out_at(parts, 0);
+    std::vector<int> in_lds;
     int at = 0;
+    for (const Irrep &i : ins) {
+        const int len = i.dim(), pad = round_up(i.mul, step) * (2 * i.l + 1);
+        in_lds.push_back(-1);
+        for (const Class &c : classes)
+            if (c.l == i.l && c.p == i.p) {
+                d.segments.push_back({c.part, at, len, in_at[c.part], pad});
+                in_lds.back() = in_at[c.part];
+                in_at[c.part] += pad;
+            }
+        at += len;
+    }
+    at = 0;
     for (size_t o = 0; o < outs.size(); ++o) {
-        const int k = 2 * outs[o].l + 1, mul = outs[o].mul;
+        const int k = 2 * outs[o].l + 1, mul = outs[o].mul, in = class_of(outs[o]).part;
         d.col.push_back(at);
         d.mul.push_back(mul);
         d.k.push_back(k);
-        d.p0.push_back((int)d.p_col.size());
-        int64_t width = 0;
+        d.part.push_back(in);
+        d.lds.push_back(out_at[in]);
+        out_at[in] += round_up(round_up(mul, 16) * k, vec);
+        d.p0.push_back((int)d.p_lds.size());
         for (const LinearPath &p : l.paths)
             if ((backward ? p.in : p.out) == (int)o) {
-                d.p_col.push_back(backward ? p.out_col : p.in_col);
+                d.p_lds.push_back(in_lds[backward ? p.out : p.in]);
                 d.p_mul.push_back(backward ? p.mul_out : p.mul_in);
                 d.p_w.push_back(p.w);
-                width += d.p_mul.back();
             }
-        d.pn.push_back((int)d.p_col.size() - d.p0.back());
-        const int blocks = (mul + 15) / 16, most = std::max(1, std::min(8, (l.elem == 8 ? 10 : 20) / k));
-        const int parts = (blocks + most - 1) / most;
-        for (int i = 0; i < parts; ++i) {
-            const int first = (int)((int64_t)blocks * i / parts), end = (int)((int64_t)blocks * (i + 1) / parts);
-            d.units.push_back({(int)o, first, end - first, 0, (int64_t)(end - first) * k * width + (int64_t)k * width});
-        }
+        d.pn.push_back((int)d.p_lds.size() - d.p0.back());
         at += mul * k;
     }
-    if (d.units.size() > (size_t)kMaxUnits) throw Error(CGTP_ERR_UNSUPPORTED, "linear: too many channels");
-    // the costliest units first, each to the wave with the least to do
-    d.waves = std::min<int>(kMaxWaves, (int)d.units.size());
-    std::vector<int64_t> load(d.waves, 0);
-    std::vector<Unit *> by_cost;
-    for (Unit &u : d.units) by_cost.push_back(&u);
-    std::stable_sort(by_cost.begin(), by_cost.end(), [](const Unit *a, const Unit *b) { return a->cost > b->cost; });
-    for (Unit *u : by_cost) {
-        u->wave = (int)(std::min_element(load.begin(), load.end()) - load.begin());
-        load[u->wave] += u->cost;
+    for (int p = 0; p < parts; ++p) {
+        d.in_pitch[p] = odd_pitch(d.in_pitch[p], vec);
+        d.out_pitch[p] = odd_pitch(d.out_pitch[p], vec);
+        d.lds_bytes = std::max(d.lds_bytes, 16 * l.elem * (d.in_pitch[p] + d.out_pitch[p]));
     }
+    // eight waves where LDS leaves room for one workgroup on a CU, else four
+    d.waves = d.lds_bytes > kLds / 2 ? 8 : 4;
+    int most_units = 1;
+    for (int p = 0; p < parts; ++p) {
+        // Units: a wave's even share of the part's 16-blocks times components, no more than 20 (10 in double), since
+        // their sums are held twice (of the expert at hand, and of all): 160 registers of a lane.
+        int64_t work = 0;
+        for (size_t o = 0; o < outs.size(); ++o)
+            if (d.part[o] == p) work += (int64_t)((d.mul[o] + 15) / 16) * d.k[o];
+        const int most = (int)std::min<int64_t>(l.elem == 8 ? 10 : 20, (work + d.waves - 1) / d.waves);
+        std::vector<Unit> units;
+        for (size_t o = 0; o < outs.size(); ++o) {
+            if (d.part[o] != p) continue;
+            const int blocks = (d.mul[o] + 15) / 16, n = std::max(1, most / d.k[o]), pieces = (blocks + n - 1) / n;
+            for (int i = 0; i < pieces; ++i) {
+                const int first = (int)((int64_t)blocks * i / pieces), end = (int)((int64_t)blocks * (i + 1) / pieces);
+                units.push_back({p, (int)o, first, end - first, 0});
+            }
+        }
+        // the costliest first, each to the wave with the least to do
+        std::stable_sort(units.begin(), units.end(), [&](const Unit &a, const Unit &b) { return a.count * d.k[a.out] > b.count * d.k[b.out]; });
+        std::vector<int> load(d.waves, 0);
+        for (Unit &u : units) {
+            u.wave = (int)(std::min_element(load.begin(), load.end()) - load.begin());
+            load[u.wave] += u.count * d.k[u.out];
+        }
+        most_units = std::max<int>(most_units, (int)units.size());
+        d.units.insert(d.units.end(), units.begin(), units.end());
+    }
+    d.waves = std::min(d.waves, most_units);
+    if (d.units.size() > (size_t)kMaxUnits) throw Error(CGTP_ERR_UNSUPPORTED, "linear: too many channels");
 }
 
 // Channels that a lane holds of an operand of a gradient's tile: 16-bit operands of eight nodes, or 4 (2 in
@@ -155,18 +233,31 @@ void direction_text(Text &t, const char *name, const Direction &d, bool dot)
 {
     const char *st = "    static ";
     t.s += std::string("struct ") + name + " {\n";
-    t.num("NOUT", (int64_t)d.col.size(), st);
     t.num("DOT", dot ? 1 : 0, st);
+    t.num("NPARTS", (int64_t)d.in_pitch.size(), st);
+    t.num("LDS_BYTES", d.lds_bytes, st);
+    t.list("IN_PITCH", d.in_pitch.size(), [&](size_t i) { return d.in_pitch[i]; }, st);
+    t.list("OUT_PITCH", d.out_pitch.size(), [&](size_t i) { return d.out_pitch[i]; }, st);
+    t.num("NS", (int64_t)d.segments.size(), st);
+    t.list("S_PART", d.segments.size(), [&](size_t i) { return d.segments[i].part; }, st);
+    t.list("S_COL", d.segments.size(), [&](size_t i) { return d.segments[i].col; }, st);
+    t.list("S_LEN", d.segments.size(), [&](size_t i) { return d.segments[i].len; }, st);
+    t.list("S_LDS", d.segments.size(), [&](size_t i) { return d.segments[i].lds; }, st);
+    t.list("S_PAD", d.segments.size(), [&](size_t i) { return d.segments[i].pad; }, st);
+    t.num("NOUT", (int64_t)d.col.size(), st);
+    t.list("O_PART", d.part.size(), [&](size_t i) { return d.part[i]; }, st);
     t.list("O_COL", d.col.size(), [&](size_t i) { return d.col[i]; }, st);
     t.list("O_MUL", d.mul.size(), [&](size_t i) { return d.mul[i]; }, st);
     t.list("O_K", d.k.size(), [&](size_t i) { return d.k[i]; }, st);
+    t.list("O_LDS", d.lds.size(), [&](size_t i) { return d.lds[i]; }, st);
     t.list("O_P0", d.p0.size(), [&](size_t i) { return d.p0[i]; }, st);
     t.list("O_PN", d.pn.size(), [&](size_t i) { return d.pn[i]; }, st);
-    t.list("P_COL", d.p_col.size(), [&](size_t i) { return d.p_col[i]; }, st);
+    t.list("P_LDS", d.p_lds.size(), [&](size_t i) { return d.p_lds[i]; }, st);
     t.list("P_MUL", d.p_mul.size(), [&](size_t i) { return d.p_mul[i]; }, st);
     t.list("P_W", d.p_w.size(), [&](size_t i) { return d.p_w[i]; }, st);
     t.num("NU", (int64_t)d.units.size(), st);
     t.num("WAVES", d.waves, st);
+    t.list("U_PART", d.units.size(), [&](size_t i) { return d.units[i].part; }, st);
     t.list("U_OUT", d.units.size(), [&](size_t i) { return d.units[i].out; }, st);
     t.list("U_N0", d.units.size(), [&](size_t i) { return d.units[i].first; }, st);
     t.list("U_NN", d.units.size(), [&](size_t i) { return d.units[i].count; }, st);
@@ -286,8 +377,8 @@ cgtp_status cgtp_linear_create(const char *in_irreps, const char *out_irreps, co
         h->real = real_bytes(c.dtype);
         const std::vector<Irrep> ins = parse_irreps(in_irreps, "input"), outs = parse_irreps(out_irreps, "output");
         find_paths(*h, ins, outs);
-        plan_direction(*h, h->fwd, outs, false);
-        plan_direction(*h, h->bwd, ins, true);
+        plan_direction(*h, h->fwd, ins, outs, false);
+        plan_direction(*h, h->bwd, outs, ins, true);
         plan_tiles(*h);
         h->mod.build(constants(*h) + kRowKernels + kLinearKernels,
                      {"cgtp_linear_fwd", "cgtp_linear_bwd_x", "cgtp_linear_transpose", "cgtp_linear_bwd_w",

@@ -6,11 +6,16 @@
 //   E, K          experts; experts of a row (0: the one expert of every row, with weight 1)
 //   NUMEL         weights of an expert
 //   Forward, Backward: the product's two directions, each a struct of
-//     NOUT, O_COL, O_MUL, O_K, O_P0, O_PN   output irreps: first column, channels, 2l+1, first path, paths
-//     P_COL, P_MUL, P_W                     paths: the input irrep's first column and channels, the matrix
-//                                           [O_MUL][P_MUL] (row major) in the expert's weights
-//     NU, U_OUT, U_N0, U_NN, U_WAVE, WAVES  units: output irrep, first and number of its blocks of 16 channels,
-//                                           the wave that takes it; waves of a workgroup
+//     NPARTS, IN_PITCH, OUT_PITCH, LDS_BYTES  parts, worked on one after the other: pitches of their rows in LDS
+//     NS, S_PART, S_COL, S_LEN, S_LDS, S_PAD  input irreps: part, first column, columns; where they begin in LDS and
+//                                             columns there (whole steps)
+//     NOUT, O_PART, O_COL, O_MUL, O_K, O_LDS, O_P0, O_PN   output irreps: first column, channels, 2l+1, place in LDS,
+//                                             first path, paths
+//     P_LDS, P_MUL, P_W                       paths: the input irrep's place in LDS and channels, the matrix
+//                                             [O_MUL][P_MUL] (row major) in the expert's weights
+//     NU, U_PART, U_OUT, U_N0, U_NN, U_WAVE, WAVES  units: output irrep, first and number of its blocks of 16
+//                                             channels, the wave that takes it; waves of a workgroup
+//     DOT                                     1: the weights p have a gradient
 //   NPATH, W_*    for the weight gradients, per path: W_XC, W_MI the input's first column and channels, W_GC, W_MO
 //                 the output's, W_K, W_OFF the first weight
 //   NT, T_PATH, T_V, T_U, T_CV, T_CU          tiles of the gradients: path, first output and input channel,
@@ -104,43 +109,125 @@ template <int NN, int KC> DEV void step(const T (&a)[NN][KL], const T (&b)[KL * 
 #endif
 }
 
-// One path's product of an expert: w its matrix, x the node's row
-template <class D, int O, int P, int N0, int NN> DEV void path(const T *w, const T *x, int lane, V4 (&acc)[NN][D::O_K[O]])
+// ---------------------------------------------------------------- tiles of 16 rows
+// A workgroup takes 16 rows, one part of their irreps after the other: a part's input columns come into LDS by
+// loads of neighbouring lanes along the rows, and its results leave it the same way.  Operands read straight
+// from memory are runs of 16 (2l+1) bytes per lane, each instruction touching 64 cache lines for 16 bytes each.
+// In LDS an irrep starts at 16 bytes and is padded with zeros to whole steps; a row's pitch is an odd multiple
+// of 16 bytes, so that the eight lanes of an LDS access (eight nodes) meet different banks.
+constexpr int VEC = 16 / sizeof(T);
+typedef T V16 __attribute__((ext_vector_type(VEC)));
+
+template <class D, int S> DEV void copy_in(T *lds, int pitch, const T *in, long ld, const int *node)
 {
-    constexpr int KC = D::O_K[O], MI = D::P_MUL[P], MO = D::O_MUL[O];
-    const int g = lane >> 4, v = N0 * 16 + row_channel(lane & 15);
-    x += D::P_COL[P] + g * KL * KC;
-    w += D::P_W[P] + g * KL;
-    int left = MI - g * KL;
+    constexpr int LEN = D::S_LEN[S], CHUNKS = D::S_PAD[S] / VEC, TOTAL = 16 * CHUNKS, THREADS = D::WAVES * 64;
+#pragma unroll 8
+    for (int at = threadIdx.x; at < TOTAL; at += THREADS) {
+        const int r = at / CHUNKS, e = at % CHUNKS * VEC, n = node[r];
+        T v[VEC];
+        load_channels<VEC, 1, false>(in + (n < 0 ? 0 : n) * ld + D::S_COL[S] + e, n < 0 ? 0 : LEN - e, v);
+        V16 q;
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) q[i] = v[i];
+        *reinterpret_cast<V16 *>(lds + r * pitch + D::S_LDS[S] + e) = q;
+    }
+}
+
+// rows of the part's output irreps: into LDS (the row of x), or out of it
+template <class D, int O, bool OUT> DEV void copy_rows(T *lds, int pitch, T *rows, long ld, const int *node)
+{
+    constexpr int LEN = D::O_MUL[O] * D::O_K[O], CHUNKS = (LEN + VEC - 1) / VEC, TOTAL = 16 * CHUNKS, THREADS = D::WAVES * 64;
+#pragma unroll 8
+    for (int at = threadIdx.x; at < TOTAL; at += THREADS) {
+        const int r = at / CHUNKS, e = at % CHUNKS * VEC, n = node[r];
+        T *p = rows + (n < 0 ? 0 : n) * ld + D::O_COL[O] + e;
+        V16 *q = reinterpret_cast<V16 *>(lds + r * pitch + D::O_LDS[O] + e);
+        T v[VEC];
+        if (OUT) {
+            const V16 w = *q;
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) v[i] = w[i];
+            if (n < 0) continue;
+            typedef T V __attribute__((ext_vector_type(VEC), aligned(sizeof(T))));
+            if (LEN % VEC == 0 || e + VEC <= LEN) {
+                *reinterpret_cast<V *>(p) = w;
+            } else {
+#pragma unroll
+                for (int i = 0; i < VEC; ++i)
+                    if (e + i < LEN) p[i] = v[i];
+            }
+        } else {
+            load_channels<VEC, 1, false>(p, n < 0 ? 0 : LEN - e, v);
+            V16 w;
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) w[i] = v[i];
+            *q = w;
+        }
+    }
+}
+
+template <class D, int PART, int S = 0> DEV void part_in(T *lds, const T *in, long ld, const int *node)
+{
+    if constexpr (S < D::NS) {
+        if constexpr (D::S_PART[S] == PART) copy_in<D, S>(lds, D::IN_PITCH[PART], in, ld, node);
+        part_in<D, PART, S + 1>(lds, in, ld, node);
+    }
+}
+
+template <class D, int PART, bool OUT, int O = 0> DEV void part_rows(T *lds, T *rows, long ld, const int *node)
+{
+    if constexpr (O < D::NOUT) {
+        if constexpr (D::O_PART[O] == PART) copy_rows<D, O, OUT>(lds, D::OUT_PITCH[PART], rows, ld, node);
+        part_rows<D, PART, OUT, O + 1>(lds, rows, ld, node);
+    }
+}
+
+// `count` elements of LDS, 16 bytes at a time where there are as many
+template <int N> DEV void read_lds(const T *p, T *x)
+{
+    constexpr int n = N >= VEC ? VEC : N;
+    typedef T V __attribute__((ext_vector_type(n)));
+    const V r = *reinterpret_cast<const V *>(p);
+#pragma unroll
+    for (int i = 0; i < n; ++i) x[i] = r[i];
+    if constexpr (N > n) read_lds<N - n>(p + n, x + n);
+}
+
+// One path's product of an expert: w its matrix, x the node's row in LDS
+template <class D, int U, int P> DEV void path(const T *w, const T *x, int lane, V4 (&acc)[D::U_NN[U]][D::O_K[D::U_OUT[U]]])
+{
+    constexpr int O = D::U_OUT[U], N0 = D::U_N0[U], NN = D::U_NN[U], KC = D::O_K[O], MI = D::P_MUL[P], MO = D::O_MUL[O];
+    const int v = N0 * 16 + row_channel(lane & 15), k = (lane >> 4) * KL;
+    x += D::P_LDS[P] + k * KC;
+    w += D::P_W[P] + k;
     // channels past the irrep's end: their products are not stored, so any row of the matrix does for them
     int row[NN];
 #pragma unroll
-    for (int n = 0; n < NN; ++n) row[n] = (v + n * 16 < MO ? v + n * 16 : MO - 1) * MI;
-    for (int k = 0; k < MI / STEP; ++k) {
-        T b[KL * KC], a[NN][KL];
-        load_raw<KL * KC>(x, b);
+    for (int n = 0; n < NN; ++n) row[n] = ((N0 + n + 1) * 16 <= MO || v + n * 16 < MO ? v + n * 16 : MO - 1) * MI;
+#pragma unroll 4
+    for (int s = 0; s < MI / STEP; ++s) {
+        T a[NN][KL], b[KL * KC];
 #pragma unroll
-        for (int n = 0; n < NN; ++n) load_raw<KL>(w + row[n], a[n]);
+        for (int n = 0; n < NN; ++n) load_raw<KL>(w + row[n] + s * STEP, a[n]);
+        read_lds<KL * KC>(x + s * STEP * KC, b);
         step<NN, KC>(a, b, acc);
-        x += STEP * KC;
-        w += STEP;
-        left -= STEP;
     }
     if constexpr (MI % STEP != 0) {
-        T b[KL * KC], a[NN][KL];
-        load_channels<KL, KC, false>(x, left, b);
+        constexpr int s = MI / STEP;
+        T a[NN][KL], b[KL * KC];
 #pragma unroll
-        for (int n = 0; n < NN; ++n) load_channels<KL, 1, false>(w + row[n], left, a[n]);
+        for (int n = 0; n < NN; ++n) load_channels<KL, 1, false>(w + row[n] + s * STEP, MI - s * STEP - k, a[n]);
+        read_lds<KL * KC>(x + s * STEP * KC, b);
         step<NN, KC>(a, b, acc);
     }
 }
 
-template <class D, int O, int P, int END, int N0, int NN>
-DEV void paths(const T *w, const T *x, int lane, V4 (&acc)[NN][D::O_K[O]])
+template <class D, int U, int P, int END> DEV void paths(const T *w, const T *x, int lane,
+                                                         V4 (&acc)[D::U_NN[U]][D::O_K[D::U_OUT[U]]])
 {
     if constexpr (P < END) {
-        path<D, O, P, N0, NN>(w, x, lane, acc);
-        paths<D, O, P + 1, END, N0, NN>(w, x, lane, acc);
+        path<D, U, P>(w, x, lane, acc);
+        paths<D, U, P + 1, END>(w, x, lane, acc);
     }
 }
 
@@ -161,22 +248,21 @@ DEV int wave_min(int v)
 constexpr int KS = K > 0 ? K : 1;
 
 struct Node {
-    const T *in;   // its row of the product's input
-    const T *dot;  // Backward: its row of x, for the gradient of its weights; NULL without
-    T *out;
-    bool live;
-    int e[KS];     // its experts, BIG where there is none
+    const T *in;  // its row of the part's input, in LDS
+    T *out;       // and of its output, which first holds x where the weights' gradient is wanted
+    int e[KS];    // its experts, BIG where there is none
     R p[KS];
 };
 
 // A wave's 16 nodes take the experts that any of them has in rising order.  A node's sum is of its own
 // experts alone, each product scaled in R and added to it (others are not added, so what they hold cannot
 // reach it), and so depends neither on its neighbours nor on the order of the rows.
-template <class D, int U> DEV void unit(const Node &node, const T *w, int lane, R (&dp)[KS])
+template <class D, int U> DEV void unit(const Node &node, const T *w, int lane, bool dot, R (&dp)[KS])
 {
     constexpr int O = D::U_OUT[U], N0 = D::U_N0[U], NN = D::U_NN[U], KC = D::O_K[O], MO = D::O_MUL[O];
     constexpr int P0 = D::O_P0[O], PN = D::O_PN[O];
     const int v0 = N0 * 16 + 4 * (lane >> 4);  // the lane's first channel
+    T *out = node.out + D::O_LDS[O] + v0 * KC;
     V4 total[NN][KC];
 #pragma unroll
     for (int n = 0; n < NN; ++n)
@@ -198,7 +284,7 @@ template <class D, int U> DEV void unit(const Node &node, const T *w, int lane, 
             for (int n = 0; n < NN; ++n)
 #pragma unroll
                 for (int m = 0; m < KC; ++m) acc[n][m] = (V4)(R)0;
-            paths<D, O, P0, P0 + PN, N0, NN>(we, node.in, lane, acc);
+            paths<D, U, P0, P0 + PN>(we, node.in, lane, acc);
             if (K == 0) {
 #pragma unroll
                 for (int n = 0; n < NN; ++n)
@@ -214,23 +300,25 @@ template <class D, int U> DEV void unit(const Node &node, const T *w, int lane, 
                     p += node.p[j];
                     has = true;
                 }
+            if (has) {
 #pragma unroll
-            for (int n = 0; n < NN; ++n)
+                for (int n = 0; n < NN; ++n)
 #pragma unroll
-                for (int m = 0; m < KC; ++m)
+                    for (int m = 0; m < KC; ++m)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) total[n][m][i] = has ? fma(p, acc[n][m][i], total[n][m][i]) : total[n][m][i];
-            if (D::DOT && node.dot) {
+                        for (int i = 0; i < 4; ++i) total[n][m][i] = fma(p, acc[n][m][i], total[n][m][i]);
+            }
+            if (D::DOT && dot) {
                 R s = 0;
 #pragma unroll
                 for (int n = 0; n < NN; ++n) {
                     T x[4 * KC];
-                    load_channels<4, KC, false>(node.dot + D::O_COL[O] + (v0 + n * 16) * KC, MO - v0 - n * 16, x);
+                    read_lds<4 * KC>(out + n * 16 * KC, x);
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
 #pragma unroll
                         for (int m = 0; m < KC; ++m)
-                            if (v0 + n * 16 + i < MO) s = fma(acc[n][m][i], (R)x[i * KC + m], s);
+                            if ((N0 + n + 1) * 16 <= MO || v0 + n * 16 + i < MO) s = fma(acc[n][m][i], (R)x[i * KC + m], s);
                 }
                 s = swap32(swap16(s));
 #pragma unroll
@@ -239,92 +327,111 @@ template <class D, int U> DEV void unit(const Node &node, const T *w, int lane, 
             last = next;
         }
     }
-    if (!node.live || !node.out) return;
 #pragma unroll
     for (int n = 0; n < NN; ++n) {
-        R v[4 * KC];
+        constexpr int n4 = 4 * KC >= VEC ? VEC : 4 * KC;
+        typedef T V __attribute__((ext_vector_type(n4)));
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int q = 0; q < 4 * KC / n4; ++q) {
+            V r;
 #pragma unroll
-            for (int m = 0; m < KC; ++m) v[i * KC + m] = total[n][m][i];
-        const int count = MO - v0 - n * 16;
-        T *out = node.out + D::O_COL[O] + (v0 + n * 16) * KC;
-        if ((N0 + n + 1) * 16 <= MO || count >= 4) {
-            store_run<4 * KC>(out, v);
-        } else {
+            for (int i = 0; i < n4; ++i) r[i] = (T)total[n][(q * n4 + i) % KC][(q * n4 + i) / KC];
+            *reinterpret_cast<V *>(out + n * 16 * KC + q * n4) = r;
+        }
+        if constexpr (4 * KC % n4 != 0) {
 #pragma unroll
-            for (int i = 0; i < 4 * KC; ++i)
-                if (i < count * KC) out[i] = (T)v[i];
+            for (int i = 4 * KC / n4 * n4; i < 4 * KC; ++i) out[n * 16 * KC + i] = (T)total[n][i % KC][i / KC];
         }
     }
 }
 
-template <class D, int U = 0> DEV void units(const Node &node, const T *w, int wave, int lane, R (&dp)[KS])
+template <class D, int PART, int U = 0> DEV void units(const Node &node, const T *w, int wave, int lane, bool dot, R (&dp)[KS])
 {
     if constexpr (U < D::NU) {
-        if (D::U_WAVE[U] == wave) unit<D, U>(node, w, lane, dp);
-        units<D, U + 1>(node, w, wave, lane, dp);
+        if constexpr (D::U_PART[U] == PART) {
+            if (D::U_WAVE[U] == wave) unit<D, U>(node, w, lane, dot, dp);
+        }
+        units<D, PART, U + 1>(node, w, wave, lane, dot, dp);
+    }
+}
+
+template <class D, int PART = 0>
+DEV void parts(Node &node, T *tile, const int *rows, const T *in, long in_ld, const T *w, T *out, long out_ld, const T *x,
+               long x_ld, int wave, int lane, R (&dp)[KS])
+{
+    if constexpr (PART < D::NPARTS) {
+        T *results = tile + 16 * D::IN_PITCH[PART];
+        if (PART > 0) __syncthreads();  // the part before has left LDS
+        part_in<D, PART>(tile, in, in_ld, rows);
+        if (D::DOT && x) part_rows<D, PART, false>(results, const_cast<T *>(x), x_ld, rows);
+        __syncthreads();
+        node.in = tile + (lane & 15) * D::IN_PITCH[PART];
+        node.out = results + (lane & 15) * D::OUT_PITCH[PART];
+        units<D, PART>(node, w, wave, lane, x != nullptr, dp);
+        if (out) {
+            __syncthreads();
+            part_rows<D, PART, true>(results, out, out_ld, rows);
+        }
+        parts<D, PART + 1>(node, tile, rows, in, in_ld, w, out, out_ld, x, x_ld, wave, lane, dp);
     }
 }
 
 template <class D>
 DEV void product(const T *in, long in_ld, const T *w, const int *experts, const R *weights, const int *order, long N,
-                 T *out, long out_ld, const T *dot, long dot_ld, R *grad_weights, R *lds)
+                 T *out, long out_ld, const T *x, long x_ld, R *grad_weights)
 {
+    __shared__ V16 tile[D::LDS_BYTES / 16];
+    __shared__ int rows[16];
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
     const long at = (long)blockIdx.x * 16 + (lane & 15);
-    long n = at < N ? at : N - 1;
-    if (order) n = order[n];
+    long n = at < N ? at : -1;
+    if (order && n >= 0) n = order[n];
+    if (n >= N || n < 0) n = -1;
+    if (threadIdx.x < 16) rows[threadIdx.x] = (int)n;
     Node node;
-    node.live = at < N && n >= 0 && n < N;
-    n = n < 0 ? 0 : n < N ? n : N - 1;
-    node.in = in + n * in_ld;
-    node.out = out ? out + n * out_ld : nullptr;
-    node.dot = dot ? dot + n * dot_ld : nullptr;
     R dp[KS];
 #pragma unroll
     for (int j = 0; j < KS; ++j) {
-        const int e = K > 0 ? experts[n * K + j] : BIG;
-        const bool has = node.live && e >= 0 && e < E;
+        const int e = K > 0 && n >= 0 ? experts[n * K + j] : -1;
+        const bool has = e >= 0 && e < E;
         node.e[j] = has ? e : BIG;
         node.p[j] = has ? weights[n * K + j] : (R)0;
         dp[j] = 0;
     }
-    units<D>(node, w, wave, lane, dp);
+    __syncthreads();
+    parts<D>(node, reinterpret_cast<T *>(tile), rows, in, in_ld, w, out, out_ld, x, x_ld, wave, lane, dp);
     if (K > 0 && D::DOT && grad_weights) {
         // the waves' shares of a node's sum, in the waves' order
+        __shared__ R lds[D::DOT ? D::WAVES * 16 * KS : 1];
 #pragma unroll
         for (int j = 0; j < K; ++j)
             if (lane < 16) lds[(wave * 16 + lane) * KS + j] = dp[j];
         __syncthreads();
         for (int t = threadIdx.x; t < 16 * K; t += D::WAVES * 64) {
-            const int i = t / KS, j = t % KS;
+            const int i = t / KS, j = t % KS, row = rows[i];
             R s = 0;
 #pragma unroll
             for (int v = 0; v < D::WAVES; ++v) s += lds[(v * 16 + i) * KS + j];
-            const long a = (long)blockIdx.x * 16 + i;
-            const long row = a < N ? (order ? order[a] : a) : -1;
-            if (row >= 0 && row < N) grad_weights[row * K + j] = s;
+            if (row >= 0) grad_weights[(long)row * K + j] = s;
         }
     }
 }
 
-extern "C" __global__ void __launch_bounds__(Forward::WAVES * 64)
+extern "C" __global__ void __launch_bounds__(Forward::WAVES * 64, 2)
 cgtp_linear_fwd(const T *__restrict__ x, long x_ld, const T *__restrict__ w, const int *__restrict__ experts,
                 const R *__restrict__ weights, const int *__restrict__ order, long N, T *__restrict__ out, long out_ld)
 {
-    product<Forward>(x, x_ld, w, experts, weights, order, N, out, out_ld, nullptr, 0, nullptr, nullptr);
+    product<Forward>(x, x_ld, w, experts, weights, order, N, out, out_ld, nullptr, 0, nullptr);
 }
 
 // grad_x and the gradient of the weights p: dp[n][j] = <x[n], W^T g[n]>.  w holds the transposed matrices.
-extern "C" __global__ void __launch_bounds__(Backward::WAVES * 64)
+extern "C" __global__ void __launch_bounds__(Backward::WAVES * 64, 2)
 cgtp_linear_bwd_x(const T *__restrict__ g, long g_ld, const T *__restrict__ w, const int *__restrict__ experts,
                   const R *__restrict__ weights, const int *__restrict__ order, long N, T *__restrict__ grad_x,
                   long grad_x_ld, const T *__restrict__ x, long x_ld, R *__restrict__ grad_weights)
 {
-    __shared__ R lds[Backward::WAVES * 16 * KS];
     product<Backward>(g, g_ld, w, experts, weights, order, N, grad_x, grad_x_ld, grad_weights ? x : nullptr, x_ld,
-                      grad_weights, lds);
+                      grad_weights);
 }
 
 // every matrix [mul_out][mul_in] transposed, in its place
