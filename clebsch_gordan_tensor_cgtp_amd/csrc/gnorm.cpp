@@ -14,9 +14,9 @@ struct cgtp_group_norm {
     int elem = 4, real = 4;              // bytes of an element; of a statistic or weight
     int cv = 1, p = 1, rw = 1, ns = 1;   // channels a lane takes together, lanes of a row, rows at once, slots
     cgtp::ConfigModule mod;
-    enum { stats, join, apply, bwd_sums, bwd_join, bwd_apply, columns };
-    int width() const { return cfg.channels / cfg.groups; }
-    int batch() const { return ns * cv <= 8 ? 4 : 2; }
+    int held_fwd = 1, held_bwd = 1, waves = 1;  // rows that a lane holds; most waves of a workgroup
+    enum { fwd, fwd_large, bwd, bwd_large };
+    int groups_pow2 = 1;
 };
 
 namespace cgtp {
@@ -30,55 +30,94 @@ int pow2_at_least(int n)
     return p;
 }
 
-// A lane takes up to 16 bytes of a row at a time; short rows lie side by side in a wave.
+// A lane takes up to 16 bytes of a row at a time; short rows lie side by side in a wave.  In the forward it holds 128
+// bytes of its graph's rows as they are in memory; in the backward rows of x and dy in the statistics' type, in what
+// registers the waves of a workgroup leave beside seven values per channel.  Wide rows, of which a lane holds more
+// channels, get fewer waves.
 void lay_out(cgtp_group_norm &g)
 {
     const int c = g.cfg.channels;
     g.elem = elem_bytes(g.cfg.dtype);
     g.real = real_bytes(g.cfg.dtype);
-    g.cv = std::min(16 / g.elem, pow2_at_least(c));
+    g.cv = 16 / g.elem;
+    while (g.cv > c) g.cv /= 2;
     const int units = (c + g.cv - 1) / g.cv;
     g.p = std::min(units, 64);
     g.ns = (units + 63) / 64;
     g.rw = 64 / g.p;
+    g.groups_pow2 = pow2_at_least(g.cfg.groups);
+    const int channels = g.ns * g.cv, regs = channels * g.real / 4;
+    g.held_fwd = std::max(1, 128 / (channels * g.elem));
+    g.waves = regs <= 8 ? 16 : regs <= 16 ? 8 : 4;
+    g.held_bwd = regs <= 4 ? 8 : 2;
 }
 
 std::string constants(const cgtp_group_norm &g)
 {
     std::string s = "// group norm of " + std::to_string(g.cfg.channels) + " channels\n";
     auto num = [&](const char *n, long v) { s += std::string("constexpr int ") + n + " = " + std::to_string(v) + ";\n"; };
+    s += "#define FAST_EXP (sizeof(T) <= 4)\n";
     s += std::string("typedef ") + type_name(g.cfg.dtype) + " T;\n";
     s += std::string("typedef ") + (g.cfg.dtype == CGTP_F64 ? "double" : "float") + " R;\n";
     num("ACT", g.cfg.act);
     num("C", g.cfg.channels);
     num("GROUPS", g.cfg.groups);
-    num("W", g.width());
+    num("W", g.cfg.channels / g.cfg.groups);
     num("CV", g.cv);
     num("P", g.p);
     num("RW", g.rw);
     num("NS", g.ns);
-    num("GL", std::min(64, pow2_at_least(g.cfg.groups)));
-    num("CHUNK_LDS", (long)g.rw * g.cfg.channels);
+    num("GP", g.groups_pow2);
+    num("BF", g.held_fwd);
+    num("BB", g.held_bwd);
+    num("NWMAX", g.waves);
     return s;
 }
 
-// Rows of a wave: whole batches, and no more waves than `most`.
-int64_t chunk_rows(const cgtp_group_norm &g, int64_t N, int64_t most)
-{
-    const int64_t step = (int64_t)g.rw * g.batch();
-    return std::max<int64_t>(1, (N + most * step - 1) / (most * step)) * step;
-}
-
-constexpr int64_t kForwardWaves = 4096, kBackwardWaves = 2048;
-
+// How a pass over N rows in S graphs is launched (gnorm_kernels.h has the two ways over the rows).
 struct Split {
-    int64_t rows, chunks;
+    int waves;       // of a workgroup
+    int64_t cap;     // rows of a graph that one workgroup takes
+    int64_t rows;    // of a chunk
+    int64_t chunks, graphs;  // workgroups of the first launch
+    bool large;      // whether a graph can have more than cap rows
 };
 
-Split split(const cgtp_group_norm &g, int64_t N, bool backward)
+// Where a workgroup of the most waves holds all N rows, as few waves as do: no graph is large, and the second
+// launch is left out.  Else 2.5 mean graphs: of graphs of uneven sizes most are one workgroup's then, and
+// waves that a smaller one leaves idle are few; where that is far more than a workgroup's, nearly all are large, and four
+// waves share them out more evenly.  (4,000 graphs of 50 rows on average, 64 channels in bf16.)
+// Chunks: at most 1,024, whose pieces each workgroup of the second launch joins for itself; a backward's
+// workgroups take graphs in turn, since each leaves its partial sums of the weights' gradients.
+Split split(const cgtp_group_norm &g, int64_t N, int64_t S, bool backward)
 {
-    const int64_t rows = chunk_rows(g, N, backward ? kBackwardWaves : kForwardWaves);
-    return {rows, (N + rows - 1) / rows};
+    Split p{};
+    const int64_t held = (int64_t)g.rw * (backward ? g.held_bwd : g.held_fwd);
+    const int64_t want = N <= held * g.waves ? N : (int64_t)(2.5 * (double)N / (double)std::max<int64_t>(1, S));
+    p.waves = want > 4 * held * g.waves ? std::min(4, g.waves) : 1;
+    if (want <= 4 * held * g.waves)
+        while (p.waves < g.waves && held * p.waves < want) p.waves *= 2;
+    p.cap = held * p.waves;
+    p.large = N > p.cap;
+    const int64_t step = (int64_t)g.rw * p.waves * (g.ns * g.cv <= 4 ? 4 : 2);
+    p.rows = std::max<int64_t>(1, (N + 1024 * step - 1) / (1024 * step)) * step;
+    p.chunks = (N + p.rows - 1) / p.rows;
+    p.graphs = backward ? std::min<int64_t>(S, 1024) : S;
+    return p;
+}
+
+// bytes of LDS: a lane's sums of `quantities`, the groups' and their parts (or a column per channel)
+int lds_bytes(const cgtp_group_norm &g, int waves, int quantities, bool columns)
+{
+    const int w = g.cfg.channels / g.cfg.groups, es = w % g.cv == 0 ? g.cv : 1, ce = (g.cfg.channels + es - 1) / es;
+    const int per_group = std::max(1, 64 * waves / g.groups_pow2 / 64);
+    const int sums = quantities * (waves * g.rw * ce + g.cfg.groups * (1 + per_group));
+    return std::max(sums, columns ? waves * g.rw * g.cfg.channels : 0) * g.real;
+}
+
+int lds_bytes_large(const cgtp_group_norm &g, int threads)
+{
+    return std::max((3 * threads + 2 * g.cfg.groups) * g.real, threads * 8);
 }
 
 size_t aligned(size_t n) { return (n + 255) / 256 * 256; }
@@ -90,17 +129,21 @@ struct Workspace {
 
 Workspace workspace_of(const cgtp_group_norm &g, int64_t N, int64_t S, bool backward)
 {
-    const Split sp = split(g, N, backward);
+    const Split sp = split(g, N, S, backward);
     Workspace w{};
     if (S == 0) return w;
-    w.part = (size_t)(sp.chunks + S) * g.cfg.groups * 2 * g.real;
-    // the forward's statistics, where the caller wants none; the backward's means
-    w.stat = (size_t)S * g.cfg.groups * 2 * g.real;
-    if (backward) w.wpart = (size_t)sp.chunks * 2 * g.cfg.channels * g.real;
+    if (sp.large) w.part = (size_t)(sp.chunks + S) * g.cfg.groups * 2 * g.real;
+    if (!backward) w.stat = (size_t)S * g.cfg.groups * 2 * g.real;  // where the caller wants no statistics
+    if (backward) w.wpart = (size_t)(sp.chunks + sp.graphs) * 2 * g.cfg.channels * g.real;
     return w;
 }
 
-int join_threads(int64_t S) { return S > 8192 ? 64 : 256; }
+void run_lds(hipFunction_t f, int64_t groups, int threads, int lds, void **args, void *stream)
+{
+    check_hip(hipModuleLaunchKernel(f, (unsigned)groups, 1, 1, (unsigned)threads, 1, 1, (unsigned)lds,
+                                    static_cast<hipStream_t>(stream), args, nullptr),
+              "hipModuleLaunchKernel");
+}
 
 void check_graphs(int64_t S, const int32_t *ptr)
 {
@@ -134,8 +177,7 @@ cgtp_status cgtp_group_norm_create(const cgtp_group_norm_config *config, cgtp_gr
         h->cfg = c;
         lay_out(*h);
         h->mod.build(constants(*h) + kRowKernels + kGroupNormKernels,
-                     {"cgtp_gnorm_stats", "cgtp_gnorm_join", "cgtp_gnorm_apply", "cgtp_gnorm_bwd_sums",
-                      "cgtp_gnorm_bwd_join", "cgtp_gnorm_bwd_apply", "cgtp_gnorm_columns"});
+                     {"cgtp_gnorm_fwd", "cgtp_gnorm_fwd_large", "cgtp_gnorm_bwd", "cgtp_gnorm_bwd_large"});
         *norm_out = h.release();
     });
 }
@@ -196,26 +238,24 @@ cgtp_status cgtp_group_norm_forward(const cgtp_group_norm *norm, int64_t N, int6
         all.flat(workspace, ws.bytes(), "workspace", true);
         all.check();
         const auto &F = g.mod.here();
-        const Split sp = split(g, N, false);
-        void *part = workspace;
+        const Split sp = split(g, N, S, false);
+        require(S + sp.chunks < INT_MAX, "too many graphs");
+        void *piece = workspace;
         if (!mean) {
             mean = static_cast<char *>(workspace) + aligned(ws.part);
             rstd = static_cast<char *>(mean) + ns;
         }
-        long xl = (long)x_ld, yl = (long)y_ld, n = (long)N, rows = (long)sp.rows;
+        long xl = (long)x_ld, yl = (long)y_ld, n = (long)N, rows = (long)sp.rows, cap = (long)sp.cap;
         int s = (int)S;
         float ef = (float)g.cfg.eps;
         double ed = g.cfg.eps;
         void *eps = g.real == 8 ? (void *)&ed : (void *)&ef;
-        if (sp.chunks) {
-            void *args[] = {&x, &xl, &ptr, &s, &n, &rows, &part};
-            run(F[cgtp_group_norm::stats], sp.chunks, 64, args, stream);
-        }
-        void *jargs[] = {&ptr, &n, &rows, &part, &mean, &rstd, eps};
-        run(F[cgtp_group_norm::join], S, join_threads(S), jargs, stream);
-        if (sp.chunks) {
-            void *args[] = {&x, &xl, &ptr, &s, &n, &rows, &w, &bias, &mean, &rstd, &y, &yl, &fill};
-            run(F[cgtp_group_norm::apply], sp.chunks, 64, args, stream);
+        void *args[] = {&x, &xl, &ptr, &s, &n, &rows, &cap, &w, &bias, &y, &yl, &fill, &mean, &rstd, &piece, eps};
+        run_lds(F[cgtp_group_norm::fwd], sp.chunks + sp.graphs, 64 * sp.waves, lds_bytes(g, sp.waves, 1, false), args, stream);
+        if (sp.large) {
+            const int threads = 64 * std::min(std::max(sp.waves, 4), g.waves);
+            void *largs[] = {&x, &xl, &ptr, &s, &n, &rows, &cap, &w, &bias, &piece, &y, &yl, &mean, &rstd, eps};
+            run_lds(F[cgtp_group_norm::fwd_large], sp.chunks, threads, lds_bytes_large(g, threads), largs, stream);
         }
     });
 }
@@ -263,27 +303,23 @@ cgtp_status cgtp_group_norm_backward(const cgtp_group_norm *norm, int64_t N, int
         all.flat(grad_bias, nw, "grad_bias", true);
         all.check();
         const auto &F = g.mod.here();
-        const Split sp = split(g, N, true);
+        const Split sp = split(g, N, S, true);
         char *at = static_cast<char *>(workspace);
-        void *part = at, *stat = at + aligned(ws.part), *wpart = at + aligned(ws.part) + aligned(ws.stat);
-        if (!weights) wpart = nullptr;
-        long xl = (long)x_ld, dyl = (long)grad_y_ld, dxl = (long)grad_x_ld, n = (long)N, rows = (long)sp.rows;
-        long chunks = work ? (long)sp.chunks : 0;
-        int s = (int)S;
+        void *piece = at, *wpart = weights ? at + aligned(ws.part) + aligned(ws.stat) : nullptr;
+        long xl = (long)x_ld, dyl = (long)grad_y_ld, dxl = (long)grad_x_ld, n = (long)N, rows = (long)sp.rows, cap = (long)sp.cap;
+        long count = work ? (long)(sp.chunks + sp.graphs) : 0;
+        int s = (int)S, graphs = (int)sp.graphs, columns = weights ? (2 * c + 15) / 16 : 0;
         if (work) {
-            void *args[] = {&x, &xl, &grad_y, &dyl, &ptr, &s, &n, &rows, &w, &bias, &mean, &rstd, &part, &wpart};
-            run(F[cgtp_group_norm::bwd_sums], sp.chunks, 64, args, stream);
-            if (grad_x) {
-                void *jargs[] = {&ptr, &n, &rows, &part, &stat};
-                run(F[cgtp_group_norm::bwd_join], S, join_threads(S), jargs, stream);
-                void *aargs[] = {&x, &xl, &grad_y, &dyl, &ptr, &s, &n, &rows, &w, &bias, &mean, &rstd, &stat, &grad_x, &dxl,
-                                 &fill};
-                run(F[cgtp_group_norm::bwd_apply], sp.chunks, 64, aargs, stream);
-            }
+            void *args[] = {&x, &xl, &grad_y, &dyl, &ptr, &s, &n, &rows, &graphs, &cap, &w, &bias, &mean, &rstd, &grad_x, &dxl,
+                            &fill, &piece, &wpart};
+            run_lds(F[cgtp_group_norm::bwd], sp.chunks + sp.graphs, 64 * sp.waves, lds_bytes(g, sp.waves, 2, true), args, stream);
         }
-        if (weights) {
-            void *args[] = {&wpart, &chunks, &grad_w, &grad_bias};
-            run(F[cgtp_group_norm::columns], (2 * c + 15) / 16, 1024, args, stream);
+        const int64_t finish = work && grad_x && sp.large ? sp.chunks : 0;
+        if (columns + finish > 0) {
+            const int threads = 64 * std::min(std::max(sp.waves, 8), g.waves);
+            void *args[] = {&x, &xl, &grad_y, &dyl, &ptr, &s, &n, &rows, &cap, &w, &bias, &mean, &rstd, &piece, &grad_x, &dxl,
+                            &columns, &wpart, &count, &grad_w, &grad_bias};
+            run_lds(F[cgtp_group_norm::bwd_large], columns + finish, threads, lds_bytes_large(g, threads), args, stream);
         }
     });
 }

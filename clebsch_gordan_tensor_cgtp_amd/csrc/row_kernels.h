@@ -12,18 +12,18 @@ static const char kRowKernels[] = R"HIP(
 // ---------------------------------------------------------------- runs of elements
 // Rows start at any element, so the vector types claim no more than the element's alignment.
 
-template <int N, typename S> DEV void load_run(const S *p, R *x)
+template <int N, typename S, typename X> DEV void load_run(const S *p, X *x)
 {
     if constexpr (N > 0) {
         constexpr int W = 16 / sizeof(S);
         constexpr int n = N >= W ? W : N >= 8 ? 8 : N >= 4 ? 4 : N >= 2 ? 2 : 1;
         typedef S V __attribute__((ext_vector_type(n), aligned(sizeof(S))));
         if constexpr (n == 1) {
-            x[0] = (R)p[0];
+            x[0] = (X)p[0];
         } else {
             const V r = *reinterpret_cast<const V *>(p);
 #pragma unroll
-            for (int i = 0; i < n; ++i) x[i] = (R)r[i];
+            for (int i = 0; i < n; ++i) x[i] = (X)r[i];
         }
         load_run<N - n>(p + n, x + n);
     }
@@ -98,26 +98,22 @@ DEV double swap32(double v)
 }
 
 // ---------------------------------------------------------------- activations
+// A text before this one may ask for the hardware's exponential and reciprocal in float too (FAST_EXP).
+#ifndef FAST_EXP
+#define FAST_EXP (sizeof(T) == 2)
+#endif
 // Rows of 16 bits take the hardware's exponential and reciprocal: their errors, |g| 2^-23 and 2^-23 of the
 // result, are far below a rounding to 16 bits; the weight gradients, which are float, have them in every row's
 // term, as large as a few of float's own roundings (the join's backward, 8,192 scalar rows
 // of 4,096 in bf16 with a SiLU gate: 131 us with expf and a division, 116 us).
-DEV float exp_of(float v) { return sizeof(T) == 2 ? __builtin_amdgcn_exp2f(v * 1.44269504f) : expf(v); }
-DEV float inverse(float v) { return sizeof(T) == 2 ? __builtin_amdgcn_rcpf(v) : 1.0f / v; }
+DEV float exp_of(float v) { return FAST_EXP ? __builtin_amdgcn_exp2f(v * 1.44269504f) : expf(v); }
+DEV float inverse(float v) { return FAST_EXP ? __builtin_amdgcn_rcpf(v) : 1.0f / v; }
 DEV double inverse(double v) { return 1.0 / v; }
 DEV double exp_of(double v) { return exp(v); }
 DEV float tanh_of(float v) { return tanhf(v); }
 DEV double tanh_of(double v) { return tanh(v); }
 DEV float root_inverse(float v) { return 1.0f / __builtin_sqrtf(v); }
 DEV double root_inverse(double v) { return 1.0 / __builtin_sqrt(v); }
-
-DEV R act_value(R g)
-{
-    if (ACT == 0) return g;
-    if (ACT == 3) return tanh_of(g);
-    const R s = inverse((R)1 + exp_of(-g));
-    return ACT == 1 ? s : g * s;
-}
 
 // tanh(g) from e = exp(-2 |g|) and r = 1 / (1 + e); below 1/4, where 1 - e would cancel, its series to g^9 (what
 // follows is under 2^-26 of it there).  Doubles take the function itself.
@@ -128,6 +124,18 @@ DEV float tanh_from(float g, float e, float r)
     return g2 < 0.0625f ? small : g < 0 ? -t : t;
 }
 DEV double tanh_from(double g, double, double) { return tanh(g); }
+
+DEV R act_value(R g)
+{
+    if (ACT == 0) return g;
+    if (ACT == 3) {
+        if (!FAST_EXP || sizeof(T) == 2) return tanh_of(g);
+        const R e = exp_of(g < 0 ? 2 * g : -2 * g);
+        return tanh_from(g, e, inverse((R)1 + e));
+    }
+    const R s = inverse((R)1 + exp_of(-g));
+    return ACT == 1 ? s : g * s;
+}
 
 // act'(g) and act(g).  The sigmoid and its complement are q = e / (1 + e) and 1 - q, e = exp(-|g|), and the slope
 // their product; with 1 - s from s it would carry a rounding of 1 (17% of it at 15, all of it at 17).  tanh's

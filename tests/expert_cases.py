@@ -43,10 +43,11 @@ def within(name, got, value, most, dtype=None):
 # ------------------------------------------------------------------------------------ group norm
 
 # channels, groups, graphs' sizes: one channel; one row; empty graphs; groups inside a lane's channels and over
-# many lanes; odd rows; several slots of a lane; as many groups as channels; graphs over many waves
+# many lanes; odd rows; several slots of a lane; as many groups as channels; graphs of one workgroup beside graphs over
+# many, and these over as many chunks as there are
 NORM_SHAPES = [(1, 1, [3]), (4, 2, [1]), (4, 4, [0, 5, 0, 0, 9, 0]), (32, 4, [21] * 24), (95, 5, [700, 1, 3, 0, 411]),
                (64, 64, [130, 2]), (2048, 4, [9, 30]), (513, 3, [40]), (24, 1, [1, 1, 1, 2]), (130, 13, [900]),
-               (16, 16, [5000, 1, 7000])]
+               (16, 16, [5000, 1, 7000]), (40, 8, [1] * 300 + [9000, 4, 2600, 0] + [7] * 300), (1024, 512, [3000, 20])]
 
 
 def norm_inputs(channels, graphs, dtype, seed, outside=(2, 3)):
@@ -61,17 +62,17 @@ def norm_inputs(channels, graphs, dtype, seed, outside=(2, 3)):
 
 
 def norm_roundings(norm, rows):
-    """Additions that one result of a sum over rows x channels passes through.  In a lane: its batches of rows, each
-    joined in 4 roundings after 5 of its own.  Over the wave: a group's RW * W lane sums by LG lanes, then a tree of 6.
-    Over the waves: a chunk is at least one batch of RW rows, and nj >= 64 / GL lanes join in 4 roundings each, then
-    a tree of 8 joins.  A dozen products and quotients."""
-    const = {m[0]: int(m[1]) for m in re.findall(r"constexpr int (\w+) = (\d+);", norm.source)}
-    batch = const["RW"] * (4 if const["NS"] * const["CV"] <= 8 else 2)
-    chunk = max(1, -(-rows // (2048 * batch))) * batch
-    lane = 9 * (chunk // batch)
-    lanes = const["RW"] * const["W"] * const["GL"] // 64 + 1
-    joins = 4 * (rows // chunk * const["GL"] // 64 + 1)
-    return lane + lanes + 6 + joins + 32 + 12
+    """Additions that one result of a sum over rows x channels passes through.  In a lane: the 64 rows at most that it holds,
+    and its channels of a group; or along a chunk, a 1,024th of the rows at least, its batches of rows, each joined in 4
+    roundings after 5 of its own.  Over a workgroup: a group's sums of RG rows by threads / GP threads (one, of fewer threads
+    than groups), a tree of 6 and up to 16 waves.  Over a graph's pieces: 256 threads or more join them, GP side by side, in 4
+    roundings each, then a tree of 10 joins.  A dozen products and quotients."""
+    c = {m[0]: int(m[1]) for m in re.findall(r"constexpr int (\w+) = (\d+);", norm.source)}
+    step = c["RW"] * (4 if c["NS"] * c["CV"] <= 4 else 2)
+    batches = -(-rows // (1024 * step))
+    pieces = rows // (batches * step) + 1
+    lanes = c["RW"] * c["W"] * c["GP"] // 64 + min(16, c["GP"] // 64) * c["RW"] * c["W"] + 1
+    return 64 + c["CV"] + 9 * batches + lanes + 6 + 16 + 4 * (min(pieces, 1024) * c["GP"] // 256 + 1) + 40 + 12
 
 
 def stat_bounds(x, ptr, mean, rstd, u, c):
