@@ -6,7 +6,7 @@ tensor is not given, it is allocated here with ``torch.empty`` -- the only
 allocation on the path, and one the library itself never makes.  If
 ``libcgtp.so`` is missing the first call raises: there is no fallback.
 
-The block and optimizer calls (norm, join, AdamW) go through a small compiled module
+The block, group norm, routing, experts' and optimizer calls go through a small compiled module
 (``csrc/torch/calls.cpp``) when their outputs are all new: the same checks, outputs and entry points
 at half the cost of a call.  What it does not take comes back here.
 """
@@ -1019,6 +1019,7 @@ class _Compiled:
         self._h = h
         self.torch_dtype = _torch_dtype(self.dtype)                              # of rows
         self.real_dtype = _torch_dtype("f64" if self.dtype == "f64" else "f32")  # of statistics and weights
+        self._calls = _calls()
 
     @property
     def handle(self):
@@ -1029,6 +1030,7 @@ class _Compiled:
         return getattr(lib(), self._name + "_source")(self._h).decode()
 
     def close(self):
+        self._meta = None
         if self._h is not None and _lib is not None:
             getattr(lib(), self._name + "_destroy")(self._h)
         self._h = None
@@ -1048,6 +1050,7 @@ class GroupNorm(_Compiled):
     def __init__(self, channels, groups, dtype="f32", act="identity", eps=1e-6):
         self.channels, self.groups, self.dtype, self.act, self.eps = int(channels), int(groups), dtype, act, float(eps)
         self._create(ctypes.byref(GroupNormConfig(DTYPES[dtype], self.channels, self.groups, ACTS[act], self.eps)))
+        self._meta = self._calls.group_norm(self._h.value, self.channels, self.groups, DTYPES[dtype])
 
 
 @lru_cache(maxsize=None)
@@ -1075,6 +1078,10 @@ def group_norm_forward(norm: GroupNorm, x, ptr, w, bias, y=None, mean=None, rstd
     """(y, mean, rstd): y = act((x - mean) * rstd * w + bias), mean and rstd [graphs][groups] over the rows
     ptr[b]..ptr[b+1] of a graph and the channels of a group.  x and y may have a row pitch; w and bias
     None stand for ones and zeros.  Rows of no graph are left as they were in a given y, and zeros in a new one."""
+    if y is None and mean is None and rstd is None and workspace is None and stream is None:
+        got = norm._calls.group_norm_forward(norm._meta, x, ptr, w, bias, need_stats)
+        if got is not None:
+            return _answer(got)
     if stream is not None:
         return _in_stream(stream, group_norm_forward, norm, x, ptr, w, bias, y, mean, rstd, need_stats, workspace)
     dev = _device_index(x, "x")
@@ -1099,6 +1106,10 @@ def group_norm_backward(norm: GroupNorm, x, ptr, w, bias, mean, rstd, grad_y, gr
     """(grad_x, grad_w, grad_bias) from the forward's mean and rstd; entries not in ``need`` are None and not
     computed.  x, grad_y and grad_x may have a row pitch.  Rows of no graph are left as they were in a given
     grad_x, and zeros in a new one."""
+    if grad_x is None and grad_w is None and grad_bias is None and workspace is None and stream is None:
+        got = norm._calls.group_norm_backward(norm._meta, x, ptr, w, bias, mean, rstd, grad_y, *need)
+        if got is not None:
+            return _answer(got)
     if stream is not None:
         return _in_stream(stream, group_norm_backward, norm, x, ptr, w, bias, mean, rstd, grad_y, grad_x, grad_w,
                           grad_bias, need, workspace)
@@ -1134,6 +1145,7 @@ class Router(_Compiled):
         self.renormalise, self.scale = bool(renormalise), float(scale)
         self._create(ctypes.byref(RouterConfig(DTYPES[dtype], SCORES[score], self.experts, self.top_k, self.groups,
                                                self.top_groups, int(self.renormalise), self.scale)))
+        self._meta = self._calls.router(self._h.value, self.experts, self.top_k, DTYPES[dtype])
 
 
 @lru_cache(maxsize=None)
@@ -1154,6 +1166,10 @@ class RouteOrder(NamedTuple):
 def route_forward(router: Router, logits, bias=None, experts=None, weights=None, stream=None):
     """(experts, weights), both [N][top_k]: the chosen experts (int32, -1 where too few are not masked) and their
     weights.  ``bias`` takes part in the choice alone.  logits may have a row pitch."""
+    if experts is None and weights is None and stream is None:
+        got = router._calls.route_forward(router._meta, logits, bias)
+        if got is not None:
+            return _answer(got)
     if stream is not None:
         return _in_stream(stream, route_forward, router, logits, bias, experts, weights)
     import torch
@@ -1170,6 +1186,10 @@ def route_forward(router: Router, logits, bias=None, experts=None, weights=None,
 
 def route_backward(router: Router, logits, experts, grad_weights, grad_logits=None, stream=None):
     """grad_logits [N][E] from the gradient of the weights, the choice held fixed."""
+    if grad_logits is None and stream is None:
+        got = router._calls.route_backward(router._meta, logits, experts, grad_weights)
+        if got is not None:
+            return _answer(got)[0]
     if stream is not None:
         return _in_stream(stream, route_backward, router, logits, experts, grad_weights, grad_logits)
     import torch
@@ -1190,8 +1210,15 @@ def route_order_workspace_size(router: Router, n: int) -> int:
     return v.value
 
 
-def route_order(router: Router, experts, outs=(None, None, None), workspace=None, stream=None) -> RouteOrder:
+_NO_LISTS = (None,) * 3
+
+
+def route_order(router: Router, experts, outs=_NO_LISTS, workspace=None, stream=None) -> RouteOrder:
     """The lists that the experts' products go by (rows, slots, offsets), from experts [N][top_k]."""
+    if outs is _NO_LISTS and workspace is None and stream is None:
+        got = router._calls.route_order(router._meta, experts)
+        if got is not None:
+            return RouteOrder(*_answer(got))
     if stream is not None:
         return _in_stream(stream, route_order, router, experts, outs, workspace)
     import torch
@@ -1221,6 +1248,8 @@ class Linear(_Compiled):
         info = LinearInfo()
         _check(lib().cgtp_linear_info_get(self._h, ctypes.byref(info)))
         self.d_in, self.d_out, self.num_paths, self.weight_numel = info.d_in, info.d_out, info.num_paths, info.weight_numel
+        self._meta = self._calls.linear(self._h.value, self.d_in, self.d_out, self.experts, self.top_k, self.weight_numel,
+                                        DTYPES[dtype])
 
 
 @lru_cache(maxsize=None)
@@ -1254,6 +1283,10 @@ def _choice(linear, n, experts, weights, order, dev):
 def linear_forward(linear: Linear, x, w, experts=None, weights=None, order=None, out=None, stream=None):
     """out[n] = sum_j weights[n][j] * W[experts[n][j]] x[n] (W x without a choice).  ``order`` is
     route_order's for these experts; without it rows are taken as they lie.  x and out may have a row pitch."""
+    if out is None and stream is None:
+        got = linear._calls.linear_forward(linear._meta, x, w, experts, weights, order)
+        if got is not None:
+            return _answer(got)[0]
     if stream is not None:
         return _in_stream(stream, linear_forward, linear, x, w, experts, weights, order, out)
     dev = _device_index(x, "x")
@@ -1267,11 +1300,15 @@ def linear_forward(linear: Linear, x, w, experts=None, weights=None, order=None,
     return out
 
 
-def linear_backward(linear: Linear, x, w, grad_out, experts=None, weights=None, order=None, outs=(None,) * 3,
+def linear_backward(linear: Linear, x, w, grad_out, experts=None, weights=None, order=None, outs=_NO_LISTS,
                     need=(True,) * 3, workspace=None, stream=None):
     """(grad_x, grad_w, grad_weights); entries not in ``need`` (and grad_weights without a choice) are None
     and not computed.  ``order`` as in linear_forward; grad_w needs it.  x, grad_out and grad_x may have a
     row pitch."""
+    if outs is _NO_LISTS and workspace is None and stream is None:
+        got = linear._calls.linear_backward(linear._meta, x, w, grad_out, experts, weights, order, *need)
+        if got is not None:
+            return _answer(got)
     if stream is not None:
         return _in_stream(stream, linear_backward, linear, x, w, grad_out, experts, weights, order, outs, need, workspace)
     dev = _device_index(x, "x")

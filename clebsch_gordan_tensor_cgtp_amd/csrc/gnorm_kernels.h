@@ -104,6 +104,19 @@ template <int J = 0, typename S> DEV void store_row(S *row, int lane, const R *x
     }
 }
 
+// a row's channels of a lane as they are in memory
+struct Raw {
+    typedef T V __attribute__((ext_vector_type(CV)));
+    V v[NS];
+    __device__ __forceinline__ R at(int i) const { return (R)v[i / CV][i % CV]; }
+};
+DEV void load_raw(const T *row, int lane, Raw &x)
+{
+    typedef T V __attribute__((ext_vector_type(CV), aligned(sizeof(T))));
+#pragma unroll
+    for (int j = 0; j < NS; ++j) x.v[j] = *reinterpret_cast<const V *>(row + first_channel(lane, j));
+}
+
 // one value per channel, `none` where there are none
 DEV void load_channels(const R *w, int lane, R none, R (&x)[EPL])
 {
@@ -283,23 +296,21 @@ cgtp_gnorm_fwd(const T *__restrict__ x, long ld, const int *__restrict__ ptr, in
         return;
     }
     // The rows stay as they are in memory, 16-bit ones in half the registers: more graphs fit a CU at once.
-    T v[BF][EPL];
+    Raw v[BF];
     R s[1][EPL], m[EPL];
     const int left = at.on ? (int)n - at.row : 0;  // of its rows and those behind them
     const T *px = x + (lo + at.row) * ld;
 #pragma unroll
     for (int t = 0; t < BF; ++t, px += at.RG * ld) {
         if (t * at.RG < left)
-            load_row(px, at.lane, v[t]);
+            load_raw(px, at.lane, v[t]);
         else
-            EACH(i) v[t][i] = (T)0;
-    }
-    EACH(i)
-    {
-        s[0][i] = (R)0;
 #pragma unroll
-        for (int t = 0; t < BF; ++t) s[0][i] += (R)v[t][i];
+            for (int j = 0; j < NS; ++j) v[t].v[j] = (Raw::V)(T)0;
     }
+    EACH(i) s[0][i] = (R)0;
+#pragma unroll
+    for (int t = 0; t < BF; ++t) EACH(i) s[0][i] += v[t].at(i);
     group_totals<1>(at, s, sums, part_sums, total);
     const R inv = (R)1 / (R)(n * W);
     load_groups(total, at.lane, m);
@@ -307,12 +318,14 @@ cgtp_gnorm_fwd(const T *__restrict__ x, long ld, const int *__restrict__ ptr, in
     {
         m[i] *= inv;
         s[0][i] = (R)0;
+    }
 #pragma unroll
-        for (int t = 0; t < BF; ++t) {
-            const R o = t * at.RG < left ? (R)v[t][i] - m[i] : (R)0;
+    for (int t = 0; t < BF; ++t)
+        if (t * at.RG < left) EACH(i)
+        {
+            const R o = v[t].at(i) - m[i];
             s[0][i] = fma(o, o, s[0][i]);
         }
-    }
     for (int g = threadIdx.x; g < GROUPS; g += blockDim.x) mean[g0 * GROUPS + g] = total[g] * inv;
     group_totals<1>(at, s, sums, part_sums, total);
     R k[EPL], wc[EPL], bc[EPL];
@@ -326,7 +339,7 @@ cgtp_gnorm_fwd(const T *__restrict__ x, long ld, const int *__restrict__ ptr, in
     for (int t = 0; t < BF; ++t, py += at.RG * y_ld) {
         if (t * at.RG >= left) continue;
         R o[EPL];
-        EACH(i) o[i] = act_value(fma((R)v[t][i] - m[i], k[i], bc[i]));
+        EACH(i) o[i] = act_value(fma(v[t].at(i) - m[i], k[i], bc[i]));
         store_row(py, at.lane, o);
     }
 }

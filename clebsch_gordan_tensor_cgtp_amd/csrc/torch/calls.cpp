@@ -1,4 +1,4 @@
-// The block and optimizer calls from Python, for the ordinary call, whose outputs are all new: checks,
+// The block, group norm, routing, experts' and optimizer calls from Python, for the ordinary call, whose outputs are all new: checks,
 // outputs, the current stream and the C entry point in compiled code (a small join takes 5.9 us
 // here and 11.9 us through ctypes, of which the launch is 3).  Each function returns None where an
 // argument is not as its entry point wants it; binding.py then goes its own way, through ctypes, and
@@ -32,7 +32,26 @@ struct AdamWMeta {
     at::ScalarType elem, real;
 };
 
-const char *const kBlock = "cgtp.block", *const kAdamW = "cgtp.adamw";
+struct GroupNormMeta {
+    const cgtp_group_norm *norm;
+    int64_t channels, groups;
+    at::ScalarType rows, real;
+};
+
+struct RouterMeta {
+    const cgtp_router *router;
+    int64_t experts, top_k;
+    at::ScalarType rows, real;
+};
+
+struct LinearMeta {
+    const cgtp_linear *linear;
+    int64_t d_in, d_out, experts, top_k, numel;
+    at::ScalarType rows, real;
+};
+
+const char *const kBlock = "cgtp.block", *const kAdamW = "cgtp.adamw", *const kGroupNorm = "cgtp.group_norm",
+           *const kRouter = "cgtp.router", *const kLinear = "cgtp.linear";
 
 at::ScalarType elem_type(long dtype)
 {
@@ -273,6 +292,289 @@ PyObject *join_backward(PyObject *, PyObject *const *a, Py_ssize_t n_args)
     END_HANDLE_TH_ERRORS
 }
 
+// ------------------------------------------------------------------------------------------ experts
+
+template <class M> PyObject *capsule(M *m, const char *name, PyCapsule_Destructor drop)
+{
+    if (PyErr_Occurred()) {
+        delete m;
+        return nullptr;
+    }
+    return PyCapsule_New(m, name, drop);
+}
+
+at::ScalarType real_type(long dtype) { return dtype == CGTP_F64 ? at::kDouble : at::kFloat; }
+
+// (handle, channels, groups, dtype)
+PyObject *group_norm(PyObject *, PyObject *const *a, Py_ssize_t n)
+{
+    HANDLE_TH_ERRORS
+    if (!takes(n, 4)) return nullptr;
+    const long dtype = PyLong_AsLong(a[3]);
+    return capsule(new GroupNormMeta{static_cast<const cgtp_group_norm *>(PyLong_AsVoidPtr(a[0])), PyLong_AsLongLong(a[1]),
+                                     PyLong_AsLongLong(a[2]), elem_type(dtype), real_type(dtype)},
+                   kGroupNorm, [](PyObject *o) { delete static_cast<GroupNormMeta *>(PyCapsule_GetPointer(o, kGroupNorm)); });
+    END_HANDLE_TH_ERRORS
+}
+
+// the graphs of row pointers ptr; -1 where they are none
+int64_t graphs_of(const Args &in, PyObject *o, const int32_t **ptr)
+{
+    const at::Tensor *t = tensor(o);
+    if (!in.here(t, at::kInt) || t->dim() != 1 || t->size(0) < 1 || !t->is_contiguous()) return -1;
+    *ptr = static_cast<const int32_t *>(t->data_ptr());
+    return t->size(0) - 1;
+}
+
+// (norm, x, ptr, w, bias, need_stats) -> (y, mean, rstd)
+PyObject *group_norm_forward(PyObject *, PyObject *const *a, Py_ssize_t n_args)
+{
+    HANDLE_TH_ERRORS
+    if (!takes(n_args, 6)) return nullptr;
+    if (a[0] == Py_None) Py_RETURN_NONE;  // closed
+    const auto *m = static_cast<const GroupNormMeta *>(PyCapsule_GetPointer(a[0], kGroupNorm));
+    if (!m) return nullptr;
+    const at::Tensor *x = tensor(a[1]);
+    Args in(x);
+    if (!in.fine || x->dim() != 2) Py_RETURN_NONE;
+    const int64_t n = x->size(0);
+    int64_t ld;
+    const int32_t *ptr = nullptr;
+    const int64_t s = graphs_of(in, a[2], &ptr);
+    const void *xp = in.rows(a[1], m->rows, n, m->channels, &ld), *w = in.at(a[3], m->real, {m->channels}, true),
+               *bias = in.at(a[4], m->real, {m->channels}, true);
+    if (!in.fine || s < 0) Py_RETURN_NONE;
+    const auto real = x->options().dtype(m->real);
+    at::Tensor y = at::empty({n, m->channels}, x->options()), mean, rstd, ws;
+    if (PyObject_IsTrue(a[5]) == 1) {
+        mean = at::empty({s, m->groups}, real);
+        rstd = at::empty({s, m->groups}, real);
+    }
+    size_t bytes = 0;
+    cgtp_status st = cgtp_group_norm_workspace_size(m->norm, n, s, 0, &bytes);
+    if (st == CGTP_OK && bytes) ws = at::empty({(int64_t)bytes}, x->options().dtype(at::kByte));
+    if (st == CGTP_OK)
+        st = cgtp_group_norm_forward(m->norm, n, s, ptr, xp, ld, w, bias, address(y), m->channels, 1, address(mean),
+                                     address(rstd), address(ws), bytes, in.stream());
+    return answer(st, {&y, &mean, &rstd});
+    END_HANDLE_TH_ERRORS
+}
+
+// (norm, x, ptr, w, bias, mean, rstd, grad_y, need of the three) -> (grad_x, grad_w, grad_bias)
+PyObject *group_norm_backward(PyObject *, PyObject *const *a, Py_ssize_t n_args)
+{
+    HANDLE_TH_ERRORS
+    if (!takes(n_args, 11)) return nullptr;
+    if (a[0] == Py_None) Py_RETURN_NONE;  // closed
+    const auto *m = static_cast<const GroupNormMeta *>(PyCapsule_GetPointer(a[0], kGroupNorm));
+    if (!m) return nullptr;
+    const at::Tensor *x = tensor(a[1]);
+    Args in(x);
+    if (!in.fine || x->dim() != 2) Py_RETURN_NONE;
+    const int64_t n = x->size(0), c = m->channels;
+    int64_t ld, dy_ld;
+    const int32_t *ptr = nullptr;
+    const int64_t s = graphs_of(in, a[2], &ptr);
+    if (s < 0) Py_RETURN_NONE;
+    const void *xp = in.rows(a[1], m->rows, n, c, &ld), *w = in.at(a[3], m->real, {c}, true),
+               *bias = in.at(a[4], m->real, {c}, true), *mean = in.at(a[5], m->real, {s, m->groups}),
+               *rstd = in.at(a[6], m->real, {s, m->groups}), *dy = in.rows(a[7], m->rows, n, c, &dy_ld);
+    if (!in.fine) Py_RETURN_NONE;
+    const auto real = x->options().dtype(m->real);
+    at::Tensor gx, gw, gb, ws;
+    if (PyObject_IsTrue(a[8]) == 1) gx = at::empty({n, c}, x->options());
+    if (PyObject_IsTrue(a[9]) == 1) gw = at::empty({c}, real);
+    if (PyObject_IsTrue(a[10]) == 1) gb = at::empty({c}, real);
+    size_t bytes = 0;
+    cgtp_status st = cgtp_group_norm_workspace_size(m->norm, n, s, 1, &bytes);
+    if (st == CGTP_OK && bytes) ws = at::empty({(int64_t)bytes}, x->options().dtype(at::kByte));
+    if (st == CGTP_OK)
+        st = cgtp_group_norm_backward(m->norm, n, s, ptr, xp, ld, w, bias, mean, rstd, dy, dy_ld, address(gx), c, 1,
+                                      address(gw), address(gb), address(ws), bytes, in.stream());
+    return answer(st, {&gx, &gw, &gb});
+    END_HANDLE_TH_ERRORS
+}
+
+// (handle, experts, top_k, dtype)
+PyObject *router(PyObject *, PyObject *const *a, Py_ssize_t n)
+{
+    HANDLE_TH_ERRORS
+    if (!takes(n, 4)) return nullptr;
+    const long dtype = PyLong_AsLong(a[3]);
+    return capsule(new RouterMeta{static_cast<const cgtp_router *>(PyLong_AsVoidPtr(a[0])), PyLong_AsLongLong(a[1]),
+                                  PyLong_AsLongLong(a[2]), elem_type(dtype), real_type(dtype)},
+                   kRouter, [](PyObject *o) { delete static_cast<RouterMeta *>(PyCapsule_GetPointer(o, kRouter)); });
+    END_HANDLE_TH_ERRORS
+}
+
+const RouterMeta *router_of(PyObject *o) { return static_cast<const RouterMeta *>(PyCapsule_GetPointer(o, kRouter)); }
+
+// (router, logits, bias) -> (experts, weights)
+PyObject *route_forward(PyObject *, PyObject *const *a, Py_ssize_t n_args)
+{
+    HANDLE_TH_ERRORS
+    if (!takes(n_args, 3)) return nullptr;
+    if (a[0] == Py_None) Py_RETURN_NONE;  // closed
+    const RouterMeta *m = router_of(a[0]);
+    if (!m) return nullptr;
+    const at::Tensor *l = tensor(a[1]);
+    Args in(l);
+    if (!in.fine || l->dim() != 2) Py_RETURN_NONE;
+    const int64_t n = l->size(0);
+    int64_t ld;
+    const void *lp = in.rows(a[1], m->rows, n, m->experts, &ld), *bias = in.at(a[2], m->real, {m->experts}, true);
+    if (!in.fine) Py_RETURN_NONE;
+    at::Tensor experts = at::empty({n, m->top_k}, l->options().dtype(at::kInt)),
+               weights = at::empty({n, m->top_k}, l->options().dtype(m->real));
+    return answer(cgtp_route_forward(m->router, n, lp, ld, bias, static_cast<int32_t *>(address(experts)), address(weights),
+                                     in.stream()),
+                  {&experts, &weights});
+    END_HANDLE_TH_ERRORS
+}
+
+// (router, logits, experts, grad_weights) -> (grad_logits,)
+PyObject *route_backward(PyObject *, PyObject *const *a, Py_ssize_t n_args)
+{
+    HANDLE_TH_ERRORS
+    if (!takes(n_args, 4)) return nullptr;
+    if (a[0] == Py_None) Py_RETURN_NONE;  // closed
+    const RouterMeta *m = router_of(a[0]);
+    if (!m) return nullptr;
+    const at::Tensor *l = tensor(a[1]);
+    Args in(l);
+    if (!in.fine || l->dim() != 2) Py_RETURN_NONE;
+    const int64_t n = l->size(0);
+    int64_t ld;
+    const void *lp = in.rows(a[1], m->rows, n, m->experts, &ld), *e = in.at(a[2], at::kInt, {n, m->top_k}),
+               *g = in.at(a[3], m->real, {n, m->top_k});
+    if (!in.fine) Py_RETURN_NONE;
+    at::Tensor out = at::empty({n, m->experts}, l->options());
+    return answer(cgtp_route_backward(m->router, n, lp, ld, static_cast<const int32_t *>(e), g, address(out), in.stream()), {&out});
+    END_HANDLE_TH_ERRORS
+}
+
+// (router, experts) -> (rows, slots, offsets)
+PyObject *route_order(PyObject *, PyObject *const *a, Py_ssize_t n_args)
+{
+    HANDLE_TH_ERRORS
+    if (!takes(n_args, 2)) return nullptr;
+    if (a[0] == Py_None) Py_RETURN_NONE;  // closed
+    const RouterMeta *m = router_of(a[0]);
+    if (!m) return nullptr;
+    const at::Tensor *x = tensor(a[1]);
+    Args in(x);
+    if (!in.fine || x->dim() != 2) Py_RETURN_NONE;
+    const int64_t n = x->size(0);
+    const void *e = in.at(a[1], at::kInt, {n, m->top_k});
+    if (!in.fine) Py_RETURN_NONE;
+    at::Tensor rows = at::empty({n}, x->options()), slots = at::empty({n * m->top_k}, x->options()),
+               offsets = at::empty({m->experts + 1}, x->options()), ws;
+    size_t bytes = 0;
+    cgtp_status st = cgtp_route_order_workspace_size(m->router, n, &bytes);
+    if (st == CGTP_OK && bytes) ws = at::empty({(int64_t)bytes}, x->options().dtype(at::kByte));
+    if (st == CGTP_OK)
+        st = cgtp_route_order(m->router, n, static_cast<const int32_t *>(e), static_cast<int32_t *>(address(rows)),
+                              static_cast<int32_t *>(address(slots)), static_cast<int32_t *>(address(offsets)), address(ws),
+                              bytes, in.stream());
+    return answer(st, {&rows, &slots, &offsets});
+    END_HANDLE_TH_ERRORS
+}
+
+// (handle, d_in, d_out, experts, top_k, weight_numel, dtype)
+PyObject *linear(PyObject *, PyObject *const *a, Py_ssize_t n)
+{
+    HANDLE_TH_ERRORS
+    if (!takes(n, 7)) return nullptr;
+    const long dtype = PyLong_AsLong(a[6]);
+    return capsule(new LinearMeta{static_cast<const cgtp_linear *>(PyLong_AsVoidPtr(a[0])), PyLong_AsLongLong(a[1]),
+                                  PyLong_AsLongLong(a[2]), PyLong_AsLongLong(a[3]), PyLong_AsLongLong(a[4]),
+                                  PyLong_AsLongLong(a[5]), elem_type(dtype), real_type(dtype)},
+                   kLinear, [](PyObject *o) { delete static_cast<LinearMeta *>(PyCapsule_GetPointer(o, kLinear)); });
+    END_HANDLE_TH_ERRORS
+}
+
+// a linear's choice of experts: experts, weights, and of the order rows, slots and offsets
+struct Choice {
+    const int32_t *experts = nullptr;
+    const void *weights = nullptr;
+    const int32_t *rows = nullptr, *slots = nullptr, *offsets = nullptr;
+};
+
+// from the two tensors and the order (None or a tuple of three), `fine` cleared where they are not as they have to be
+Choice choice(Args &in, const LinearMeta *m, int64_t n, PyObject *experts, PyObject *weights, PyObject *order)
+{
+    Choice c;
+    if (m->top_k == 0) {
+        in.fine = in.fine && experts == Py_None && weights == Py_None && order == Py_None;
+        return c;
+    }
+    c.experts = static_cast<const int32_t *>(in.at(experts, at::kInt, {n, m->top_k}));
+    c.weights = in.at(weights, m->real, {n, m->top_k});
+    if (order == Py_None) return c;
+    if (!PyTuple_Check(order) || PyTuple_GET_SIZE(order) != 3) {
+        in.fine = false;
+        return c;
+    }
+    c.rows = static_cast<const int32_t *>(in.at(PyTuple_GET_ITEM(order, 0), at::kInt, {n}, true));
+    c.slots = static_cast<const int32_t *>(in.at(PyTuple_GET_ITEM(order, 1), at::kInt, {n * m->top_k}, true));
+    c.offsets = static_cast<const int32_t *>(in.at(PyTuple_GET_ITEM(order, 2), at::kInt, {m->experts + 1}, true));
+    return c;
+}
+
+// (linear, x, w, experts, weights, order) -> (out,)
+PyObject *linear_forward(PyObject *, PyObject *const *a, Py_ssize_t n_args)
+{
+    HANDLE_TH_ERRORS
+    if (!takes(n_args, 6)) return nullptr;
+    if (a[0] == Py_None) Py_RETURN_NONE;  // closed
+    const auto *m = static_cast<const LinearMeta *>(PyCapsule_GetPointer(a[0], kLinear));
+    if (!m) return nullptr;
+    const at::Tensor *x = tensor(a[1]);
+    Args in(x);
+    if (!in.fine || x->dim() != 2) Py_RETURN_NONE;
+    const int64_t n = x->size(0);
+    int64_t ld;
+    const void *xp = in.rows(a[1], m->rows, n, m->d_in, &ld), *w = in.at(a[2], m->rows, {m->experts, m->numel});
+    const Choice c = choice(in, m, n, a[3], a[4], a[5]);
+    if (!in.fine) Py_RETURN_NONE;
+    at::Tensor out = at::empty({n, m->d_out}, x->options());
+    return answer(cgtp_linear_forward(m->linear, n, xp, ld, w, c.experts, c.weights, c.rows, address(out), m->d_out, in.stream()),
+                  {&out});
+    END_HANDLE_TH_ERRORS
+}
+
+// (linear, x, w, grad_out, experts, weights, order, need of the three) -> (grad_x, grad_w, grad_weights)
+PyObject *linear_backward(PyObject *, PyObject *const *a, Py_ssize_t n_args)
+{
+    HANDLE_TH_ERRORS
+    if (!takes(n_args, 10)) return nullptr;
+    if (a[0] == Py_None) Py_RETURN_NONE;  // closed
+    const auto *m = static_cast<const LinearMeta *>(PyCapsule_GetPointer(a[0], kLinear));
+    if (!m) return nullptr;
+    const at::Tensor *x = tensor(a[1]);
+    Args in(x);
+    if (!in.fine || x->dim() != 2) Py_RETURN_NONE;
+    const int64_t n = x->size(0);
+    int64_t ld, g_ld;
+    const void *xp = in.rows(a[1], m->rows, n, m->d_in, &ld), *w = in.at(a[2], m->rows, {m->experts, m->numel}),
+               *g = in.rows(a[3], m->rows, n, m->d_out, &g_ld);
+    const Choice c = choice(in, m, n, a[4], a[5], a[6]);
+    const bool need_w = PyObject_IsTrue(a[8]) == 1;
+    if (!in.fine || (need_w && m->top_k && (!a[6] || a[6] == Py_None))) Py_RETURN_NONE;
+    at::Tensor gx, gw, gp, ws;
+    if (PyObject_IsTrue(a[7]) == 1) gx = at::empty({n, m->d_in}, x->options());
+    if (need_w) gw = at::empty({m->experts, m->numel}, x->options());
+    if (PyObject_IsTrue(a[9]) == 1 && m->top_k) gp = at::empty({n, m->top_k}, x->options().dtype(m->real));
+    size_t bytes = 0;
+    cgtp_status st = cgtp_linear_workspace_size(m->linear, n, &bytes);
+    if (st == CGTP_OK && bytes) ws = at::empty({(int64_t)bytes}, x->options().dtype(at::kByte));
+    if (st == CGTP_OK)
+        st = cgtp_linear_backward(m->linear, n, xp, ld, w, c.experts, c.weights, c.rows, c.slots, c.offsets, g, g_ld,
+                                  address(gx), m->d_in, address(gw), address(gp), address(ws), bytes, in.stream());
+    return answer(st, {&gx, &gw, &gp});
+    END_HANDLE_TH_ERRORS
+}
+
 // ------------------------------------------------------------------------------------------ optimizer
 
 // (handle, sizes, elements, blocks, norm_workspace, state_bits, dtype)
@@ -414,7 +716,10 @@ PyObject *adamw_state_read(PyObject *, PyObject *const *a, Py_ssize_t n_args)
 PyMethodDef kMethods[] = {CGTP_CALL(block),        CGTP_CALL(norm_forward),  CGTP_CALL(norm_backward),
                           CGTP_CALL(join_forward), CGTP_CALL(join_backward), CGTP_CALL(adamw),
                           CGTP_CALL(grad_norm),    CGTP_CALL(adamw_step),    CGTP_CALL(takes_tensors),
-                          CGTP_CALL(adamw_state_read),
+                          CGTP_CALL(adamw_state_read), CGTP_CALL(group_norm),
+                          CGTP_CALL(group_norm_forward), CGTP_CALL(group_norm_backward), CGTP_CALL(router),
+                          CGTP_CALL(route_forward), CGTP_CALL(route_backward), CGTP_CALL(route_order), CGTP_CALL(linear),
+                          CGTP_CALL(linear_forward), CGTP_CALL(linear_backward),
                           {nullptr, nullptr, 0, nullptr}};
 #undef CGTP_CALL
 
