@@ -8,7 +8,7 @@
 namespace cgtp {
 
 constexpr int kOrderBins = 4097;   // keys of a list, one of them for what has no expert
-constexpr int kOrderWaves = 256;   // waves that count and place a long list
+constexpr int kStretch = 8192;     // most items of a list that one workgroup places
 constexpr int kMaxExperts = 512;
 
 size_t order_workspace(int64_t N, int K, int E);
