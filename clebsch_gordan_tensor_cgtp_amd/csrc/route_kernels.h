@@ -16,7 +16,6 @@ static const char kRouteKernels[] = R"HIP(
 constexpr int RPB = 256 / L;  // rows of a workgroup
 #define EACH(i) _Pragma("unroll") for (int i = 0; i < EPL; ++i)
 
-DEV double inf() { return __builtin_huge_val(); }
 DEV float lowest(float) { return -__builtin_huge_valf(); }
 DEV double lowest(double) { return -__builtin_huge_val(); }
 
@@ -60,17 +59,13 @@ template <int LANES, int STEP = 1, typename V> DEV V lanes_max(V v)
     return v;
 }
 
-// the larger score, of equal ones the lower expert
-template <int STEP = 1, typename V> DEV void lanes_best(V &c, int &e)
+template <int LANES, int STEP = 1> DEV int lanes_min(int v)
 {
-    if constexpr (STEP < L) {
-        const V oc = other<STEP>(c);
-        const int oe = other<STEP>(e);
-        const bool take = oc > c || (oc == c && oe < e);
-        c = take ? oc : c;
-        e = take ? oe : e;
-        lanes_best<STEP * 2>(c, e);
+    if constexpr (STEP < LANES) {
+        const int o = other<STEP>(v);
+        return lanes_min<LANES, STEP * 2>(o < v ? o : v);
     }
+    return v;
 }
 
 // the two largest of a group's lanes
@@ -107,39 +102,84 @@ template <typename S, typename V> DEV void load_share(const S *row, Share sh, V 
     }
 }
 
-// Scores, choice and weights of a row by L lanes.  Scores are doubles whatever the logits' type: which of
-// two neighbours is chosen does not depend on a rounding of the exponential.  An expert whose logit
-// or whose biased score is -inf is masked: it is not chosen, and has no score.
-extern "C" __global__ void __launch_bounds__(256)
-cgtp_route_fwd(const T *__restrict__ logits, long ld, const R *__restrict__ bias, int *__restrict__ experts,
-               R *__restrict__ weights, long N, double scale)
+// ---------------------------------------------------------------- choice
+// A row is L lanes'.  Which of two neighbouring experts is chosen is a matter of their scores in double, whatever the
+// logits' type.  An expert whose logit or whose biased score is -inf is masked: it is not chosen, and has no score.
+struct Row {
+    Share sh;
+    int q, base;  // the lane's number in the row, the wave's lane of the row's first
+    const T *logits;
+    const R *bias;
+};
+
+// the row's groups that are taken: c of the others masked.  Returns whether a group's sum lies so close to another's
+// (`close` times their size) that the order of the two is not sure.
+template <typename V> DEV bool take_groups(const Row &row, V (&c)[EPL], const V (&score)[EPL], V close)
 {
-    const int q = threadIdx.x % L;
-    const long at = (long)blockIdx.x * RPB + threadIdx.x / L, row = at < N ? at : N - 1;
-    const Share sh = share_of(q);
-    double s[EPL], c[EPL], b[EPL];
-    load_share(logits + row * ld, sh, lowest(0.0), s);
-    if (bias)
-        load_share(bias, sh, 0.0, b);
-    else
-        EACH(i) b[i] = 0;
-    double most = lowest(0.0);
-    EACH(i) most = s[i] > most ? s[i] : most;
-    if (!SIGMOID) most = lanes_max<L>(most);
-    double total = 0;
+    V b1 = lowest((V)0), b2 = lowest((V)0);
     EACH(i)
     {
-        const bool masked = s[i] == lowest(0.0);
-        if (SIGMOID)
-            s[i] = masked ? 0.0 : 1.0 / (1.0 + exp(-s[i]));
-        else
-            s[i] = masked ? 0.0 : exp(s[i] - most);
+        const V v = c[i] > lowest((V)0) ? score[i] : lowest((V)0), low = v > b1 ? b1 : v;
+        b1 = v > b1 ? v : b1;
+        b2 = low > b2 ? low : b2;
+    }
+    group_best(b1, b2);
+    const V mine = b2 > lowest((V)0) ? b1 + b2 : b1, near = close * ((V)1 + (mine < (V)0 ? -mine : mine));
+    const int g = row.q / LPG;
+    int rank = 0;
+    bool unsure = false;
+#pragma unroll
+    for (int o = 0; o < NGRP; ++o) {
+        const V theirs = from_lane(mine, row.base + o * LPG), gap = theirs - mine;
+        rank += theirs > mine || (theirs == mine && o < g);
+        unsure = unsure || (o != g && gap >= -near && gap <= near);
+    }
+    EACH(i) c[i] = rank < TOPG ? c[i] : lowest((V)0);
+    return close > (V)0 && unsure;
+}
+
+// The PICKS largest c in falling order, of equal ones the lowest expert first: -1 where none is left.
+template <int PICKS, typename V> DEV void pick(const Row &row, V (&c)[EPL], int (&chosen)[PICKS], V (&best)[PICKS])
+{
+#pragma unroll
+    for (int j = 0; j < PICKS; ++j) {
+        V most = c[0];
+#pragma unroll
+        for (int i = 1; i < EPL; ++i) most = c[i] > most ? c[i] : most;
+        most = lanes_max<L>(most);
+        int e = E;
+#pragma unroll
+        for (int i = EPL - 1; i >= 0; --i) e = c[i] == most ? row.sh.first + i : e;
+        e = lanes_min<L>(e);
+        EACH(i) c[i] = row.sh.first + i == e ? lowest((V)0) : c[i];
+        chosen[j] = most > lowest((V)0) ? e : -1;
+        best[j] = most;
+    }
+}
+
+// The choice in double.
+DEV void choose(const Row &row, int (&chosen)[K])
+{
+    double s[EPL], c[EPL], b[EPL], most = lowest(0.0), total = 0;
+    load_share(row.logits, row.sh, lowest(0.0), s);
+    if (row.bias)
+        load_share(row.bias, row.sh, 0.0, b);
+    else
+        EACH(i) b[i] = 0;
+    EACH(i)
+    {
+        most = s[i] > most ? s[i] : most;
+        c[i] = s[i] == lowest(0.0) ? lowest(0.0) : 0.0;
+    }
+    if (!SIGMOID) most = lanes_max<L>(most);
+    EACH(i)
+    {
+        s[i] = c[i] < 0.0 ? 0.0 : SIGMOID ? 1.0 / (1.0 + exp(-s[i])) : exp(s[i] - most);
         total += s[i];
-        c[i] = masked ? lowest(0.0) : 0.0;
     }
     if (!SIGMOID) {
         total = lanes_sum<L>(total);
-        EACH(i) s[i] = c[i] == 0.0 ? s[i] / total : 0.0;
+        EACH(i) s[i] = c[i] < 0.0 ? 0.0 : s[i] / total;
     }
     EACH(i)
     {
@@ -149,74 +189,138 @@ cgtp_route_fwd(const T *__restrict__ logits, long ld, const R *__restrict__ bias
         }
     }
     if (TOPG < NGRP) {
-        double b1 = lowest(0.0), b2 = lowest(0.0);
-        EACH(i)
-        {
-            const double low = c[i] > b1 ? b1 : c[i];
-            b1 = c[i] > b1 ? c[i] : b1;
-            b2 = low > b2 ? low : b2;
-        }
-        group_best(b1, b2);
-        const double mine = b2 > lowest(0.0) ? b1 + b2 : b1;
-        const int g = q / LPG, base = (threadIdx.x & 63) - q;
-        int rank = 0;
-        for (int o = 0; o < NGRP; ++o) {
-            const double theirs = from_lane(mine, base + o * LPG);
-            rank += theirs > mine || (theirs == mine && o < g);
-        }
-        EACH(i) c[i] = rank < TOPG ? c[i] : lowest(0.0);
+        EACH(i) b[i] = c[i];
+        take_groups(row, c, b, 0.0);
     }
-    int chosen[K];
-    double score[K], sum = 0;
+    double best[K];
+    pick(row, c, chosen, best);
+}
+
+// The choice in float, and whether it is surely the one in double.  Without a bias experts go by their logits, whose
+// order is the scores' but where these are equal as doubles: logits that differ by next to nothing, or scores near 1
+// or 0.  With one, a score is off by less than 2^-20 of 1 (a rounding of the exponent's argument, |x| exp(-|x|) of it, the
+// exponential, a sum of up to 512 and a quotient), so c in neighbouring places have to be further apart than twice
+// that, or of equal logits and biases.
+DEV bool choose_fast(const Row &row, int (&chosen)[K])
+{
+    constexpr float CLOSE = 4e-6f;
+    constexpr int PICKS = K < E ? K + 1 : K;  // the one after the last shows whether that one is sure
+    float x[EPL], c[EPL], s[EPL], most = lowest(0.0f);
+    load_share(row.logits, row.sh, lowest(0.0f), x);
+    EACH(i) most = x[i] > most ? x[i] : most;
+    most = lanes_max<L>(most);
+    bool sure = most < (SIGMOID ? 18.0f : 1e4f);
+    EACH(i) c[i] = x[i];
+    if (row.bias || TOPG < NGRP) {
+        float total = 0, b[EPL];
+        if (row.bias)
+            load_share(row.bias, row.sh, 0.0f, b);
+        else
+            EACH(i) b[i] = 0;
+        EACH(i)
+        {
+            const float e = __builtin_amdgcn_exp2f((SIGMOID ? -x[i] : x[i] - most) * 1.44269504f);
+            s[i] = SIGMOID ? __builtin_amdgcn_rcpf(1.0f + e) : e;
+            total += x[i] > lowest(0.0f) ? s[i] : 0.0f;
+        }
+        if (!SIGMOID) {
+            const float inv = __builtin_amdgcn_rcpf(lanes_sum<L>(total));
+            EACH(i) s[i] *= inv;
+        }
+        EACH(i)
+        {
+            s[i] += b[i];
+            if (row.bias) c[i] = x[i] > lowest(0.0f) ? s[i] : lowest(0.0f);
+            sure = sure && (x[i] == lowest(0.0f) || s[i] - s[i] == 0.0f);  // finite
+        }
+        if (TOPG < NGRP) sure = !take_groups(row, c, s, 2 * CLOSE) && sure;
+    } else {
+        EACH(i) sure = sure && (x[i] == lowest(0.0f) || x[i] - x[i] == 0.0f);
+    }
+    int picked[PICKS];
+    float best[PICKS];
+    pick(row, c, picked, best);
 #pragma unroll
-    for (int j = 0; j < K; ++j) {
-        double best = lowest(0.0);
-        int e = E;
-        EACH(i)
-        {
-            const bool take = c[i] > best;
-            best = take ? c[i] : best;
-            e = take ? sh.first + i : e;
+    for (int j = 0; j < K; ++j) chosen[j] = picked[j];
+#pragma unroll
+    for (int j = 0; j < PICKS; ++j) {
+        if (j % L != row.q) continue;  // a lane looks at some places and the next ones
+        if (picked[j] < 0) continue;
+        if (!row.bias) {
+            const float next = j + 1 < PICKS ? best[j + 1] : best[j], gap = best[j] - next;
+            // far below 1 (a sigmoid) or the largest (a softmax) scores may be too small for a double
+            sure = sure && (gap == 0.0f || gap > 1e-10f * (1.0f + fabsf(best[j]) + fabsf(most))) &&
+                   (SIGMOID ? best[j] : best[j] - most) > -600.0f;
+        } else if (j + 1 < PICKS && picked[j + 1] >= 0 && best[j] - best[j + 1] <= CLOSE * (1.0f + fabsf(best[j]))) {
+            const int e0 = picked[j], e1 = picked[j + 1];
+            sure = sure && row.logits[e0] == row.logits[e1] && row.bias[e0] == row.bias[e1];
         }
-        lanes_best(best, e);
-        const bool some = best > lowest(0.0);
-        double v = 0;
-        EACH(i)
-        {
-            const bool it = sh.first + i == e;
-            v = it ? s[i] : v;
-            c[i] = it ? lowest(0.0) : c[i];
-        }
-        const int owner = (threadIdx.x & 63) - q + (e / GW) * LPG + (e % GW) / EPL;
-        v = from_lane(v, some ? owner : (int)(threadIdx.x & 63));
-        chosen[j] = some ? e : -1;
-        score[j] = some ? v : 0.0;
-        sum += score[j];
+    }
+    return lanes_min<L>(sure ? 1 : 0) != 0;
+}
+
+// Choice and weights of a row by L lanes.  A weight is formed in double from the chosen logits, each by one lane.
+extern "C" __global__ void __launch_bounds__(256)
+cgtp_route_fwd(const T *__restrict__ logits, long ld, const R *__restrict__ bias, int *__restrict__ experts,
+               R *__restrict__ weights, long N, double scale)
+{
+    const long at = (long)blockIdx.x * RPB + threadIdx.x / L, n = at < N ? at : N - 1;
+    Row row;
+    row.q = threadIdx.x % L;
+    row.base = (threadIdx.x & 63) - row.q;
+    row.sh = share_of(row.q);
+    row.logits = logits + n * ld;
+    row.bias = bias;
+    int chosen[K];
+    bool sure = false;
+    if constexpr (sizeof(R) == 4) sure = choose_fast(row, chosen);
+    if (!sure) choose(row, chosen);
+    double total = 1, most = 0;
+    if (!SIGMOID && !RENORM) {
+        double x[EPL];
+        load_share(row.logits, row.sh, lowest(0.0), x);
+        most = lowest(0.0);
+        EACH(i) most = x[i] > most ? x[i] : most;
+        most = lanes_max<L>(most);
+        total = 0;
+        EACH(i) total += x[i] == lowest(0.0) ? 0.0 : exp(x[i] - most);
+        total = lanes_sum<L>(total);
+    }
+    // the lane's places, K / L of them
+    constexpr int PLACES = (K + L - 1) / L;
+    int e[PLACES];
+    double x[PLACES], top = lowest(0.0), sum = 0;
+#pragma unroll
+    for (int p = 0; p < PLACES; ++p) {
+        e[p] = -1;
+#pragma unroll
+        for (int j = p * L; j < K && j < (p + 1) * L; ++j) e[p] = j % L == row.q ? chosen[j] : e[p];
+        x[p] = e[p] < 0 ? lowest(0.0) : (double)(R)row.logits[e[p]];
+        top = x[p] > top ? x[p] : top;
+    }
+    if (RENORM) {
+        // with the largest exponential taken out: scores too small for a double have shares
+        top = lanes_max<L>(top);
+        if (SIGMOID && top > 0.0) top = 0.0;
+    }
+#pragma unroll
+    for (int p = 0; p < PLACES; ++p) {
+        if (RENORM)
+            x[p] = e[p] < 0 ? 0.0 : SIGMOID ? 1.0 / (exp(top) + exp(top - x[p])) : exp(x[p] - top);
+        else
+            x[p] = e[p] < 0 ? 0.0 : SIGMOID ? 1.0 / (1.0 + exp(-x[p])) : exp(x[p] - most) / total;
+        sum += x[p];
+    }
+    if (RENORM) {
+        sum = lanes_sum<L>(sum);
+        scale = sum == 0.0 ? 0.0 : scale / sum;
     }
     if (at >= N) return;
-    if (RENORM && sum < 1e-290) {
-        // scores near or below a double's range (far under an unchosen logit, or sigmoids of under -660): their shares
-        // with the largest exponential taken out, as in the backward
-        double x[K], top = lowest(0.0);
 #pragma unroll
-        for (int j = 0; j < K; ++j) {
-            x[j] = chosen[j] < 0 ? lowest(0.0) : (double)(R)logits[row * ld + chosen[j]];
-            top = x[j] > top ? x[j] : top;
-        }
-        if (SIGMOID && top > 0.0) top = 0.0;
-        sum = 0;
-#pragma unroll
-        for (int j = 0; j < K; ++j) {
-            score[j] = chosen[j] < 0 ? 0.0 : SIGMOID ? 1.0 / (exp(top) + exp(top - x[j])) : exp(x[j] - top);
-            sum += score[j];
-        }
-    }
-    const double f = RENORM ? (sum == 0.0 ? 0.0 : scale / sum) : scale;
-#pragma unroll
-    for (int j = 0; j < K; ++j)
-        if (q == j % L) {
-            experts[row * K + j] = chosen[j];
-            weights[row * K + j] = (R)(score[j] * f);
+    for (int p = 0; p < PLACES; ++p)
+        if (p * L + row.q < K) {
+            experts[n * K + p * L + row.q] = e[p];
+            weights[n * K + p * L + row.q] = (R)(x[p] * scale);
         }
 }
 
