@@ -37,7 +37,7 @@ struct Direction {
 };
 
 struct Tile {
-    int path, v, u, cv, cu;
+    int path, v, u, bv, bu, wv, wu, nodes;
 };
 
 }  // namespace
@@ -58,7 +58,7 @@ namespace cgtp {
 
 namespace {
 
-constexpr int kMaxPaths = 64, kMaxUnits = 128, kLds = 160 * 1024;
+constexpr int kMaxPaths = 64, kMaxUnits = 128, kLds = 160 * 1024, kMaxStretch = 512;
 
 void find_paths(cgtp_linear &l, const std::vector<Irrep> &ins, const std::vector<Irrep> &outs)
 {
@@ -198,24 +198,27 @@ void plan_direction(cgtp_linear &l, Direction &d, const std::vector<Irrep> &ins,
     if (d.units.size() > (size_t)kMaxUnits) throw Error(CGTP_ERR_UNSUPPORTED, "linear: too many channels");
 }
 
-// Channels that a lane holds of an operand of a gradient's tile: 16-bit operands of eight nodes, or 4 (2 in
-// double) 16-blocks of one.
-int lane_channels(const cgtp_linear &l, int mul, int k)
-{
-    const int most = l.elem == 2 ? (k == 1 ? 4 : k <= 3 ? 4 : k <= 7 ? 2 : 1) : l.elem == 8 ? (k <= 7 ? 2 : 1) : k <= 7 ? 4 : 2;
-    int c = 1;
-    while (c < most && c * 16 < mul) c *= 2;
-    return c;
-}
-
+// Tiles of the gradients: four waves, two along each side where there are blocks for them, hold up to 4 x 4 16-blocks
+// each (2 x 2 in double, and in 16 bits for many components, whose rows fill LDS); the nodes at hand take up to 32 KB of
+// LDS, 64 KB of 16-bit rows, of which a matrix instruction takes 32.  Tiles of many components come first: they take longest.
 void plan_tiles(cgtp_linear &l)
 {
     for (size_t p = 0; p < l.paths.size(); ++p) {
         const LinearPath &q = l.paths[p];
-        const int cv = lane_channels(l, q.mul_out, q.k), cu = lane_channels(l, q.mul_in, q.k);
-        for (int v = 0; v < q.mul_out; v += 16 * cv)
-            for (int u = 0; u < q.mul_in; u += 16 * cu) l.tiles.push_back({(int)p, v, u, cv, cu});
+        const int bv = (q.mul_out + 15) / 16, bu = (q.mul_in + 15) / 16;
+        const int most = l.elem == 8 || (l.elem == 2 && q.k > 3) ? 2 : 4;
+        int wv = std::min(2, bv), wu = std::min(2, bu);
+        if (wv == 1) wu = std::min(4, bu);
+        if (wu == 1) wv = std::min(4, bv);
+        for (int v = 0; v < bv; v += most * wv)
+            for (int u = 0; u < bu; u += most * wu) {
+                Tile t{(int)p, 16 * v, 16 * u, std::min(bv - v, most * wv), std::min(bu - u, most * wu), wv, wu, 0};
+                const int step = l.elem == 2 ? 32 : 4, row = 16 * (t.bv + t.bu) * q.k * l.elem;
+                t.nodes = step * std::max(1, std::min(l.elem == 2 ? 2 : 8, (l.elem == 2 ? 65536 : 32768) / (row * step)));
+                l.tiles.push_back(t);
+            }
     }
+    std::stable_sort(l.tiles.begin(), l.tiles.end(), [&](const Tile &a, const Tile &b) { return l.paths[a.path].k > l.paths[b.path].k; });
 }
 
 struct Text {
@@ -293,26 +296,30 @@ std::string constants(const cgtp_linear &l)
     t.list("T_PATH", l.tiles.size(), [&](size_t i) { return l.tiles[i].path; });
     t.list("T_V", l.tiles.size(), [&](size_t i) { return l.tiles[i].v; });
     t.list("T_U", l.tiles.size(), [&](size_t i) { return l.tiles[i].u; });
-    t.list("T_CV", l.tiles.size(), [&](size_t i) { return l.tiles[i].cv; });
-    t.list("T_CU", l.tiles.size(), [&](size_t i) { return l.tiles[i].cu; });
+    t.list("T_BV", l.tiles.size(), [&](size_t i) { return l.tiles[i].bv; });
+    t.list("T_BU", l.tiles.size(), [&](size_t i) { return l.tiles[i].bu; });
+    t.list("T_WV", l.tiles.size(), [&](size_t i) { return l.tiles[i].wv; });
+    t.list("T_WU", l.tiles.size(), [&](size_t i) { return l.tiles[i].wu; });
+    t.list("T_NODES", l.tiles.size(), [&](size_t i) { return l.tiles[i].nodes; });
+    t.num("MAX_STRETCH", kMaxStretch);
     return t.s;
 }
 
 int64_t slots_of(const cgtp_linear &l, int64_t N) { return N * std::max(1, l.cfg.top_k); }
 
-// Slots of a stretch of the weight gradients: enough stretches for some waves to each of the 1,024 SIMDs, but
-// no shorter than 64 slots, each stretch writing a partial sum of every weight.
+// Slots of a stretch of the weight gradients: enough workgroups for some to each of the 256 CUs, but no shorter than
+// 64 slots, each stretch writing a partial sum of every weight.
 int64_t stretch_len(const cgtp_linear &l, int64_t N)
 {
-    const int64_t slots = slots_of(l, N), waves = std::max<int64_t>(1, 4096 / (int64_t)l.tiles.size());
-    const int64_t len = std::max<int64_t>(64, (slots + waves - 1) / waves);
-    return (len + 31) / 32 * 32;
+    const int64_t slots = slots_of(l, N), groups = std::max<int64_t>(1, 1024 / (int64_t)l.tiles.size());
+    const int64_t len = std::max<int64_t>(64, (slots + groups - 1) / groups);
+    return std::min<int64_t>(kMaxStretch, (len + 31) / 32 * 32);
 }
 
 int64_t stretches(const cgtp_linear &l, int64_t N)
 {
     const int64_t len = stretch_len(l, N);
-    return slots_of(l, N) / len + l.cfg.experts;
+    return (slots_of(l, N) / len + l.cfg.experts + 7) / 8 * 8;  // a whole number to each of the 8 XCDs
 }
 
 size_t aligned(size_t n) { return (n + 255) / 256 * 256; }
@@ -516,7 +523,7 @@ cgtp_status cgtp_linear_backward(const cgtp_linear *linear, int64_t N, const voi
         }
         if (grad_w) {
             void *args[] = {&x, &xl, &grad_out, &gl, &weights, &slots, &offsets, &n, &count, &len, &part};
-            run2(F[cgtp_linear::backward_w], (int64_t)l.tiles.size(), stretches(l, N), 64, args, stream);
+            run(F[cgtp_linear::backward_w], (int64_t)l.tiles.size() * stretches(l, N), 256, args, stream);
             void *rargs[] = {&part, &offsets, &count, &len, &grad_w};
             run2(F[cgtp_linear::reduce], (l.numel + 255) / 256, l.cfg.experts, 256, rargs, stream);
         }

@@ -18,8 +18,8 @@
 //     DOT                                     1: the weights p have a gradient
 //   NPATH, W_*    for the weight gradients, per path: W_XC, W_MI the input's first column and channels, W_GC, W_MO
 //                 the output's, W_K, W_OFF the first weight
-//   NT, T_PATH, T_V, T_U, T_CV, T_CU          tiles of the gradients: path, first output and input channel,
-//                                             channels a lane holds of each (times 16 in the tile)
+//   NT, T_PATH, T_V, T_U, T_BV, T_BU          tiles of the gradients: path, first output and input channel, 16-blocks
+//   T_WV, T_WU, T_NODES, MAX_STRETCH          of each; waves along each, nodes in LDS at a time; most slots of a stretch
 #pragma once
 
 namespace cgtp {
@@ -448,11 +448,10 @@ extern "C" __global__ void __launch_bounds__(256) cgtp_linear_transpose(const T 
 )HIP"
 R"HIP(
 // ---------------------------------------------------------------- weight gradients
-// dW[e][v][u] = sum over the expert's slots of p sum_m g[v][m] x[u][m].  A wave takes a stretch of one
-// expert's slots and one tile of a path; nodes are the summed index.  A lane holds neighbouring
-// channels here too, T_CV (T_CU) of them: channel 16-blocks of a tile are interleaved, block j having every
-// T_CV-th channel from j on.  16-bit operands take g p rounded to T: one rounding more of each term.
-constexpr int NL = HALF ? 8 : 1;  // nodes of a lane's quarter in a step
+// dW[e][v][u] = sum over the expert's slots of p sum_m g[v][m] x[u][m].  A workgroup takes a stretch of one
+// expert's slots and one tile of a path; nodes are the summed index.  Its rows come into LDS along the rows, NODES at a
+// time, the next ones on their way in registers while the present ones are multiplied, and p is put to g on the way.
+// 16-bit operands take g p rounded to T: one rounding more of each term.
 
 struct Stretch {
     int expert;
@@ -485,93 +484,198 @@ DEV Stretch stretch_of(const int *offsets, long count, long len, long number, in
     return {e, b < lo ? hi : b, b + len < hi ? b + len : hi};
 }
 
-template <int I> DEV void tile(const T *x, long x_ld, const T *g, long g_ld, const R *weights, const int *slots,
-                               Stretch s, long N, long count, R *part, int lane)
-{
-    constexpr int P = T_PATH[I], KC = W_K[P], CV = T_CV[I], CU = T_CU[I], MO = W_MO[P], MI = W_MI[P];
-    const int a = lane & 15, quarter = lane >> 4;
-    const int v = T_V[I] + a * CV, u = T_U[I] + a * CU;  // the lane's first channels
-    const int nv = MO - v < 0 ? 0 : MO - v, nu = MI - u < 0 ? 0 : MI - u;
-    V4 acc[CV][CU];
-#pragma unroll
-    for (int j = 0; j < CV; ++j)
-#pragma unroll
-        for (int k = 0; k < CU; ++k) acc[j][k] = (V4)(R)0;
-    for (long s0 = s.begin; s0 < s.end; s0 += 4 * NL) {
-        T gr[NL][CV * KC], xr[NL][CU * KC];
-#pragma unroll
-        for (int t = 0; t < NL; ++t) {
-            const long at = s0 + quarter * NL + t;
-            bool in = at < s.end;
-            long slot = in ? (slots ? slots[at] : at) : 0;
-            in = in && slot >= 0 && slot < count;
-            slot = in ? slot : 0;
-            const long n = slot / KS;
-            const R p = K > 0 ? weights[slot] : (R)1;
-            load_channels<CV, KC, false>(g + n * g_ld + W_GC[P] + v * KC, in ? nv : 0, gr[t]);
-            load_channels<CU, KC, false>(x + n * x_ld + W_XC[P] + u * KC, in ? nu : 0, xr[t]);
-            if (K > 0) {
-#pragma unroll
-                for (int i = 0; i < CV * KC; ++i) gr[t][i] = in ? (T)((R)gr[t][i] * p) : (T)0;
-            }
-        }
-#pragma unroll
-        for (int m = 0; m < KC; ++m) {
+// LDS of a workgroup: rows and weights of its stretch's slots, then the nodes at hand
+struct Table {
+    int row[MAX_STRETCH];  // -1 where a slot has none
+    R p[MAX_STRETCH];
+};
+
 #if defined(BITS16)
-            V8 xv[CU];
-#pragma unroll
-            for (int k = 0; k < CU; ++k)
-#pragma unroll
-                for (int t = 0; t < 8; ++t) xv[k][t] = xr[t][k * KC + m];
-#pragma unroll
-            for (int j = 0; j < CV; ++j) {
-                V8 gv;
-#pragma unroll
-                for (int t = 0; t < 8; ++t) gv[t] = gr[t][j * KC + m];
-#pragma unroll
-                for (int k = 0; k < CU; ++k) acc[j][k] = mfma(gv, xv[k], acc[j][k]);
-            }
+constexpr int OCTET = 8;  // nodes that an operand's lane holds; in LDS a column's eight lie side by side
 #else
-#pragma unroll
-            for (int j = 0; j < CV; ++j)
-#pragma unroll
-                for (int k = 0; k < CU; ++k) acc[j][k] = MFMA(gr[0][j * KC + m], xr[0][k * KC + m], acc[j][k]);
+constexpr int OCTET = 1;
 #endif
+
+template <int I> struct Shape {
+    static constexpr int P = T_PATH[I], KC = W_K[P], WV = T_WV[I], WU = T_WU[I];
+    static constexpr int NV = (T_BV[I] + WV - 1) / WV, NU = (T_BU[I] + WU - 1) / WU;  // blocks of a wave
+    static constexpr int V = T_V[I], U = T_U[I], MO = W_MO[P], MI = W_MI[P];
+    static constexpr int GC = (MO - V < T_BV[I] * 16 ? MO - V : T_BV[I] * 16) * KC;   // columns of the tile
+    static constexpr int XC = (MI - U < T_BU[I] * 16 ? MI - U : T_BU[I] * 16) * KC;
+    static constexpr int GP = NV * WV * 16 * KC, XP = NU * WU * 16 * KC;               // and in LDS
+    // a node's row in LDS begins 16 banks after the one before, so that a wave's four nodes meet different ones
+    static constexpr int PITCH = ((GP + XP) * (int)sizeof(T) + 255) / 256 * 256 / (int)sizeof(T) + 64 / (int)sizeof(T);
+    static constexpr int NODES = T_NODES[I], CG = (GC + VEC - 1) / VEC, CX = (XC + VEC - 1) / VEC;
+    static constexpr int UNITS = NODES / OCTET * (CG + CX), ROUNDS = (UNITS + 255) / 256;
+};
+
+// What a thread brings of the nodes from `first` on: ROUNDS runs of VEC columns, of OCTET nodes each.
+template <int I> DEV void fetch(const T *x, long x_ld, const T *g, long g_ld, const Table &tab, int first, int count,
+                                V16 (&v)[Shape<I>::ROUNDS][OCTET])
+{
+    typedef Shape<I> S;
+#pragma unroll
+    for (int r = 0; r < S::ROUNDS; ++r) {
+        const int at = r * 256 + threadIdx.x, c = at % (S::CG + S::CX);
+        const bool out = c < S::CG;
+        const int col = (out ? c : c - S::CG) * VEC, left = (out ? S::GC : S::XC) - col;
+        const T *base = out ? g + W_GC[S::P] + S::V * S::KC + col : x + W_XC[S::P] + S::U * S::KC + col;
+        const long ld = out ? g_ld : x_ld;
+#pragma unroll
+        for (int o = 0; o < OCTET; ++o) {
+            const int node = first + at / (S::CG + S::CX) * OCTET + o;
+            const int row = at < S::UNITS && node < count ? tab.row[node] : -1;
+            T q[VEC];
+            load_channels<VEC, 1, false>(base + (row < 0 ? 0 : row) * ld, row < 0 ? 0 : left, q);
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) v[r][o][i] = q[i];
         }
     }
-#pragma unroll
-    for (int j = 0; j < CV; ++j)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int row = sizeof(T) == 8 ? quarter + 4 * i : 4 * quarter + i, vo = T_V[I] + row * CV + j;
-            if (vo < MO) {
-#pragma unroll
-                for (int k = 0; k < CU; ++k)
-                    if (k < nu) part[W_OFF[P] + vo * MI + u + k] = acc[j][k][i];
-            }
-        }
 }
 
-template <int I = 0> DEV void tiles(int which, const T *x, long x_ld, const T *g, long g_ld, const R *weights,
-                                    const int *slots, Stretch s, long N, long count, R *part, int lane)
+template <int I> DEV void keep(T *lds, const Table &tab, int first, int count, const V16 (&v)[Shape<I>::ROUNDS][OCTET])
+{
+    typedef Shape<I> S;
+#pragma unroll
+    for (int r = 0; r < S::ROUNDS; ++r) {
+        const int at = r * 256 + threadIdx.x, c = at % (S::CG + S::CX), node = at / (S::CG + S::CX) * OCTET;
+        if (at >= S::UNITS) break;
+        const bool out = c < S::CG;
+        V16 q[OCTET];
+#pragma unroll
+        for (int o = 0; o < OCTET; ++o) {
+            q[o] = v[r][o];
+            if (K > 0 && out) {
+                const bool in = first + node + o < count;
+                const R p = in ? tab.p[first + node + o] : (R)0;
+#pragma unroll
+                for (int i = 0; i < VEC; ++i) q[o][i] = in ? (T)((R)v[r][o][i] * p) : (T)0;
+            }
+        }
+        const int col = out ? c * VEC : S::GP + (c - S::CG) * VEC;
+        if (OCTET == 1) {
+            *reinterpret_cast<V16 *>(lds + node * S::PITCH + col) = q[0];
+        } else {
+            // columns of eight nodes, eight of them: turned over in registers
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) {
+                V16 t;
+#pragma unroll
+                for (int o = 0; o < OCTET; ++o) t[o % VEC] = q[o][i];
+                *reinterpret_cast<V16 *>(lds + node * S::PITCH + (col + i) * OCTET) = t;
+            }
+        }
+    }
+}
+
+template <int I> DEV void tile(const T *x, long x_ld, const T *g, long g_ld, const Table &tab, int count, R *part, T *lds)
+{
+    typedef Shape<I> S;
+    constexpr int NV = S::NV, NU = S::NU, KC = S::KC;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+    const int a = lane & 15, quarter = lane >> 4, wv = wave / S::WU, wu = wave % S::WU;
+    const bool works = wave < S::WV * S::WU;
+    V4 acc[NV][NU];
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+#pragma unroll
+        for (int k = 0; k < NU; ++k) acc[j][k] = (V4)(R)0;
+    V16 v[S::ROUNDS][OCTET];
+    fetch<I>(x, x_ld, g, g_ld, tab, 0, count, v);
+    for (int first = 0; first < count; first += S::NODES) {
+        __syncthreads();
+        keep<I>(lds, tab, first, count, v);
+        __syncthreads();
+        if (first + S::NODES < count) fetch<I>(x, x_ld, g, g_ld, tab, first + S::NODES, count, v);
+        if (!works) continue;
+#pragma unroll 1
+        for (int n = 0; n < S::NODES; n += 4 * OCTET) {
+            const T *row = lds + (n + quarter * OCTET) * S::PITCH;
+            const T *gr = row + (wv * NV * 16 + a) * KC * OCTET, *xr = row + (S::GP + (wu * NU * 16 + a) * KC) * OCTET;
+#pragma unroll
+            for (int m = 0; m < KC; ++m) {
+#if defined(BITS16)
+                V8 ga[NV], xa[NU];
+#pragma unroll
+                for (int j = 0; j < NV; ++j) ga[j] = *reinterpret_cast<const V8 *>(gr + (j * 16 * KC + m) * OCTET);
+#pragma unroll
+                for (int k = 0; k < NU; ++k) xa[k] = *reinterpret_cast<const V8 *>(xr + (k * 16 * KC + m) * OCTET);
+#pragma unroll
+                for (int j = 0; j < NV; ++j)
+#pragma unroll
+                    for (int k = 0; k < NU; ++k) acc[j][k] = mfma(ga[j], xa[k], acc[j][k]);
+#else
+                T ga[NV], xa[NU];
+#pragma unroll
+                for (int j = 0; j < NV; ++j) ga[j] = gr[j * 16 * KC + m];
+#pragma unroll
+                for (int k = 0; k < NU; ++k) xa[k] = xr[k * 16 * KC + m];
+#pragma unroll
+                for (int j = 0; j < NV; ++j)
+#pragma unroll
+                    for (int k = 0; k < NU; ++k) acc[j][k] = MFMA(ga[j], xa[k], acc[j][k]);
+#endif
+            }
+        }
+    }
+    if (!works) return;
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+#pragma unroll
+        for (int k = 0; k < NU; ++k)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int row = sizeof(T) == 8 ? quarter + 4 * i : 4 * quarter + i;
+                const int vo = S::V + (wv * NV + j) * 16 + row, uo = S::U + (wu * NU + k) * 16 + a;
+                // blocks past the tile belong to the next one
+                if ((wv * NV + j) < T_BV[I] && (wu * NU + k) < T_BU[I] && vo < S::MO && uo < S::MI)
+                    part[W_OFF[S::P] + vo * S::MI + uo] = acc[j][k][i];
+            }
+}
+
+template <int I = 0> DEV void tiles(int which, const T *x, long x_ld, const T *g, long g_ld, const Table &tab, int count, R *part,
+                                    T *lds)
 {
     if constexpr (I < NT) {
         if (which == I)
-            tile<I>(x, x_ld, g, g_ld, weights, slots, s, N, count, part, lane);
+            tile<I>(x, x_ld, g, g_ld, tab, count, part, lds);
         else
-            tiles<I + 1>(which, x, x_ld, g, g_ld, weights, slots, s, N, count, part, lane);
+            tiles<I + 1>(which, x, x_ld, g, g_ld, tab, count, part, lds);
     }
 }
 
-extern "C" __global__ void __launch_bounds__(64)
+template <int I = 0> constexpr int tile_elements()
+{
+    if constexpr (I < NT) {
+        constexpr int mine = Shape<I>::NODES * Shape<I>::PITCH, rest = tile_elements<I + 1>();
+        return mine > rest ? mine : rest;
+    }
+    return 0;
+}
+
+extern "C" __global__ void __launch_bounds__(256, 2)
 cgtp_linear_bwd_w(const T *__restrict__ x, long x_ld, const T *__restrict__ g, long g_ld, const R *__restrict__ weights,
                   const int *__restrict__ slots, const int *__restrict__ offsets, long N, long count, long len,
                   R *__restrict__ part)
 {
-    const int lane = threadIdx.x;
-    const Stretch s = stretch_of(offsets, count, len, blockIdx.y, lane);
+    __shared__ Table tab;
+    __shared__ V16 lds[tile_elements() / VEC];
+    // the tiles of one stretch follow each other on one XCD, whose L2 has the rows
+    const long stretches = gridDim.x / (8 * NT) * 8, id = blockIdx.x;
+    const long number = id / (8 * NT) * 8 + id % 8;
+    const int which = (int)(id / 8 % NT);
+    if (number >= stretches) return;
+    const Stretch s = stretch_of(offsets, count, len, number, threadIdx.x & 63);
     if (s.begin >= s.end) return;
-    tiles(blockIdx.x, x, x_ld, g, g_ld, weights, slots, s, N, count, part + (long)blockIdx.y * NUMEL, lane);
+    const int n = (int)(s.end - s.begin);
+    for (int i = threadIdx.x; i < n; i += 256) {
+        const long slot = slots ? slots[s.begin + i] : s.begin + i;
+        const bool in = slot >= 0 && slot < count;
+        tab.row[i] = in ? (int)(slot / KS) : -1;
+        tab.p[i] = K > 0 && in ? weights[slot] : (R)1;
+    }
+    __syncthreads();
+    tiles(which, x, x_ld, g, g_ld, tab, n, part + number * NUMEL, reinterpret_cast<T *>(lds));
 }
 
 // the stretches of each expert, in their order; zeros for an expert without slots

@@ -142,9 +142,10 @@ def test_linear_layout(a, b, e, k, n, dtype):
     assert [c[n] for n in ("W_MI", "W_XC", "W_MO", "W_GC", "W_K", "W_OFF")] == [list(v) for v in zip(*found)]
     # the gradients' tiles cover every weight once
     seen = []
-    for p, v, u, cv, cu in zip(*[c[n] for n in ("T_PATH", "T_V", "T_U", "T_CV", "T_CU")]):
+    for p, v, u, bv, bu, wv, wu, nodes in zip(*[c["T_" + n] for n in ("PATH", "V", "U", "BV", "BU", "WV", "WU", "NODES")]):
         mi, _, mo, _, _, off = found[p]
-        seen += [off + i * mi + j for i in range(v, min(mo, v + 16 * cv)) for j in range(u, min(mi, u + 16 * cu))]
+        seen += [off + i * mi + j for i in range(v, min(mo, v + 16 * bv)) for j in range(u, min(mi, u + 16 * bu))]
+        assert wv * wu <= 4 and nodes % 4 == 0
     assert sorted(seen) == list(range(numel))
     # the units of each direction cover every 16-block of every irrep once, in waves that exist
     for name in ("Forward", "Backward"):
