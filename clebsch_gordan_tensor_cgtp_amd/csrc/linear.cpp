@@ -91,7 +91,8 @@ int round_up(int n, int to) { return (n + to - 1) / to * to; }
 int odd_pitch(int elements, int vec) { return (round_up(elements, vec) / vec | 1) * vec; }
 
 // Irreps of one degree and parity belong to one part: no others read what they read.  Parts are filled up to
-// 64 KB of LDS for their rows in and out, so that two workgroups or more share a CU; a wide irrep may take all of it.
+// 64 KB of LDS for their rows in and out, so that two workgroups or more share a CU; where one degree's alone take over
+// 76 KB, results do not go through LDS.
 void plan_direction(cgtp_linear &l, Direction &d, const std::vector<Irrep> &ins, const std::vector<Irrep> &outs, bool backward)
 {
     const int vec = 16 / l.elem, step = l.elem == 2 ? 32 : 16;
@@ -121,12 +122,15 @@ void plan_direction(cgtp_linear &l, Direction &d, const std::vector<Irrep> &ins,
         c.part = part;
         d.in_pitch[part] += c.in;
         d.out_pitch[part] += c.out;
-        if (bytes(d.in_pitch[part], d.out_pitch[part]) > kLds - 8 * 1024)
+        if (bytes(d.in_pitch[part], 0) > kLds - 8 * 1024)
             throw Error(CGTP_ERR_UNSUPPORTED, "linear: 16 rows of one degree and parity need " +
-                                                  std::to_string(bytes(d.in_pitch[part], d.out_pitch[part])) +
+                                                  std::to_string(bytes(d.in_pitch[part], 0)) +
                                                   " bytes of LDS, a workgroup has 155648 for them");
     }
     const int parts = part + 1;
+    std::vector<bool> direct;
+    for (int p = 0; p < parts; ++p)
+        direct.push_back(16 * l.elem * (odd_pitch(d.in_pitch[p], vec) + odd_pitch(d.out_pitch[p], vec)) > 76 * 1024);
     std::vector<int> in_at(parts, 0), out_at(parts, 0);
     std::vector<int> in_lds;
     int at = 0;
@@ -162,7 +166,7 @@ void plan_direction(cgtp_linear &l, Direction &d, const std::vector<Irrep> &ins,
     }
     for (int p = 0; p < parts; ++p) {
         d.in_pitch[p] = odd_pitch(d.in_pitch[p], vec);
-        d.out_pitch[p] = odd_pitch(d.out_pitch[p], vec);
+        d.out_pitch[p] = direct[p] ? 0 : odd_pitch(d.out_pitch[p], vec);
         d.lds_bytes = std::max(d.lds_bytes, 16 * l.elem * (d.in_pitch[p] + d.out_pitch[p]));
     }
     // eight waves where LDS leaves room for one workgroup on a CU, else four
