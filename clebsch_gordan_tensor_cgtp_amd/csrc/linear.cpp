@@ -48,10 +48,10 @@ struct cgtp_linear {
     int d_in = 0, d_out = 0;
     int64_t numel = 0;
     std::vector<LinearPath> paths;
-    Direction fwd, bwd;
+    Direction fwd, bwd, fwd_few, bwd_few;  // and of few rows
     std::vector<Tile> tiles;
     cgtp::ConfigModule mod;
-    enum { forward, backward_x, transpose, backward_w, reduce };
+    enum { forward, backward_x, transpose, backward_w, reduce, forward_few, backward_x_few };
 };
 
 namespace cgtp {
@@ -93,7 +93,7 @@ int odd_pitch(int elements, int vec) { return (round_up(elements, vec) / vec | 1
 // Irreps of one degree and parity belong to one part: no others read what they read.  Parts are filled up to
 // 64 KB of LDS for their rows in and out, so that two workgroups or more share a CU; where one degree's alone take over
 // 76 KB, results do not go through LDS.
-void plan_direction(cgtp_linear &l, Direction &d, const std::vector<Irrep> &ins, const std::vector<Irrep> &outs, bool backward)
+void plan_direction(cgtp_linear &l, Direction &d, const std::vector<Irrep> &ins, const std::vector<Irrep> &outs, bool backward, bool few)
 {
     const int vec = 16 / l.elem, step = l.elem == 2 ? 32 : 16;
     struct Class {
@@ -169,8 +169,11 @@ void plan_direction(cgtp_linear &l, Direction &d, const std::vector<Irrep> &ins,
         d.out_pitch[p] = direct[p] ? 0 : odd_pitch(d.out_pitch[p], vec);
         d.lds_bytes = std::max(d.lds_bytes, 16 * l.elem * (d.in_pitch[p] + d.out_pitch[p]));
     }
-    // eight waves where LDS leaves room for one workgroup on a CU, else four
-    d.waves = d.lds_bytes > kLds / 2 ? 8 : 4;
+    // Four waves; eight where results do not go through LDS, of which parts are wide (20,000 rows of 128x(0e,1o,2e,3o) in
+    // fp32, forward: 300 us with four, 265 us).  For few rows, a workgroup or less to each CU, up to twelve: what
+    // counts then is the way through one tile (21 rows of 64x(0e,1o,2e) in bf16: 10.1 us with four, 8.2 us; 200,000 of
+    // them 181 us, with eight 225 us).
+    d.waves = few ? 12 : std::count(direct.begin(), direct.end(), true) ? 8 : 4;
     int most_units = 1;
     for (int p = 0; p < parts; ++p) {
         // Units: a wave's even share of the part's 16-blocks times components, no more than 20 (10 in double), since
@@ -289,6 +292,8 @@ std::string constants(const cgtp_linear &l)
     t.num("NUMEL", l.numel);
     direction_text(t, "Forward", l.fwd, false);
     direction_text(t, "Backward", l.bwd, l.cfg.top_k > 0);
+    direction_text(t, "ForwardFew", l.fwd_few, false);
+    direction_text(t, "BackwardFew", l.bwd_few, l.cfg.top_k > 0);
     t.num("NPATH", (int64_t)l.paths.size());
     t.list("W_XC", l.paths.size(), [&](size_t i) { return l.paths[i].in_col; });
     t.list("W_MI", l.paths.size(), [&](size_t i) { return l.paths[i].mul_in; });
@@ -308,6 +313,8 @@ std::string constants(const cgtp_linear &l)
     t.num("MAX_STRETCH", kMaxStretch);
     return t.s;
 }
+
+bool few_rows(int64_t N) { return N <= 16 * 256; }
 
 int64_t slots_of(const cgtp_linear &l, int64_t N) { return N * std::max(1, l.cfg.top_k); }
 
@@ -388,12 +395,14 @@ cgtp_status cgtp_linear_create(const char *in_irreps, const char *out_irreps, co
         h->real = real_bytes(c.dtype);
         const std::vector<Irrep> ins = parse_irreps(in_irreps, "input"), outs = parse_irreps(out_irreps, "output");
         find_paths(*h, ins, outs);
-        plan_direction(*h, h->fwd, ins, outs, false);
-        plan_direction(*h, h->bwd, outs, ins, true);
+        plan_direction(*h, h->fwd, ins, outs, false, false);
+        plan_direction(*h, h->bwd, outs, ins, true, false);
+        plan_direction(*h, h->fwd_few, ins, outs, false, true);
+        plan_direction(*h, h->bwd_few, outs, ins, true, true);
         plan_tiles(*h);
         h->mod.build(constants(*h) + kRowKernels + kLinearKernels,
                      {"cgtp_linear_fwd", "cgtp_linear_bwd_x", "cgtp_linear_transpose", "cgtp_linear_bwd_w",
-                      "cgtp_linear_reduce"});
+                      "cgtp_linear_reduce", "cgtp_linear_fwd_few", "cgtp_linear_bwd_x_few"});
         *linear_out = h.release();
     });
 }
@@ -448,7 +457,9 @@ cgtp_status cgtp_linear_forward(const cgtp_linear *linear, int64_t N, const void
         const auto &F = l.mod.here();
         long xl = (long)x_ld, ol = (long)out_ld, n = (long)N;
         void *args[] = {&x, &xl, &w, &experts, &weights, &rows, &n, &out, &ol};
-        run(F[cgtp_linear::forward], (N + 15) / 16, l.fwd.waves * 64, args, stream);
+        const bool few = few_rows(N);
+        run(F[few ? cgtp_linear::forward_few : cgtp_linear::forward], (N + 15) / 16, (few ? l.fwd_few : l.fwd).waves * 64, args,
+            stream);
     });
 }
 
@@ -523,7 +534,9 @@ cgtp_status cgtp_linear_backward(const cgtp_linear *linear, int64_t N, const voi
             void *targs[] = {&w, &turned};
             run2(F[cgtp_linear::transpose], (l.numel + 255) / 256, l.cfg.experts, 256, targs, stream);
             void *args[] = {&grad_out, &gl, &turned, &experts, &weights, &rows, &n, &grad_x, &gxl, &x, &xl, &grad_weights};
-            run(F[cgtp_linear::backward_x], (N + 15) / 16, l.bwd.waves * 64, args, stream);
+            const bool few = few_rows(N);
+            run(F[few ? cgtp_linear::backward_x_few : cgtp_linear::backward_x], (N + 15) / 16,
+                (few ? l.bwd_few : l.bwd).waves * 64, args, stream);
         }
         if (grad_w) {
             void *args[] = {&x, &xl, &grad_out, &gl, &weights, &slots, &offsets, &n, &count, &len, &part};

@@ -5,7 +5,7 @@
 // Constants of a plan, beside T, R and ACT:
 //   E, K          experts; experts of a row (0: the one expert of every row, with weight 1)
 //   NUMEL         weights of an expert
-//   Forward, Backward: the product's two directions, each a struct of
+//   Forward, Backward, and for few rows ForwardFew, BackwardFew: the product's two directions, each a struct of
 //     NPARTS, IN_PITCH, OUT_PITCH, LDS_BYTES  parts, worked on one after the other: pitches of their rows in LDS
 //     NS, S_PART, S_COL, S_LEN, S_LDS, S_PAD  input irreps: part, first column, columns; where they begin in LDS and
 //                                             columns there (whole steps)
@@ -114,7 +114,7 @@ template <int NN, int KC> DEV void step(const T (&a)[NN][KL], const T (&b)[KL * 
 // loads of neighbouring lanes along the rows, and its results leave it the same way.  Operands read straight
 // from memory are runs of 16 (2l+1) bytes per lane, each instruction touching 64 cache lines for 16 bytes each.
 // A part that would leave a CU one workgroup (OUT_PITCH 0) stores its results from registers all the same: two workgroups
-// that overlap are worth more there (20,000 rows of 128x(0e,1o,2e,3o) in fp32, forward: 304 us through LDS, FWDNEW).
+// that overlap are worth more there (20,000 rows of 128x(0e,1o,2e,3o) in fp32, forward: 304 us through LDS, 265 us).
 // In LDS an irrep starts at 16 bytes and is padded with zeros to whole steps; a row's pitch is an odd multiple
 // of 16 bytes, so that the eight lanes of an LDS access (eight nodes) meet different banks.
 constexpr int VEC = 16 / sizeof(T);
@@ -447,22 +447,28 @@ DEV void product(const T *in, long in_ld, const T *w, const int *experts, const 
     }
 }
 
-extern "C" __global__ void __launch_bounds__(Forward::WAVES * 64, 2)
-cgtp_linear_fwd(const T *__restrict__ x, long x_ld, const T *__restrict__ w, const int *__restrict__ experts,
-                const R *__restrict__ weights, const int *__restrict__ order, long N, T *__restrict__ out, long out_ld)
-{
-    product<Forward>(x, x_ld, w, experts, weights, order, N, out, out_ld, nullptr, 0, nullptr);
-}
+#define FORWARD(name, D)                                                                                            \
+    extern "C" __global__ void __launch_bounds__(D::WAVES * 64, 2)                                                  \
+    name(const T *__restrict__ x, long x_ld, const T *__restrict__ w, const int *__restrict__ experts,              \
+         const R *__restrict__ weights, const int *__restrict__ order, long N, T *__restrict__ out, long out_ld)    \
+    {                                                                                                               \
+        product<D>(x, x_ld, w, experts, weights, order, N, out, out_ld, nullptr, 0, nullptr);                       \
+    }
+FORWARD(cgtp_linear_fwd, Forward)
+FORWARD(cgtp_linear_fwd_few, ForwardFew)
 
 // grad_x and the gradient of the weights p: dp[n][j] = <x[n], W^T g[n]>.  w holds the transposed matrices.
-extern "C" __global__ void __launch_bounds__(Backward::WAVES * 64, 2)
-cgtp_linear_bwd_x(const T *__restrict__ g, long g_ld, const T *__restrict__ w, const int *__restrict__ experts,
-                  const R *__restrict__ weights, const int *__restrict__ order, long N, T *__restrict__ grad_x,
-                  long grad_x_ld, const T *__restrict__ x, long x_ld, R *__restrict__ grad_weights)
-{
-    product<Backward>(g, g_ld, w, experts, weights, order, N, grad_x, grad_x_ld, grad_weights ? x : nullptr, x_ld,
-                      grad_weights);
-}
+#define BACKWARD(name, D)                                                                                           \
+    extern "C" __global__ void __launch_bounds__(D::WAVES * 64, 2)                                                  \
+    name(const T *__restrict__ g, long g_ld, const T *__restrict__ w, const int *__restrict__ experts,              \
+         const R *__restrict__ weights, const int *__restrict__ order, long N, T *__restrict__ grad_x,              \
+         long grad_x_ld, const T *__restrict__ x, long x_ld, R *__restrict__ grad_weights)                          \
+    {                                                                                                               \
+        product<D>(g, g_ld, w, experts, weights, order, N, grad_x, grad_x_ld, grad_weights ? x : nullptr, x_ld,     \
+                   grad_weights);                                                                                   \
+    }
+BACKWARD(cgtp_linear_bwd_x, Backward)
+BACKWARD(cgtp_linear_bwd_x_few, BackwardFew)
 
 // every matrix [mul_out][mul_in] transposed, in its place
 extern "C" __global__ void __launch_bounds__(256) cgtp_linear_transpose(const T *__restrict__ w, T *__restrict__ wt)
@@ -691,7 +697,7 @@ cgtp_linear_bwd_w(const T *__restrict__ x, long x_ld, const T *__restrict__ g, l
     __shared__ Table tab;
     __shared__ V16 lds[tile_elements() / VEC];
     // All stretches of the tile that takes longest come first.  With the tiles of a stretch side by side a CU got the same
-    // tile every time (four tiles, 32 CUs to an XCD): 378 us for 20,000 rows of 128x(0e,1o,2e,3o) in fp32, not NEW.
+    // tile every time (four tiles, 32 CUs to an XCD): 378 us for 20,000 rows of 128x(0e,1o,2e,3o) in fp32, this way 230 us.
     const long stretches = gridDim.x / NT, number = blockIdx.x % stretches;
     const int which = (int)(blockIdx.x / stretches);
     const Stretch s = stretch_of(offsets, count, len, number, threadIdx.x & 63);

@@ -148,11 +148,11 @@ def test_linear_layout(a, b, e, k, n, dtype):
         assert wv * wu <= 4 and nodes % 4 == 0
     assert sorted(seen) == list(range(numel))
     # the units of each direction cover every 16-block of every irrep once, in waves that exist
-    for name in ("Forward", "Backward"):
+    for name in ("Forward", "Backward", "ForwardFew", "BackwardFew"):
         d = constants(re.search(r"struct %s \{\n(.*?)\n\};\n" % name, linear.source, re.S).group(1))
         blocks = [(o, i) for o, f, m in zip(d["U_OUT"], d["U_N0"], d["U_NN"]) for i in range(f, f + m)]
         assert sorted(blocks) == [(o, i) for o, mul in enumerate(d["O_MUL"]) for i in range(-(-mul // 16))]
-        assert sorted(set(d["U_WAVE"])) == list(range(d["WAVES"][0])) and d["WAVES"][0] <= 8
+        assert sorted(set(d["U_WAVE"])) == list(range(d["WAVES"][0])) and d["WAVES"][0] <= 12
     assert "atomic" not in linear.source.lower()
 
 
