@@ -33,7 +33,7 @@ struct Direction {
     std::vector<Segment> segments;
     std::vector<int> in_pitch, out_pitch;             // parts, in elements
     std::vector<Unit> units;
-    int waves = 1, lds_bytes = 0;
+    int waves = 1, simd_waves = 2, lds_bytes = 0;
 };
 
 struct Tile {
@@ -174,6 +174,7 @@ void plan_direction(cgtp_linear &l, Direction &d, const std::vector<Irrep> &ins,
     // counts then is the way through one tile (21 rows of 64x(0e,1o,2e) in bf16: 10.1 us with four, 8.2 us; 200,000 of
     // them 181 us, with eight 225 us).
     d.waves = few ? 12 : std::count(direct.begin(), direct.end(), true) ? 8 : 4;
+    if (d.waves == 8) d.simd_waves = 4;  // two such workgroups on a CU (the backward: 352 us with one, 303 us)
     int most_units = 1;
     for (int p = 0; p < parts; ++p) {
         // Units: a wave's even share of the part's 16-blocks times components, no more than 20 (10 in double), since
@@ -244,6 +245,7 @@ void direction_text(Text &t, const char *name, const Direction &d, bool dot)
     const char *st = "    static ";
     t.s += std::string("struct ") + name + " {\n";
     t.num("DOT", dot ? 1 : 0, st);
+    t.num("SIMD_WAVES", d.simd_waves, st);
     t.num("NPARTS", (int64_t)d.in_pitch.size(), st);
     t.num("LDS_BYTES", d.lds_bytes, st);
     t.list("IN_PITCH", d.in_pitch.size(), [&](size_t i) { return d.in_pitch[i]; }, st);

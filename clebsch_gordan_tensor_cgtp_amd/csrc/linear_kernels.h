@@ -15,7 +15,7 @@
 //                                             [O_MUL][P_MUL] (row major) in the expert's weights
 //     NU, U_PART, U_OUT, U_N0, U_NN, U_WAVE, WAVES  units: output irrep, first and number of its blocks of 16
 //                                             channels, the wave that takes it; waves of a workgroup
-//     DOT                                     1: the weights p have a gradient
+//     DOT, SIMD_WAVES                         1: the weights p have a gradient; waves that registers are kept few enough for
 //   NPATH, W_*    for the weight gradients, per path: W_XC, W_MI the input's first column and channels, W_GC, W_MO
 //                 the output's, W_K, W_OFF the first weight
 //   NT, T_PATH, T_V, T_U, T_BV, T_BU          tiles of the gradients: path, first output and input channel, 16-blocks
@@ -274,6 +274,13 @@ template <class D, int U> DEV void unit(const Node &node, const T *w, int lane, 
 #pragma unroll
         for (int m = 0; m < KC; ++m) total[n][m] = (V4)(R)0;
     if constexpr (PN > 0) {
+        // a direct part's x stays in registers from one expert to the next
+        T xr[DIRECT && D::DOT ? NN : 1][4 * KC];
+        if constexpr (DIRECT && D::DOT) {
+#pragma unroll
+            for (int n = 0; n < NN; ++n)
+                load_channels<4, KC, false>(node.x + D::O_COL[O] + (v0 + n * 16) * KC, node.x ? MO - v0 - n * 16 : 0, xr[n]);
+        }
         int last = -1;
         for (;;) {
             int next = BIG;
@@ -318,10 +325,12 @@ template <class D, int U> DEV void unit(const Node &node, const T *w, int lane, 
 #pragma unroll
                 for (int n = 0; n < NN; ++n) {
                     T x[4 * KC];
-                    if (DIRECT)
-                        load_channels<4, KC, false>(node.x + D::O_COL[O] + (v0 + n * 16) * KC, node.x ? MO - v0 - n * 16 : 0, x);
-                    else
+                    if constexpr (DIRECT) {
+#pragma unroll
+                        for (int i = 0; i < 4 * KC; ++i) x[i] = xr[n][i];
+                    } else {
                         read_lds<4 * KC>(out + n * 16 * KC, x);
+                    }
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
 #pragma unroll
@@ -448,7 +457,7 @@ DEV void product(const T *in, long in_ld, const T *w, const int *experts, const 
 }
 
 #define FORWARD(name, D)                                                                                            \
-    extern "C" __global__ void __launch_bounds__(D::WAVES * 64, 2)                                                  \
+    extern "C" __global__ void __launch_bounds__(D::WAVES * 64, D::SIMD_WAVES)                                      \
     name(const T *__restrict__ x, long x_ld, const T *__restrict__ w, const int *__restrict__ experts,              \
          const R *__restrict__ weights, const int *__restrict__ order, long N, T *__restrict__ out, long out_ld)    \
     {                                                                                                               \
@@ -459,7 +468,7 @@ FORWARD(cgtp_linear_fwd_few, ForwardFew)
 
 // grad_x and the gradient of the weights p: dp[n][j] = <x[n], W^T g[n]>.  w holds the transposed matrices.
 #define BACKWARD(name, D)                                                                                           \
-    extern "C" __global__ void __launch_bounds__(D::WAVES * 64, 2)                                                  \
+    extern "C" __global__ void __launch_bounds__(D::WAVES * 64, D::SIMD_WAVES)                                      \
     name(const T *__restrict__ g, long g_ld, const T *__restrict__ w, const int *__restrict__ experts,              \
          const R *__restrict__ weights, const int *__restrict__ order, long N, T *__restrict__ grad_x,              \
          long grad_x_ld, const T *__restrict__ x, long x_ld, R *__restrict__ grad_weights)                          \

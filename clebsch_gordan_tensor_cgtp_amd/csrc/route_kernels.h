@@ -138,11 +138,11 @@ template <typename V> DEV bool take_groups(const Row &row, V (&c)[EPL], const V 
     return close > (V)0 && unsure;
 }
 
-// The PICKS largest c in falling order, of equal ones the lowest expert first: -1 where none is left.
-template <int PICKS, typename V> DEV void pick(const Row &row, V (&c)[EPL], int (&chosen)[PICKS], V (&best)[PICKS])
+// The K largest c in falling order, of equal ones the lowest expert first: -1 where none is left.  They are masked in c.
+template <typename V> DEV void pick(const Row &row, V (&c)[EPL], int (&chosen)[K], V (&best)[K])
 {
 #pragma unroll
-    for (int j = 0; j < PICKS; ++j) {
+    for (int j = 0; j < K; ++j) {
         V most = c[0];
 #pragma unroll
         for (int i = 1; i < EPL; ++i) most = c[i] > most ? c[i] : most;
@@ -204,7 +204,6 @@ DEV void choose(const Row &row, int (&chosen)[K])
 DEV bool choose_fast(const Row &row, int (&chosen)[K])
 {
     constexpr float CLOSE = 4e-6f;
-    constexpr int PICKS = K < E ? K + 1 : K;  // the one after the last shows whether that one is sure
     float x[EPL], c[EPL], s[EPL], most = lowest(0.0f);
     load_share(row.logits, row.sh, lowest(0.0f), x);
     EACH(i) most = x[i] > most ? x[i] : most;
@@ -237,23 +236,22 @@ DEV bool choose_fast(const Row &row, int (&chosen)[K])
     } else {
         EACH(i) sure = sure && (x[i] == lowest(0.0f) || x[i] - x[i] == 0.0f);
     }
-    int picked[PICKS];
-    float best[PICKS];
-    pick(row, c, picked, best);
+    float best[K], rest = lowest(0.0f);
+    pick(row, c, chosen, best);
+    EACH(i) rest = c[i] > rest ? c[i] : rest;
+    rest = lanes_max<L>(rest);  // the best that is left shows whether the last one is sure
 #pragma unroll
-    for (int j = 0; j < K; ++j) chosen[j] = picked[j];
-#pragma unroll
-    for (int j = 0; j < PICKS; ++j) {
+    for (int j = 0; j < K; ++j) {
         if (j % L != row.q) continue;  // a lane looks at some places and the next ones
-        if (picked[j] < 0) continue;
+        if (chosen[j] < 0) continue;
+        const float next = j + 1 < K ? best[j + 1] : rest, gap = best[j] - next;
         if (!row.bias) {
-            const float next = j + 1 < PICKS ? best[j + 1] : best[j], gap = best[j] - next;
             // far below 1 (a sigmoid) or the largest (a softmax) scores may be too small for a double
             sure = sure && (gap == 0.0f || gap > 1e-10f * (1.0f + fabsf(best[j]) + fabsf(most))) &&
                    (SIGMOID ? best[j] : best[j] - most) > -600.0f;
-        } else if (j + 1 < PICKS && picked[j + 1] >= 0 && best[j] - best[j + 1] <= CLOSE * (1.0f + fabsf(best[j]))) {
-            const int e0 = picked[j], e1 = picked[j + 1];
-            sure = sure && row.logits[e0] == row.logits[e1] && row.bias[e0] == row.bias[e1];
+        } else if (gap <= CLOSE * (1.0f + fabsf(best[j]))) {
+            const int e0 = chosen[j], e1 = j + 1 < K ? chosen[j + 1] : -1;
+            sure = sure && e1 >= 0 && row.logits[e0] == row.logits[e1] && row.bias[e0] == row.bias[e1];
         }
     }
     return lanes_min<L>(sure ? 1 : 0) != 0;
