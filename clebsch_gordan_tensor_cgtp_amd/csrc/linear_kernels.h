@@ -706,7 +706,8 @@ cgtp_linear_bwd_w(const T *__restrict__ x, long x_ld, const T *__restrict__ g, l
     __shared__ Table tab;
     __shared__ V16 lds[tile_elements() / VEC];
     // All stretches of the tile that takes longest come first.  With the tiles of a stretch side by side a CU got the same
-    // tile every time (four tiles, 32 CUs to an XCD): 378 us for 20,000 rows of 128x(0e,1o,2e,3o) in fp32, this way 230 us.
+    // tile every time (four tiles, 32 CUs to an XCD): 378 us for 20,000 rows of 128x(0e,1o,2e,3o) in fp32, this way 255 us (its products
+    // alone: 142).
     const long stretches = gridDim.x / NT, number = blockIdx.x % stretches;
     const int which = (int)(blockIdx.x / stretches);
     const Stretch s = stretch_of(offsets, count, len, number, threadIdx.x & 63);
