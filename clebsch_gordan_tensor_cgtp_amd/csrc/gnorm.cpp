@@ -88,7 +88,8 @@ struct Split {
 // waves that a smaller one leaves idle are few; where that is far more than a workgroup's, nearly all are large, and four
 // waves share them out more evenly.  (4,000 graphs of 50 rows on average, 64 channels in bf16.)
 // Chunks: at most 1,024, whose pieces each workgroup of the second launch joins for itself; a backward's
-// workgroups take graphs in turn, since each leaves its partial sums of the weights' gradients.
+// workgroups take graphs in turn, since each leaves its partial sums of the weights' gradients: 1,024 of them, or 8,192 where
+// each would have more than 16.
 Split split(const cgtp_group_norm &g, int64_t N, int64_t S, bool backward)
 {
     Split p{};
@@ -102,7 +103,7 @@ Split split(const cgtp_group_norm &g, int64_t N, int64_t S, bool backward)
     const int64_t step = (int64_t)g.rw * p.waves * (g.ns * g.cv <= 4 ? 4 : 2);
     p.rows = std::max<int64_t>(1, (N + 1024 * step - 1) / (1024 * step)) * step;
     p.chunks = (N + p.rows - 1) / p.rows;
-    p.graphs = backward ? std::min<int64_t>(S, 1024) : S;
+    p.graphs = backward ? std::min<int64_t>(S, S <= 16384 ? 1024 : 8192) : S;
     return p;
 }
 

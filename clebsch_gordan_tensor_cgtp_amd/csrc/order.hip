@@ -34,7 +34,10 @@ constexpr int kNone = -2147483647 - 1;  // no item
 
 __device__ __forceinline__ int key_of(const Items &s, int64_t i)
 {
-    if (s.slots) return s.experts[i];  // checked where it is used, so that its load may be in flight until then
+    if (s.slots) {
+        const int e = s.experts[i];  // checked where it is used, so that its load may be in flight until then
+        return e == kNone ? -1 : e;
+    }
     int a = s.E, b = s.E;
     for (int j0 = 0; j0 < s.K; j0 += 8) {
         int e[8];  // eight loads in flight

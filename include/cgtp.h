@@ -37,7 +37,7 @@
  * never allocates, frees or synchronises device memory; the entry points that
  * need temporary memory (cgtp_tp_backward and cgtp_conv_backward_ws for uvw,
  * cgtp_conv_backward_radial for dTheta, the block backwards' weight gradients,
- * cgtp_grad_norm) take it from the caller.  `stream` is a hipStream_t (NULL = the default
+ * cgtp_grad_norm, the group norm, cgtp_route_order, cgtp_linear_backward) take it from the caller.  `stream` is a hipStream_t (NULL = the default
  * stream); all work is enqueued on it asynchronously.
  * Index arrays are int32 and N, E < 2^31.
  *
@@ -745,7 +745,8 @@ cgtp_status cgtp_route_order(const cgtp_router *router, int64_t N, const int32_t
  * Types: x, w, out and their gradients are of the linear's dtype; weights and their gradient float (double for
  * CGTP_F64), and so are all sums.  In 16 bits the weight gradient takes the products p grad_out rounded to the type.
  * Compiled, loaded and destroyed as a block is (cgtp_block_create).  CGTP_ERR_IRREPS: no equal irreps.
- * CGTP_ERR_UNSUPPORTED: over 512 experts, 32 of a row, 64 pairs, 2^26 weights of an expert, or thousands of channels.
+ * CGTP_ERR_UNSUPPORTED: over 512 experts, 32 of a row, 64 pairs, 2^26 weights of an expert, or so many channels that 16 rows of
+ * one degree and parity exceed 152 KB (about 2,430 columns in fp32, input or output) or give more than 128 units of work.
  */
 typedef struct cgtp_linear cgtp_linear; /* opaque, immutable after creation */
 

@@ -47,7 +47,8 @@ def within(name, got, value, most, dtype=None):
 # many, and these over as many chunks as there are
 NORM_SHAPES = [(1, 1, [3]), (4, 2, [1]), (4, 4, [0, 5, 0, 0, 9, 0]), (32, 4, [21] * 24), (95, 5, [700, 1, 3, 0, 411]),
                (64, 64, [130, 2]), (2048, 4, [9, 30]), (513, 3, [40]), (24, 1, [1, 1, 1, 2]), (130, 13, [900]),
-               (16, 16, [5000, 1, 7000]), (40, 8, [1] * 300 + [9000, 4, 2600, 0] + [7] * 300), (1024, 512, [3000, 20])]
+               (16, 16, [5000, 1, 7000]), (40, 8, [1] * 300 + [9000, 4, 2600, 0] + [7] * 300), (1024, 512, [3000, 20]),
+               (2047, 1, [70, 3])]
 
 
 def norm_inputs(channels, graphs, dtype, seed, outside=(2, 3)):
@@ -101,13 +102,15 @@ def act_error(z, dz, u):
 # ------------------------------------------------------------------------------------ experts' products
 
 # irreps in, out, experts, top_k, rows: one value; every block size around 16; odd ones; an irrep twice on both
-# sides, one without a pair; high degrees; wide blocks in several units; more experts than rows; a plain layer
+# sides, one without a pair; high degrees; wide blocks in several units; more experts than rows; a plain layer; most experts
+# of a row; an irrep that fills LDS
 LINEAR_CASES = [("1x0e", "1x0e", 1, 1, 1), ("4x0e+4x1o", "4x1o+4x0e", 3, 2, 15), ("16x1o", "16x1o", 4, 1, 16),
                 ("17x0e+33x1o+5x2e", "33x0e+15x1o+7x2e", 5, 3, 67), ("8x0e+4x0e+3x1o", "5x0e+6x0e+2x1o+3x2e", 2, 2, 130),
                 ("3x7o+2x4e+40x3o", "2x7o+40x3o+5x4e", 3, 2, 33), ("128x0e+100x2e", "130x0e+65x2e", 6, 2, 50),
                 ("64x0e+64x1o", "64x0e+64x1o", 64, 2, 9), ("48x0e+20x1e", "31x0e+20x1e", 1, 0, 1030),
                 ("32x0e+32x1o+32x2e", "32x0e+32x1o+32x2e", 8, 2, 700), ("5x1e", "3x1e", 9, 8, 40),
-                ("200x0e", "7x0e", 4, 4, 513)]
+                ("200x0e", "7x0e", 4, 4, 513),
+                ("9x0e+3x1o", "3x1o+9x0e", 40, 32, 60), ("390x1o", "40x1o+3x0e", 2, 1, 40)]
 
 
 def linear_inputs(a, b, e, k, n, dtype, seed, free=True):

@@ -170,6 +170,7 @@ def test_linear_creation_refusals():
     assert create(None) == INVAL and create(b=None) == INVAL
     assert L.cgtp_linear_create(b"4x0e", b"4x0e", None, ctypes.byref(h)) == INVAL
     assert create(experts=513) == UNSUP and create(experts=64, top_k=33) == UNSUP
+    assert create(b"600x1o", b"40x1o", dtype=1) == UNSUP and "LDS" in cg.last_error()
     assert create(b"9000x0e", b"9000x0e") == UNSUP and create(b"+".join([b"1x0e"] * 9), b"+".join([b"1x0e"] * 9)) == UNSUP
     assert L.cgtp_linear_destroy(None) == 0
 

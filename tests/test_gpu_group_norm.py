@@ -228,6 +228,16 @@ def test_repeats_streams_and_graphs(device):
         assert all(a.equal(b) for a, b in zip(got, run())), i
 
 
+def test_more_graphs_than_workgroups(device):
+    """Tens of thousands of graphs of a few rows, some empty: the backward's workgroups take several each."""
+    norm = cg.group_norm_for(8, 2, "f32", act="silu", eps=EPS)
+    sizes = list(np.random.default_rng(15).integers(0, 5, 20_000))
+    t = norm_inputs(8, sizes, "f32", 15)
+    fwd, bwd = both(norm, t, device)
+    check_forward(norm, t, fwd, "f32", "silu")
+    check_backward(norm, t, fwd[1], fwd[2], bwd, "f32", "silu")
+
+
 def test_past_2_31_elements(device):
     """Rows past 2^31 elements: the last graph as if it stood alone."""
     import torch

@@ -162,6 +162,8 @@ def test_lists(device, n, k, e):
     experts = np.minimum(rng.integers(0, e, (n, k)), rng.integers(0, e, (n, k))).astype(np.int32)
     experts[rng.random((n, k)) < 0.1] = -1
     experts[rng.random((n, k)) < 0.02] = e + 3
+    experts[rng.random((n, k)) < 0.01] = np.iinfo(np.int32).min
+    experts[rng.random((n, k)) < 0.01] = np.iinfo(np.int32).max
     router = cg.router_for(max(e, k), k, "f32")
     e = router.experts
     got = cg.route_order(router, up(experts, device))
