@@ -152,7 +152,9 @@ template <class D, int O, bool OUT> DEV void copy_rows(T *lds, int pitch, T *row
             if (n < 0) continue;
             typedef T V __attribute__((ext_vector_type(VEC), aligned(sizeof(T))));
             if (LEN % VEC == 0 || e + VEC <= LEN) {
-                *reinterpret_cast<V *>(p) = w;
+                // past the caches, which keep the matrices and the rows instead: 200,000 rows of 64x(0e,1o,2e) in bf16 by one
+                // matrix 123 us, this way 95 us; of 5,000 rows there is no difference
+                __builtin_nontemporal_store((V)w, reinterpret_cast<V *>(p));
             } else {
 #pragma unroll
                 for (int i = 0; i < VEC; ++i)
