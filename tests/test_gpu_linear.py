@@ -259,3 +259,31 @@ def test_a_layer_captured_and_on_another_stream(device):
         graph.replay()
         got = [o.clone() for o in outs]
         assert all(a.equal(b) for a, b in zip(got, step())), i
+
+
+def test_two_captured_layers_replayed_at_once(device):
+    """Two graphs of one configuration, each with its own workspaces, on two streams."""
+    import torch
+    graphs, outs, wants, streams = [], [], [], [torch.cuda.Stream(), torch.cuda.Stream()]
+    layers = [layer(device, "f32", n, seed) for n, seed in ((20000, 1), (9001, 2))]
+
+    def step(p, t):
+        out, kept = layer_forward(p, t)
+        return [out] + list(layer_backward(p, t, kept).values())
+    for p, t in layers:
+        wants.append([v.clone() for v in step(p, t)])
+        torch.cuda.synchronize()
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            outs.append(step(p, t))
+    for _ in range(3):
+        for o in outs:
+            for v in o:
+                v.fill_(float("nan"))
+        torch.cuda.synchronize()
+        for s, g in zip(streams, graphs):
+            with torch.cuda.stream(s):
+                g.replay()
+        torch.cuda.synchronize()
+        for o, w in zip(outs, wants):
+            assert all(a.equal(b) for a, b in zip(o, w))
