@@ -553,6 +553,9 @@ template <int I> struct Shape {
     // a node's row in LDS begins 16 banks after the one before, so that a wave's four nodes meet different ones
     static constexpr int PITCH = ((GP + XP) * (int)sizeof(T) + 255) / 256 * 256 / (int)sizeof(T) + 64 / (int)sizeof(T);
     static constexpr int NODES = T_NODES[I], CG = (GC + VEC - 1) / VEC, CX = (XC + VEC - 1) / VEC;
+    // No run of columns is cut short: every load is made, of row 0 where there is no node, and what it brought is a zero
+    // in LDS.  With a branch around each load 200,000 rows of 64x(0e,1o,2e) in bf16, 2 of 16 experts, took 593 us, this way 347 us.
+    static constexpr bool WHOLE = GC % VEC == 0 && XC % VEC == 0;
     static constexpr int UNITS = NODES / OCTET * (CG + CX), ROUNDS = (UNITS + 255) / 256;
 };
 
@@ -573,7 +576,10 @@ template <int I> DEV void fetch(const T *x, long x_ld, const T *g, long g_ld, co
             const int node = first + at / (S::CG + S::CX) * OCTET + o;
             const int row = at < S::UNITS && node < count ? tab.row[node] : -1;
             T q[VEC];
-            load_channels<VEC, 1, false>(base + (row < 0 ? 0 : row) * ld, row < 0 ? 0 : left, q);
+            if constexpr (S::WHOLE)
+                load_raw<VEC>(base + (row < 0 ? 0 : row) * ld, q);
+            else
+                load_channels<VEC, 1, false>(base + (row < 0 ? 0 : row) * ld, row < 0 ? 0 : left, q);
 #pragma unroll
             for (int i = 0; i < VEC; ++i) v[r][o][i] = q[i];
         }
@@ -592,8 +598,12 @@ template <int I> DEV void keep(T *lds, const Table &tab, int first, int count, c
 #pragma unroll
         for (int o = 0; o < OCTET; ++o) {
             q[o] = v[r][o];
+            const bool in = first + node + o < count && (!S::WHOLE || tab.row[first + node + o] >= 0);
+            if (S::WHOLE && !(K > 0 && out)) {
+#pragma unroll
+                for (int i = 0; i < VEC; ++i) q[o][i] = in ? q[o][i] : (T)0;
+            }
             if (K > 0 && out) {
-                const bool in = first + node + o < count;
                 const R p = in ? tab.p[first + node + o] : (R)0;
 #pragma unroll
                 for (int i = 0; i < VEC; ++i) q[o][i] = in ? (T)((R)v[r][o][i] * p) : (T)0;
