@@ -127,7 +127,11 @@ template <class D, int S> DEV void copy_in(T *lds, int pitch, const T *in, long 
     for (int at = threadIdx.x; at < TOTAL; at += THREADS) {
         const int r = at / CHUNKS, e = at % CHUNKS * VEC, n = node[r];
         T v[VEC];
-        load_channels<VEC, 1, false>(in + (n < 0 ? 0 : n) * ld + D::S_COL[S] + e, n < 0 ? 0 : LEN - e, v);
+        // whole runs are loaded without a branch: a node that is none takes row 0, and its results are not stored
+        if constexpr (LEN % VEC == 0 && LEN == D::S_PAD[S])
+            load_raw<VEC>(in + (n < 0 ? 0 : n) * ld + D::S_COL[S] + e, v);
+        else
+            load_channels<VEC, 1, false>(in + (n < 0 ? 0 : n) * ld + D::S_COL[S] + e, n < 0 ? 0 : LEN - e, v);
         V16 q;
 #pragma unroll
         for (int i = 0; i < VEC; ++i) q[i] = v[i];
@@ -161,7 +165,10 @@ template <class D, int O, bool OUT> DEV void copy_rows(T *lds, int pitch, T *row
                     if (e + i < LEN) p[i] = v[i];
             }
         } else {
-            load_channels<VEC, 1, false>(p, n < 0 ? 0 : LEN - e, v);
+            if constexpr (LEN % VEC == 0)
+                load_raw<VEC>(p, v);
+            else
+                load_channels<VEC, 1, false>(p, n < 0 ? 0 : LEN - e, v);
             V16 w;
 #pragma unroll
             for (int i = 0; i < VEC; ++i) w[i] = v[i];
