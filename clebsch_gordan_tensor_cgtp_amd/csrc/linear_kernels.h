@@ -157,7 +157,7 @@ template <class D, int O, bool OUT> DEV void copy_rows(T *lds, int pitch, T *row
             typedef T V __attribute__((ext_vector_type(VEC), aligned(sizeof(T))));
             if (LEN % VEC == 0 || e + VEC <= LEN) {
                 // past the caches, which keep the matrices and the rows instead: 200,000 rows of 64x(0e,1o,2e) in bf16 by one
-                // matrix 123 us, this way 95 us; of 5,000 rows there is no difference
+                // matrix 123 us, this way 95 us (93 us now); of 5,000 rows there is no difference
                 __builtin_nontemporal_store((V)w, reinterpret_cast<V *>(p));
             } else {
 #pragma unroll
@@ -725,7 +725,7 @@ cgtp_linear_bwd_w(const T *__restrict__ x, long x_ld, const T *__restrict__ g, l
     __shared__ Table tab;
     __shared__ V16 lds[tile_elements() / VEC];
     // All stretches of the tile that takes longest come first.  With the tiles of a stretch side by side a CU got the same
-    // tile every time (four tiles, 32 CUs to an XCD): 378 us for 20,000 rows of 128x(0e,1o,2e,3o) in fp32, this way 255 us (its products
+    // tile every time (four tiles, 32 CUs to an XCD): 378 us for 20,000 rows of 128x(0e,1o,2e,3o) in fp32, this way 255 us, now 229 us (its products
     // alone: 142).
     const long stretches = gridDim.x / NT, number = blockIdx.x % stretches;
     const int which = (int)(blockIdx.x / stretches);
